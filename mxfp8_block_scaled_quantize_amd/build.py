@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmxfp8.so")
 CALIB_PATH = os.path.join(HERE, "libmxfp8_calib.so")
-SOURCES = ["api.hip", "quantize.hip", "pack_scales.hip", "gemm.hip"]
+SOURCES = ["api.hip", "quantize.hip", "pack_scales.hip", "gemm.hip", "api_mx4.hip", "mx4_quantize.hip", "mx4_gemm.hip",
+           "moe.hip"]
 CALIB_SOURCES = ["calib.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

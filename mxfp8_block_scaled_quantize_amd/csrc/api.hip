@@ -128,6 +128,10 @@ mxfp8_status gemm_entry(const uint8_t* a, const uint32_t* a_packed, const uint8_
 
 }  // namespace
 
+namespace mx {
+void note_hip_error(hipError_t e) { g_last_hip_error = static_cast<int>(e); }
+}  // namespace mx
+
 extern "C" {
 
 const char* mxfp8_status_string(mxfp8_status s) {

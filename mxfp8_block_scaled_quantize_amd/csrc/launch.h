@@ -63,4 +63,49 @@ hipError_t launch_gemm(const uint8_t* a, const uint32_t* ap, const uint8_t* b, c
                        MxOut mxo, hipStream_t stream);
 bool gemm_grid_fits(int64_t M, int64_t N, int32_t G, bool grouped, bool swiglu);
 
+// Remembers `e` for mxfp8_last_hip_error on this thread.
+void note_hip_error(hipError_t e);
+
+// ---- MXFP4 (sizes as checked by the C ABI of include/mxfp4.h)
+bool mx4_quantize_grid_fits(int64_t R, int64_t C);
+hipError_t launch_mx4_quantize(const uint16_t* x, int64_t x_rows, int64_t R, int64_t C, int64_t ldx, const int32_t* index,
+                               bool row, bool col, bool packed, uint8_t* q_row, void* s_row, uint8_t* q_colT, void* s_colT,
+                               hipStream_t stream);
+hipError_t launch_mx4_dequantize(const uint8_t* q, const void* s, int64_t R, int64_t C, bool packed, uint16_t* out,
+                                 int64_t ldo, hipStream_t stream);
+
+// offsets == nullptr: dense (G = 0).  epilogue 0 none, 1 accumulate, 2 SwiGLU (B holds 2N rows).
+struct Mx4Gemm {
+  const uint8_t* a;
+  const uint32_t* ap;
+  const uint8_t* b;
+  const uint32_t* bp;
+  uint16_t* c;
+  int64_t ldc, M, N, K;
+  const int32_t* offsets;
+  int32_t G;
+  int epilogue;
+};
+bool mx4_gemm_grid_fits(const Mx4Gemm& g);
+hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream);
+
+// ---- mixture of experts (sizes as checked by the C ABI of include/moe.h)
+bool moe_route_grid_fits(int64_t T);
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int32_t K,
+                            int32_t groups, int32_t top_groups, int32_t group_top, bool sigmoid, bool renorm, float* weights,
+                            int32_t* ids, hipStream_t stream);
+hipError_t launch_moe_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                                     const float* dw, int32_t K, bool sigmoid, bool renorm, void* dlogits,
+                                     hipStream_t stream);
+size_t moe_dispatch_workspace(int64_t n, int64_t E);
+hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t top_k, int32_t* offsets, int32_t* token,
+                               int32_t* position, int32_t* ws, hipStream_t stream);
+bool moe_combine_grid_fits(const void* y, int dtype, int64_t ldy, int64_t T, int64_t H, const void* out);
+hipError_t launch_moe_combine(const void* y, int dtype, int64_t rows, int64_t ldy, const int32_t* pos, const float* w,
+                              int64_t T, int K, int64_t H, void* out, hipStream_t stream);
+bool moe_combine_backward_grid_fits(int64_t T, int64_t K, int64_t rows);
+hipError_t launch_moe_combine_backward(const void* y, int dtype, int64_t rows, int64_t ldy, const int32_t* pos,
+                                       const float* w, int64_t T, int K, int64_t H, const void* dout, int64_t ldd, void* dy,
+                                       float* dw, int32_t* count, hipStream_t stream);
+
 }  // namespace mx

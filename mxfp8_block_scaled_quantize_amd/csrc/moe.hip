@@ -1,0 +1,1008 @@
+// Mixture-of-experts kernels for gfx950: routing and its gradient, the stable
+// counting sort of the (token, slot) pairs, the weighted combination of the
+// experts' outputs and its gradients.
+#include <type_traits>
+
+#include "mx_device.h"
+#include "launch.h"
+
+namespace mx {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// ------------------------------------------------------------ element types
+struct Fp32 {
+  typedef float T;
+  static constexpr int V = 4;   // elements in 16 bytes
+};
+struct Bf16 {
+  typedef uint16_t T;
+  static constexpr int V = 8;
+};
+struct Fp16 {
+  typedef uint16_t T;
+  static constexpr int V = 8;
+};
+
+template <typename D>
+__device__ __forceinline__ float to_f32(typename D::T v) {
+  if constexpr (__is_same(D, Fp32)) return v;
+  else if constexpr (__is_same(D, Bf16)) return __uint_as_float((uint32_t)v << 16);
+  else return (float)__builtin_bit_cast(_Float16, v);
+}
+template <typename D>
+__device__ __forceinline__ typename D::T from_f32(float v) {
+  if constexpr (__is_same(D, Fp32)) return v;
+  else if constexpr (__is_same(D, Bf16)) return __builtin_bit_cast(uint16_t, (__bf16)v);
+  else return __builtin_bit_cast(uint16_t, (_Float16)v);
+}
+// 16 bytes <-> V floats
+template <typename D>
+__device__ __forceinline__ void unpack(u32x4 d, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (__is_same(D, Fp32)) f[i] = __uint_as_float(d[i]);
+    else if constexpr (__is_same(D, Bf16)) { f[2 * i] = bf_lo(d[i]); f[2 * i + 1] = bf_hi(d[i]); }
+    else {
+      const f16x2 h = __builtin_bit_cast(f16x2, (uint32_t)d[i]);
+      f[2 * i] = (float)h.x;
+      f[2 * i + 1] = (float)h.y;
+    }
+  }
+}
+template <typename D>
+__device__ __forceinline__ u32x4 pack(const float* f) {
+  u32x4 d;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (__is_same(D, Fp32)) d[i] = __float_as_uint(f[i]);
+    else if constexpr (__is_same(D, Bf16)) {
+      const bf16x2 h = {(__bf16)f[2 * i], (__bf16)f[2 * i + 1]};
+      d[i] = __builtin_bit_cast(uint32_t, h);
+    } else {
+      const f16x2 h = {(_Float16)f[2 * i], (_Float16)f[2 * i + 1]};
+      d[i] = __builtin_bit_cast(uint32_t, h);
+    }
+  }
+  return d;
+}
+
+// ------------------------------------------------- reductions over lane rows
+// Over the aligned runs of L lanes (16, 32 or 64); every lane gets the result.
+// Inside 16 lanes by DPP (lane ^ 1, lane ^ 2, mirrored halves, mirrored row),
+// then by the row swaps v_permlane16_swap / v_permlane32_swap.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp32(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+template <typename X, int CTRL>
+__device__ __forceinline__ X dppx(X v) {
+  if constexpr (sizeof(X) == 4) return __builtin_bit_cast(X, dpp32<CTRL>(__builtin_bit_cast(uint32_t, v)));
+  else {
+    const u32x2 d = __builtin_bit_cast(u32x2, v);
+    const u32x2 r = {dpp32<CTRL>(d.x), dpp32<CTRL>(d.y)};
+    return __builtin_bit_cast(X, r);
+  }
+}
+template <int L, typename X, typename Op>
+__device__ __forceinline__ X lanes_reduce(X v, Op op) {
+  v = op(v, dppx<X, 0xB1>(v));
+  v = op(v, dppx<X, 0x4E>(v));
+  v = op(v, dppx<X, 0x141>(v));
+  v = op(v, dppx<X, 0x140>(v));
+  if constexpr (L >= 32) {
+    X a, b;
+    if constexpr (sizeof(X) == 4) {
+      const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                      false, false);
+      a = __builtin_bit_cast(X, (uint32_t)r[0]);
+      b = __builtin_bit_cast(X, (uint32_t)r[1]);
+    } else {
+      const u32x2 d = __builtin_bit_cast(u32x2, v);
+      const auto r = __builtin_amdgcn_permlane16_swap(d.x, d.x, false, false);
+      const auto s = __builtin_amdgcn_permlane16_swap(d.y, d.y, false, false);
+      const u32x2 p = {r[0], s[0]}, q = {r[1], s[1]};
+      a = __builtin_bit_cast(X, p);
+      b = __builtin_bit_cast(X, q);
+    }
+    v = op(a, b);
+  }
+  if constexpr (L >= 64) {
+    X a, b;
+    if constexpr (sizeof(X) == 4) {
+      const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                      false, false);
+      a = __builtin_bit_cast(X, (uint32_t)r[0]);
+      b = __builtin_bit_cast(X, (uint32_t)r[1]);
+    } else {
+      const u32x2 d = __builtin_bit_cast(u32x2, v);
+      const auto r = __builtin_amdgcn_permlane32_swap(d.x, d.x, false, false);
+      const auto s = __builtin_amdgcn_permlane32_swap(d.y, d.y, false, false);
+      const u32x2 p = {r[0], s[0]}, q = {r[1], s[1]};
+      a = __builtin_bit_cast(X, p);
+      b = __builtin_bit_cast(X, q);
+    }
+    v = op(a, b);
+  }
+  return v;
+}
+struct OpMax {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return a > b ? a : b; }
+};
+struct OpMin {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return a < b ? a : b; }
+};
+struct OpAdd {
+  template <typename X>
+  __device__ __forceinline__ X operator()(X a, X b) const { return a + b; }
+};
+
+// LDS written by some lanes of a wave and read by others of the same wave.
+__device__ __forceinline__ void wave_lds_fence() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// -------------------------------------------------------------------- scores
+// exp in 32 bits with the product x log2(e) kept in two parts, so that the
+// result is within about 2 ulp (the plain exp2(x log2 e) loses |x| / 2 ulp).
+__device__ __forceinline__ float exp_of(float x) {
+  const float h = x * 1.44269504088896341f;
+  const float l = fmaf(x, 1.92596299e-08f, fmaf(x, 1.44269504088896341f, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  // h of +-inf (or beyond the range) leaves l undefined: the result is e itself
+  return fabsf(h) < 150.0f ? fmaf(e * l, 0.69314718055994531f, e) : e;
+}
+__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float rcp_of(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double rcp_of(double x) { return 1.0 / x; }
+
+// Order-preserving integers: NaN 2, -inf and up above it, +-0 the same; 1 is
+// left for experts of closed groups and 0 for those that are out.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  const uint32_t k = b ^ (((int32_t)b >> 31) | 0x80000000u);
+  return x != x ? 2u : k;
+}
+__device__ __forceinline__ uint64_t key_of(double x) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, x + 0.0);
+  const uint64_t k = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+  return x != x ? 2ull : k;
+}
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ double value_of(uint64_t k) {
+  return __builtin_bit_cast(double, k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull));
+}
+
+template <int VPL, typename D>
+__device__ __forceinline__ void load_logits(const typename D::T* __restrict__ row, int e0, int E, bool wide, float* x) {
+  constexpr int V = D::V;
+  if (wide && e0 + VPL <= E) {   // rows and lanes start at whole vectors of min(VPL, V) elements
+    if constexpr (VPL % V == 0) {
+#pragma unroll
+      for (int j = 0; j < VPL / V; j++) unpack<D>(*reinterpret_cast<const u32x4*>(row + e0 + V * j), x + V * j);
+    } else {   // VPL = 4 or 12 two-byte elements
+#pragma unroll
+      for (int j = 0; j < VPL / 4; j++) {
+        const u32x2 d = *reinterpret_cast<const u32x2*>(row + e0 + 4 * j);
+        const u32x4 p = {d.x, d.y, 0u, 0u};
+        float f[8];
+        unpack<D>(p, f);
+#pragma unroll
+        for (int i = 0; i < 4; i++) x[4 * j + i] = f[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; j++) x[j] = e0 + j < E ? to_f32<D>(row[e0 + j]) : -INFINITY;
+  }
+}
+
+// Scores in F of the lane's experts (those past E: 0).
+template <int LPR, int VPL, typename F>
+__device__ __forceinline__ void scores_of(const float* x, bool sigmoid, F* s) {
+  if (sigmoid) {
+#pragma unroll
+    for (int j = 0; j < VPL; j++) s[j] = rcp_of((F)1 + exp_of(-(F)x[j]));
+    return;
+  }
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
+  m = lanes_reduce<LPR>(m, OpMax{});
+  if (m == -INFINITY) m = 0.0f;   // a row of -inf alone: every exp is 0
+  F sum = 0;
+#pragma unroll
+  for (int j = 0; j < VPL; j++) {
+    s[j] = exp_of((F)x[j] - (F)m);
+    sum += s[j];
+  }
+  sum = lanes_reduce<LPR>(sum, OpAdd{});
+  const F r = sum == (F)0 ? (F)0 : rcp_of(sum);
+#pragma unroll
+  for (int j = 0; j < VPL; j++) s[j] *= r;
+}
+
+constexpr int kMaxGroups = 64;
+
+struct RouteArgs {
+  int E, K, groups, top_groups, group_top, per;
+  bool sigmoid, renorm, wide;
+  const float* bias;
+};
+
+// Two values whose 32-bit evaluation may be in the wrong order: their distance
+// is within the error of both.  A score's is below 1e-6 (scores are at most 1),
+// the bias adds half an ulp.
+__device__ __forceinline__ bool close_f32(float a, float b) { return a - b <= 4e-6f * (1.0f + fabsf(a)); }
+
+// One row on LPR lanes, lane l holding experts l VPL .. + VPL - 1.  Returns
+// whether (in F = float) the order of two choices that matter is in doubt.
+// SURE: the order is the logits' own, so nothing is in doubt.
+template <int LPR, int VPL, bool SURE, typename F>
+__device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, int l, char* lds, float* __restrict__ w_out,
+                                          int32_t* __restrict__ id_out, bool live) {
+  typedef typename std::conditional<sizeof(F) == 8 && !SURE, uint64_t, uint32_t>::type Key;
+  F* const vals = reinterpret_cast<F*>(lds);                                   // [LPR * VPL]
+  F* const gval = vals + LPR * VPL;                                            // [64]
+  uint32_t* const keep = reinterpret_cast<uint32_t*>(gval + kMaxGroups);       // [64]
+  F* const picked = vals;                                                      // [64], after the groups are done
+  int32_t* const picked_id = reinterpret_cast<int32_t*>(keep);
+  const int e0 = l * VPL;
+  bool doubt = false;
+  F s[VPL];
+  scores_of<LPR, VPL, F>(x, a.sigmoid, s);
+  Key key[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; j++) {
+    if (e0 + j >= a.E) key[j] = 0;
+    else if (SURE || !a.bias) key[j] = key_of(x[j]);
+    else if constexpr (!SURE) key[j] = key_of((F)(s[j] + (F)a.bias[e0 + j]));
+  }
+  if (a.groups > 1) {
+    // the value of a group comes from the choices; with group_top 1 and no
+    // bias the largest logit says the same
+#pragma unroll
+    for (int j = 0; j < VPL; j++)
+      if (e0 + j < a.E) vals[e0 + j] = SURE ? (F)x[j] : a.bias ? (F)(s[j] + (F)a.bias[e0 + j]) : s[j];
+    wave_lds_fence();
+    int lg = 1;   // lanes per group
+    while (2 * lg * a.groups <= LPR) lg *= 2;
+    for (int g0 = 0; g0 < a.groups; g0 += LPR / lg) {
+      const int g = g0 + l / lg;
+      F m1 = -INFINITY, m2 = -INFINITY;
+      if (g < a.groups)
+        for (int i = l % lg; i < a.per; i += lg) {
+          const F v = vals[g * a.per + i];
+          if (v > m1) { m2 = m1; m1 = v; }
+          else if (v > m2) m2 = v;
+        }
+      for (int d = 1; d < lg; d *= 2) {
+        const F o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
+        const F lo = m1 < o1 ? m1 : o1, hi2 = m2 > o2 ? m2 : o2;
+        m1 = m1 > o1 ? m1 : o1;
+        m2 = lo > hi2 ? lo : hi2;
+      }
+      if (g < a.groups && l % lg == 0) gval[g] = a.group_top == 2 && a.per > 1 ? m1 + m2 : m1;
+    }
+    wave_lds_fence();
+    F low = INFINITY, high = -INFINITY;   // smallest open, largest closed
+    for (int g = l; g < a.groups; g += LPR) {
+      const F v = gval[g];
+      int rank = 0;
+      for (int h = 0; h < a.groups; h++) {
+        const F o = gval[h];
+        rank += o > v || (o == v && h < g);
+      }
+      keep[g] = rank < a.top_groups;
+      if (rank < a.top_groups) low = low < v ? low : v;
+      else high = high > v ? high : v;
+    }
+    wave_lds_fence();
+    if (!SURE && sizeof(F) == 4 && a.top_groups < a.groups) {
+      low = lanes_reduce<LPR>(low, OpMin{});
+      high = lanes_reduce<LPR>(high, OpMax{});
+      doubt = close_f32((float)low, (float)high);
+    }
+    int g = e0 / a.per, next = (g + 1) * a.per;
+    uint32_t open = g < a.groups ? keep[g] : 0;
+#pragma unroll
+    for (int j = 0; j < VPL; j++) {
+      if (e0 + j == next) {
+        g++;
+        next += a.per;
+        open = g < a.groups ? keep[g] : 0;
+      }
+      if (!open && e0 + j < a.E) key[j] = 1;
+    }
+    wave_lds_fence();
+  }
+  // top_k rounds of the largest key, ties to the lowest lane and then the
+  // lowest register, i.e. the lowest expert; one more round says how far the
+  // first one left out is.
+  const bool check = !SURE && sizeof(F) == 4 && a.bias;
+  const int rounds = check && a.K < a.E ? a.K + 1 : a.K;
+  const int seg = (threadIdx.x & 63) & ~(LPR - 1);
+  F before = INFINITY;
+  for (int k = 0; k < rounds; k++) {
+    Key lm = key[0];
+#pragma unroll
+    for (int j = 1; j < VPL; j++) lm = key[j] > lm ? key[j] : lm;
+    const Key m = lanes_reduce<LPR>(lm, OpMax{});
+    uint64_t who = __ballot(lm == m) >> seg;
+    if (LPR < 64) who &= ((uint64_t)1 << (LPR & 63)) - 1;
+    if constexpr (!SURE) {
+      if (check) {
+        const F v = value_of(m);
+        if (k > 0 && m > 2) doubt = doubt || close_f32((float)before, (float)v);
+        before = v;
+      }
+    }
+    if (k < a.K && l == (int)__builtin_ctzll(who)) {
+      int at = 0;
+      F sv = 0;
+#pragma unroll
+      for (int j = VPL - 1; j >= 0; j--)
+        if (key[j] == m) {
+          at = j;
+          sv = s[j];
+        }
+#pragma unroll
+      for (int j = 0; j < VPL; j++)
+        if (j == at) key[j] = 0;
+      picked[k] = sv;
+      picked_id[k] = e0 + at;
+    }
+  }
+  wave_lds_fence();
+  F total = 0;
+  for (int k = l; k < a.K; k += LPR) total += picked[k];
+  total = lanes_reduce<LPR>(total, OpAdd{});
+  const F r = a.renorm ? (F)1 / (total + (F)1e-20) : (F)1;
+  if (live)
+    for (int k = l; k < a.K; k += LPR) {
+      w_out[k] = (float)(picked[k] * r);
+      id_out[k] = picked_id[k];
+    }
+  wave_lds_fence();
+  return doubt;
+}
+
+// A wave holds 64 / LPR rows.  The choice is made in 32 bits; a wave in which
+// the order of two values is within the rounding (about one row in a thousand
+// with a bias) makes it again in 64.
+template <typename D, int LPR, int VPL, bool SURE>
+__global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __restrict__ logits, int64_t T, int64_t ld,
+                                                        RouteArgs a, float* __restrict__ weights,
+                                                        int32_t* __restrict__ ids) {
+  constexpr int ROWS = 256 / LPR;
+  typedef typename std::conditional<SURE, float, double>::type Wide;
+  constexpr int NEED = LPR * VPL > 64 ? LPR * VPL : 64;
+  __shared__ __attribute__((aligned(16))) char lds[ROWS][(NEED + kMaxGroups) * sizeof(Wide) + kMaxGroups * 4];
+  const int l = threadIdx.x & (LPR - 1);
+  const int sub = threadIdx.x / LPR;
+  const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+  const bool live = t < T;   // rows past the end repeat the last one and write nothing
+  const int64_t tr = live ? t : T - 1;
+  float x[VPL];
+  load_logits<VPL, D>(logits + tr * ld, l * VPL, a.E, a.wide, x);
+  const bool doubt = route_row<LPR, VPL, SURE, float>(a, x, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+  if constexpr (!SURE) {
+    if (__any(doubt))
+      route_row<LPR, VPL, SURE, double>(a, x, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+  }
+}
+
+// d logits of a row: with g' = dw of the chosen experts (renormalized weights:
+// (g - <g, w>) / total), softmax d_j = s_j (g'_j - <g', s>), sigmoid
+// d_j = g'_j s_j (1 - s_j) with s (1 - s) = e / (1 + e)^2, e = exp(-|x|).
+template <typename D, int LPR, int VPL>
+__global__ __launch_bounds__(256) void moe_route_backward_kernel(const typename D::T* __restrict__ logits, int64_t T,
+                                                                 int64_t ld, RouteArgs a,
+                                                                 const int32_t* __restrict__ ids,
+                                                                 const float* __restrict__ dw,
+                                                                 typename D::T* __restrict__ out, bool wide_out) {
+  constexpr int ROWS = 256 / LPR;
+  __shared__ __attribute__((aligned(16))) uint16_t slot_of[ROWS][LPR * VPL];
+  const int l = threadIdx.x & (LPR - 1);
+  const int sub = threadIdx.x / LPR;
+  const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+  const bool live = t < T;
+  const int64_t tr = live ? t : T - 1;
+  const int e0 = l * VPL;
+  float x[VPL];
+  load_logits<VPL, D>(logits + tr * ld, e0, a.E, a.wide, x);
+  uint16_t* slot = slot_of[sub];
+#pragma unroll
+  for (int j = 0; j < VPL; j++) slot[e0 + j] = 0;
+  wave_lds_fence();
+  for (int k = l; k < a.K; k += LPR) {
+    const int e = ids[tr * a.K + k];
+    if (e >= 0 && e < a.E) slot[e] = (uint16_t)(k + 1);
+  }
+  wave_lds_fence();
+  float s[VPL], g[VPL];
+  scores_of<LPR, VPL, float>(x, a.sigmoid, s);
+  uint32_t chosen = 0;
+  float total = 0.0f, gs = 0.0f;
+#pragma unroll
+  for (int j = 0; j < VPL; j++) {
+    const int k = slot[e0 + j];
+    g[j] = k ? dw[tr * a.K + k - 1] : 0.0f;
+    if (k) {
+      chosen |= 1u << j;
+      total += s[j];
+      gs += g[j] * s[j];
+    }
+  }
+  float dot = lanes_reduce<LPR>(gs, OpAdd{});
+  if (a.renorm) {
+    total = lanes_reduce<LPR>(total, OpAdd{}) + 1e-20f;
+    const float r = 1.0f / total;
+    const float gw = dot * r;
+    gs = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPL; j++)
+      if ((chosen >> j) & 1) {
+        g[j] = (g[j] - gw) * r;
+        gs += g[j] * s[j];
+      }
+    if (!a.sigmoid) dot = lanes_reduce<LPR>(gs, OpAdd{});
+  }
+#pragma unroll
+  for (int j = 0; j < VPL; j++) {
+    if (a.sigmoid) {
+      const float e = exp_of(-fabsf(x[j]));
+      const float q = rcp_of(1.0f + e);
+      g[j] = ((chosen >> j) & 1) ? g[j] * (e * q * q) : 0.0f;
+    } else {
+      g[j] = s[j] * (g[j] - dot);
+    }
+  }
+  if (!live) return;
+  typename D::T* row = out + tr * a.E;
+  constexpr int V = D::V;
+  if (wide_out && e0 + VPL <= a.E) {
+    if constexpr (VPL % V == 0) {
+#pragma unroll
+      for (int j = 0; j < VPL / V; j++) *reinterpret_cast<u32x4*>(row + e0 + V * j) = pack<D>(g + V * j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VPL / 4; j++) {
+        const float f[8] = {g[4 * j], g[4 * j + 1], g[4 * j + 2], g[4 * j + 3], 0.f, 0.f, 0.f, 0.f};
+        const u32x4 d = pack<D>(f);
+        *reinterpret_cast<u32x2*>(row + e0 + 4 * j) = u32x2{d.x, d.y};
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPL; j++)
+      if (e0 + j < a.E) row[e0 + j] = from_f32<D>(g[j]);
+  }
+}
+
+// Lanes per row and experts per lane: the fewest lanes whose registers hold
+// the row (fewer lanes: more rows share a wave's selection rounds).
+#define MOE_ROUTE_SHAPE(CALL)            \
+  do {                                   \
+    if (a.E <= 64) CALL(16, 4);          \
+    else if (a.E <= 128) CALL(16, 8);    \
+    else if (a.E <= 256) CALL(32, 8);    \
+    else if (a.E <= 384) CALL(32, 12);   \
+    else CALL(64, 16);                   \
+  } while (0)
+
+static RouteArgs route_args(int64_t E, int32_t K, int32_t groups, int32_t top_groups, int32_t group_top, bool sigmoid,
+                            bool renorm, const float* bias) {
+  RouteArgs a;
+  a.E = (int)E;
+  a.K = K;
+  a.groups = top_groups == groups ? 1 : groups;   // every group open: no groups
+  a.top_groups = top_groups;
+  a.group_top = group_top;
+  a.per = (int)(E / groups);
+  a.sigmoid = sigmoid;
+  a.renorm = renorm;
+  a.wide = false;
+  a.bias = bias;
+  return a;
+}
+
+// Whether rows of stride ld and lanes of any VPL (a multiple of 4) can be read
+// in whole vectors: 16 bytes, or the 8 of four two-byte elements.
+static bool wide_rows(const void* p, int64_t ld, int esize, int64_t E) {
+  const int unit = (E > 64 && E <= 256) || E > 384 || esize == 4 ? 16 : 8;
+  return reinterpret_cast<uintptr_t>(p) % unit == 0 && (ld * esize) % unit == 0;
+}
+
+template <typename D>
+static hipError_t route_t(const void* logits, int64_t T, int64_t ld, RouteArgs a, float* weights, int32_t* ids,
+                          hipStream_t stream) {
+  const auto* x = static_cast<const typename D::T*>(logits);
+  a.wide = wide_rows(logits, ld, sizeof(typename D::T), a.E);
+  const bool sure = !a.bias && (a.groups == 1 || a.group_top == 1 || a.per == 1);
+#define MOE_CALL(L, V)                                                                                               \
+  do {                                                                                                               \
+    const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));                                                 \
+    if (sure)                                                                                                        \
+      hipLaunchKernelGGL((moe_route_kernel<D, L, V, true>), dim3(grid), dim3(256), 0, stream, x, T, ld, a, weights, ids); \
+    else                                                                                                             \
+      hipLaunchKernelGGL((moe_route_kernel<D, L, V, false>), dim3(grid), dim3(256), 0, stream, x, T, ld, a, weights, ids); \
+  } while (0)
+  MOE_ROUTE_SHAPE(MOE_CALL);
+#undef MOE_CALL
+  return hipGetLastError();
+}
+
+template <typename D>
+static hipError_t route_back_t(const void* logits, int64_t T, int64_t ld, RouteArgs a, const int32_t* ids,
+                               const float* dw, void* dlogits, hipStream_t stream) {
+  const auto* x = static_cast<const typename D::T*>(logits);
+  auto* o = static_cast<typename D::T*>(dlogits);
+  a.wide = wide_rows(logits, ld, sizeof(typename D::T), a.E);
+  const bool wide_out = wide_rows(dlogits, a.E, sizeof(typename D::T), a.E);
+#define MOE_CALL(L, V)                                                                                             \
+  hipLaunchKernelGGL((moe_route_backward_kernel<D, L, V>), dim3((unsigned)((T + 256 / L - 1) / (256 / L))), dim3(256), \
+                     0, stream, x, T, ld, a, ids, dw, o, wide_out)
+  MOE_ROUTE_SHAPE(MOE_CALL);
+#undef MOE_CALL
+  return hipGetLastError();
+}
+
+bool moe_route_grid_fits(int64_t T) { return grid_fits((T + 3) / 4, 1, 256); }
+
+hipError_t launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const float* bias, int32_t K,
+                            int32_t groups, int32_t top_groups, int32_t group_top, bool sigmoid, bool renorm,
+                            float* weights, int32_t* ids, hipStream_t stream) {
+  const RouteArgs a = route_args(E, K, groups, top_groups, group_top, sigmoid, renorm, bias);
+  return dtype == 0 ? route_t<Fp32>(logits, T, ld, a, weights, ids, stream)
+       : dtype == 1 ? route_t<Bf16>(logits, T, ld, a, weights, ids, stream)
+                    : route_t<Fp16>(logits, T, ld, a, weights, ids, stream);
+}
+
+hipError_t launch_moe_route_backward(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, const int32_t* ids,
+                                     const float* dw, int32_t K, bool sigmoid, bool renorm, void* dlogits,
+                                     hipStream_t stream) {
+  const RouteArgs a = route_args(E, K, 1, 1, 1, sigmoid, renorm, nullptr);
+  return dtype == 0 ? route_back_t<Fp32>(logits, T, ld, a, ids, dw, dlogits, stream)
+       : dtype == 1 ? route_back_t<Bf16>(logits, T, ld, a, ids, dw, dlogits, stream)
+                    : route_back_t<Fp16>(logits, T, ld, a, ids, dw, dlogits, stream);
+}
+
+// ------------------------------------------------------------------ dispatch
+// Stable counting sort.  A workgroup owns a run of slots, each of its 8 waves
+// a part of that run.  A wave counts its part per expert in LDS; with the
+// totals of the workgroups before it (and of all experts before this one) the
+// count becomes the next free row of (wave, expert), and the wave walks its
+// part 64 slots at a time: lanes of the same expert find each other with one
+// ballot per bit of the id, a lane's rank is the number of such lanes below
+// it, and the last of them moves the counter on.  Nothing depends on the order
+// of waves or workgroups.  Up to kOneBlock slots a single workgroup does it
+// all; beyond that a first launch leaves every run's counts in the workspace
+// and each workgroup of the second adds up what it needs of them (at most 256
+// runs, so that this stays a few hundred KB of L2 reads).
+// Ids outside [0, E) are counted as expert E, whose rows come last.
+constexpr int DW = 8;                    // waves
+constexpr int64_t kOneBlock = 4096;
+constexpr int64_t kMaxRuns = 256;
+
+__device__ __forceinline__ int bucket_of(int id, int E) { return id >= 0 && id < E ? id : E; }
+
+__global__ __launch_bounds__(64 * DW) void moe_count_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t run, int E,
+                                                            int32_t* __restrict__ counts) {
+  extern __shared__ int32_t hist[];   // [E + 1]
+  for (int e = threadIdx.x; e <= E; e += 64 * DW) hist[e] = 0;
+  __syncthreads();
+  const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += 64 * DW) atomicAdd(&hist[bucket_of(ids[i], E)], 1);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += 64 * DW) counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
+}
+
+template <bool ONE>
+__global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t run, int E,
+                                                            int32_t top_k, int bits, int runs,
+                                                            const int32_t* __restrict__ counts,
+                                                            int32_t* __restrict__ offsets, int32_t* __restrict__ token,
+                                                            int32_t* __restrict__ position) {
+  extern __shared__ int32_t next[];   // [DW][E + 1], then [E + 1] first rows of this run
+  __shared__ int32_t wave_sum[DW];
+  int32_t* const first = next + DW * (E + 1);
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
+  const int64_t part = run / DW;      // a multiple of 64
+  const int64_t plo = lo + w * part;
+  const int64_t phi = plo + part < hi ? plo + part : hi;
+  for (int i = tid; i < DW * (E + 1); i += 64 * DW) next[i] = 0;
+  __syncthreads();
+  for (int64_t i = plo + lane; i < phi; i += 64) atomicAdd(&next[w * (E + 1) + bucket_of(ids[i], E)], 1);
+  __syncthreads();
+  // totals of all runs, scanned over the experts; 64 * DW experts at a time
+  int32_t carry = 0;
+  for (int e0 = 0; e0 <= E; e0 += 64 * DW) {
+    const int e = e0 + tid;
+    int32_t total = 0, before = 0;
+    if (e <= E) {
+      if (ONE) {
+        for (int v = 0; v < DW; v++) total += next[v * (E + 1) + e];
+      } else {
+#pragma unroll 8
+        for (int r = 0; r < runs; r++) {
+          const int32_t c = counts[(int64_t)r * (E + 1) + e];
+          total += c;
+          before += r < (int)blockIdx.x ? c : 0;
+        }
+      }
+    }
+    int32_t incl = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t o = __shfl_up(incl, d, 64);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 63) wave_sum[w] = incl;
+    __syncthreads();
+    int32_t start = carry + incl - total;
+    for (int v = 0; v < DW; v++) {
+      const int32_t c = wave_sum[v];
+      if (v < w) start += c;
+      carry += c;
+    }
+    if (e <= E) {
+      if (blockIdx.x == 0) offsets[e] = start;
+      first[e] = start + before;
+    }
+    __syncthreads();
+  }
+  for (int e = tid; e <= E; e += 64 * DW) {
+    int32_t at = first[e];
+    for (int v = 0; v < DW; v++) {
+      const int32_t c = next[v * (E + 1) + e];
+      next[v * (E + 1) + e] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  for (int64_t i0 = plo; i0 < phi; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool ok = i < phi;
+    const int id = ok ? bucket_of(ids[i], E) : 0;
+    uint64_t same = __ballot(ok);
+    for (int b = 0; b < bits; b++) {
+      const uint64_t m = __ballot((id >> b) & 1);
+      same &= ((id >> b) & 1) ? m : ~m;
+    }
+    if (ok) {
+      const int32_t at = next[w * (E + 1) + id];
+      const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
+      const int32_t row = at + rank;
+      // the slots before i: i / top_k, in 32 bits (n < 2^31)
+      token[row] = id < E ? (int32_t)((uint32_t)i / (uint32_t)top_k) : -1;
+      position[i] = id < E ? row : -1;
+      if ((same >> lane) == 1) next[w * (E + 1) + id] = row + 1;   // the last lane of this id
+    }
+    wave_lds_fence();
+  }
+}
+
+static int64_t dispatch_run(int64_t n) {
+  if (n <= kOneBlock) return kOneBlock;
+  const int64_t r = ((n + kMaxRuns - 1) / kMaxRuns + 64 * DW - 1) / (64 * DW) * (64 * DW);
+  return r > kOneBlock ? r : kOneBlock;
+}
+
+size_t moe_dispatch_workspace(int64_t n, int64_t E) {
+  if (n <= kOneBlock) return 0;
+  const int64_t run = dispatch_run(n);
+  return (size_t)((n + run - 1) / run) * (size_t)(E + 1) * 4u;
+}
+
+hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t top_k, int32_t* offsets, int32_t* token,
+                               int32_t* position, int32_t* ws, hipStream_t stream) {
+  int bits = 1;
+  while ((1ll << bits) <= E) bits++;   // ids 0 .. E
+  const int64_t run = dispatch_run(n);
+  const int runs = n <= kOneBlock ? 1 : (int)((n + run - 1) / run);
+  const size_t lds = (size_t)(DW + 1) * (size_t)(E + 1) * 4u;
+  if (runs == 1) {
+    hipLaunchKernelGGL((moe_place_kernel<true>), dim3(1), dim3(64 * DW), lds, stream, ids, n, run, (int)E, top_k, bits, 1,
+                       nullptr, offsets, token, position);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)runs), dim3(64 * DW), (size_t)(E + 1) * 4u, stream, ids, n, run,
+                     (int)E, ws);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((moe_place_kernel<false>), dim3((unsigned)runs), dim3(64 * DW), lds, stream, ids, n, run, (int)E,
+                     top_k, bits, runs, ws, offsets, token, position);
+  return hipGetLastError();
+}
+
+// ------------------------------------------------------------------- combine
+// out[t] = sum_k w[t][k] y[pos[t][k]]: one pass over the rows of y, bound by
+// HBM.  A thread owns 16 bytes of a token's row (VEC; single elements where
+// rows are not 16-byte aligned) and has the loads of eight slots in flight.
+// tpt threads (a power of two, 64 .. 256, so that a wave has one token) share
+// a token.
+template <typename D, bool VEC>
+__global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* __restrict__ y, int64_t rows, int64_t ldy,
+                                                          const int32_t* __restrict__ pos, const float* __restrict__ w,
+                                                          int64_t T, int K, int64_t H, typename D::T* __restrict__ out,
+                                                          int tpt, int chunks) {
+  constexpr int V = VEC ? D::V : 1;
+  const int per = 256 / tpt;
+  const int64_t tb = blockIdx.x / chunks;
+  const int ch = (int)(blockIdx.x - tb * chunks);
+  const int64_t t = tb * per + __builtin_amdgcn_readfirstlane((int)threadIdx.x / tpt);
+  const int64_t h = ((int64_t)ch * tpt + (threadIdx.x & (tpt - 1))) * V;
+  if (t >= T || h >= H) return;
+  const int32_t* tp = pos + t * K;
+  const float* tw = w + t * K;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; i++) acc[i] = 0.0f;
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    u32x4 v[8];
+    typename D::T sv[8];
+    bool ok[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+      const int64_t p = k0 + k < K ? tp[k0 + k] : -1;
+      ok[k] = p >= 0 && p < rows;
+      if (ok[k]) {
+        if constexpr (VEC) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(y + p * ldy + h));
+        else sv[k] = y[p * ldy + h];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; k++)
+      if (ok[k]) {
+        const float wk = tw[k0 + k];
+        float f[V];
+        if constexpr (VEC) unpack<D>(v[k], f);
+        else f[0] = to_f32<D>(sv[k]);
+#pragma unroll
+        for (int i = 0; i < V; i++) acc[i] = fmaf(wk, f[i], acc[i]);
+      }
+  }
+  if constexpr (VEC) *reinterpret_cast<u32x4*>(out + t * H + h) = pack<D>(acc);
+  else out[t * H + h] = from_f32<D>(acc[0]);
+}
+
+// How often a row of y is named; clear and count in one launch where one
+// workgroup does both.
+__global__ __launch_bounds__(256) void moe_clear_kernel(int32_t* __restrict__ count, int64_t rows) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < rows) count[i] = 0;
+}
+__global__ __launch_bounds__(256) void moe_named_kernel(const int32_t* __restrict__ pos, int64_t n, int64_t rows,
+                                                        int32_t* __restrict__ count) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int64_t p = pos[i];
+  if (p >= 0 && p < rows) atomicAdd(&count[p], 1);
+}
+
+// Backward.  TPT threads (64: four tokens a workgroup, 256: one) own a token:
+// they read dout once and the token's rows of y, write the rows of dy and
+// reduce the dot products.  A row that one slot names is written here as
+// w * dout; one that several name is summed by the lowest of its slots (which
+// finds the others by going through the positions: right, and slow, for what
+// no dispatch produces).  The workgroups behind the tokens' own zero the rows
+// that nobody names.
+template <typename D, bool VEC, int TPT>
+__global__ __launch_bounds__(256) void moe_combine_backward_kernel(
+    const typename D::T* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ pos,
+    const float* __restrict__ w, int64_t T, int K, int64_t H, const typename D::T* __restrict__ dout, int64_t ldd,
+    typename D::T* __restrict__ dy, float* __restrict__ dw, const int32_t* __restrict__ count, int64_t token_blocks) {
+  constexpr int V = VEC ? D::V : 1;
+  constexpr int PER = 256 / TPT;
+  __shared__ float part[4][8];
+  const int lane = threadIdx.x & 63;
+  if ((int64_t)blockIdx.x >= token_blocks) {   // rows without a slot; launched with dy alone
+    const int64_t r0 = ((int64_t)blockIdx.x - token_blocks) * 256 + (threadIdx.x & ~63);
+    uint64_t none = __ballot(r0 + lane < rows && count[r0 + lane < rows ? r0 + lane : 0] == 0);
+    while (none) {
+      const int64_t r = r0 + __builtin_ctzll(none);
+      none &= none - 1;
+      for (int64_t h = (int64_t)lane * V; h < H; h += 64 * V) {
+        if constexpr (VEC) *reinterpret_cast<u32x4*>(dy + r * H + h) = u32x4{0u, 0u, 0u, 0u};
+        else dy[r * H + h] = from_f32<D>(0.0f);
+      }
+    }
+    return;
+  }
+  const int64_t t = (int64_t)blockIdx.x * PER + __builtin_amdgcn_readfirstlane((int)threadIdx.x / TPT);
+  const int l = threadIdx.x & (TPT - 1);
+  if (t < T) {   // uniform in a wave, and in the workgroup where TPT is 256
+    for (int k0 = 0; k0 < K; k0 += 8) {
+      int64_t p[8];
+      float wk[8], acc[8];
+      int own[8];   // 0: no row, 1: this slot's alone, 2: shared
+#pragma unroll
+      for (int k = 0; k < 8; k++) {
+        p[k] = k0 + k < K ? pos[t * K + k0 + k] : -1;
+        if (p[k] >= rows) p[k] = -1;
+        wk[k] = k0 + k < K ? w[t * K + k0 + k] : 0.0f;
+        own[k] = p[k] >= 0 && dy ? (count[p[k]] == 1 ? 1 : 2) : 0;
+        acc[k] = 0.0f;
+      }
+      for (int64_t h = (int64_t)l * V; h < H; h += TPT * V) {
+        float g[V];
+        if constexpr (VEC) unpack<D>(*reinterpret_cast<const u32x4*>(dout + t * ldd + h), g);
+        else g[0] = to_f32<D>(dout[t * ldd + h]);
+        if (dw) {
+          u32x4 v[8];
+          typename D::T sv[8];
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            if (p[k] >= 0) {
+              if constexpr (VEC) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(y + p[k] * ldy + h));
+              else sv[k] = y[p[k] * ldy + h];
+            }
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            if (p[k] >= 0) {
+              float f[V];
+              if constexpr (VEC) unpack<D>(v[k], f);
+              else f[0] = to_f32<D>(sv[k]);
+#pragma unroll
+              for (int i = 0; i < V; i++) acc[k] = fmaf(g[i], f[i], acc[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+          if (own[k] == 1) {
+            float f[V];
+#pragma unroll
+            for (int i = 0; i < V; i++) f[i] = wk[k] * g[i];
+            if constexpr (VEC) __builtin_nontemporal_store(pack<D>(f), reinterpret_cast<u32x4*>(dy + p[k] * H + h));
+            else dy[p[k] * H + h] = from_f32<D>(f[0]);
+          }
+      }
+#pragma unroll 1
+      for (int k = 0; k < 8; k++) {
+        if (own[k] != 2) continue;
+        const int64_t me = t * K + k0 + k;
+        bool earlier = false;
+        for (int64_t i0 = 0; i0 < me && !earlier; i0 += 64)
+          earlier = __any(i0 + lane < me && pos[i0 + lane < me ? i0 + lane : 0] == p[k]);
+        if (earlier) continue;
+        for (int64_t h = (int64_t)l * V; h < H; h += TPT * V) {
+          float f[V];
+#pragma unroll
+          for (int i = 0; i < V; i++) f[i] = 0.0f;
+          for (int64_t i = me; i < T * K; i++) {
+            if (pos[i] != p[k]) continue;
+            const int64_t ti = i / K;
+            float g[V];
+            if constexpr (VEC) unpack<D>(*reinterpret_cast<const u32x4*>(dout + ti * ldd + h), g);
+            else g[0] = to_f32<D>(dout[ti * ldd + h]);
+#pragma unroll
+            for (int j = 0; j < V; j++) f[j] = fmaf(w[i], g[j], f[j]);
+          }
+          if constexpr (VEC) *reinterpret_cast<u32x4*>(dy + p[k] * H + h) = pack<D>(f);
+          else dy[p[k] * H + h] = from_f32<D>(f[0]);
+        }
+      }
+      if (dw) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) acc[k] = lanes_reduce<64>(acc[k], OpAdd{});
+        if (TPT == 64) {
+#pragma unroll
+          for (int k = 0; k < 8; k++)
+            if (lane == 0 && k0 + k < K) dw[t * K + k0 + k] = acc[k];
+        } else {
+          if (lane == 0) {
+#pragma unroll
+            for (int k = 0; k < 8; k++) part[threadIdx.x >> 6][k] = acc[k];
+          }
+          __syncthreads();
+          if (threadIdx.x < 8 && k0 + (int)threadIdx.x < K) {
+            const int k = threadIdx.x;
+            dw[t * K + k0 + k] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
+          }
+          __syncthreads();
+        }
+      }
+    }
+  }
+}
+
+static bool vec_rows(const void* p, int64_t ld, int64_t H, int esize) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * esize) % 16 == 0 && (H * esize) % 16 == 0;
+}
+
+// The forward's grid: threads per token (a power of two, 64 .. 256), their
+// repeats along the row, workgroups along the tokens.
+struct CombineGrid {
+  bool vec;
+  int tpt;
+  int64_t chunks, tb;
+};
+static CombineGrid combine_grid(const void* y, int es, int64_t ldy, int64_t T, int64_t H, const void* out) {
+  CombineGrid g;
+  g.vec = vec_rows(y, ldy, H, es) && vec_rows(out, H, H, es);
+  const int64_t items = g.vec ? H * es / 16 : H;
+  g.tpt = items > 128 ? 256 : items > 64 ? 128 : 64;
+  g.chunks = (items + g.tpt - 1) / g.tpt;
+  g.tb = (T + 256 / g.tpt - 1) / (256 / g.tpt);
+  return g;
+}
+
+template <typename D>
+static hipError_t combine_t(const void* y, int64_t rows, int64_t ldy, const int32_t* pos, const float* w, int64_t T, int K,
+                            int64_t H, void* out, hipStream_t stream) {
+  const auto [vec, tpt, chunks, tb] = combine_grid(y, sizeof(typename D::T), ldy, T, H, out);
+  const auto* yy = static_cast<const typename D::T*>(y);
+  auto* o = static_cast<typename D::T*>(out);
+  if (vec)
+    hipLaunchKernelGGL((moe_combine_kernel<D, true>), dim3((unsigned)(tb * chunks)), dim3(256), 0, stream, yy, rows, ldy, pos,
+                       w, T, K, H, o, tpt, (int)chunks);
+  else
+    hipLaunchKernelGGL((moe_combine_kernel<D, false>), dim3((unsigned)(tb * chunks)), dim3(256), 0, stream, yy, rows, ldy,
+                       pos, w, T, K, H, o, tpt, (int)chunks);
+  return hipGetLastError();
+}
+
+bool moe_combine_grid_fits(const void* y, int dtype, int64_t ldy, int64_t T, int64_t H, const void* out) {
+  const CombineGrid g = combine_grid(y, dtype == 0 ? 4 : 2, ldy, T, H, out);
+  return g.chunks <= 0x7FFFFFFF && grid_fits(g.tb, g.chunks, 256);
+}
+bool moe_combine_backward_grid_fits(int64_t T, int64_t K, int64_t rows) {
+  return grid_fits(T + (rows + 255) / 256, 1, 256) && grid_fits((T * K + 255) / 256, 1, 256);
+}
+
+hipError_t launch_moe_combine(const void* y, int dtype, int64_t rows, int64_t ldy, const int32_t* pos, const float* w,
+                              int64_t T, int K, int64_t H, void* out, hipStream_t stream) {
+  return dtype == 0 ? combine_t<Fp32>(y, rows, ldy, pos, w, T, K, H, out, stream)
+       : dtype == 1 ? combine_t<Bf16>(y, rows, ldy, pos, w, T, K, H, out, stream)
+                    : combine_t<Fp16>(y, rows, ldy, pos, w, T, K, H, out, stream);
+}
+
+template <typename D>
+static hipError_t combine_back_t(const void* y, int64_t rows, int64_t ldy, const int32_t* pos, const float* w, int64_t T,
+                                 int K, int64_t H, const void* dout, int64_t ldd, void* dy, float* dw, int32_t* count,
+                                 hipStream_t stream) {
+  const int es = sizeof(typename D::T);
+  const bool vec = vec_rows(dout, ldd, H, es) && (!dw || vec_rows(y, ldy, H, es)) && (!dy || vec_rows(dy, H, H, es));
+  const int64_t items = vec ? H / D::V : H;
+  const auto* yy = static_cast<const typename D::T*>(y);
+  const auto* g = static_cast<const typename D::T*>(dout);
+  auto* o = static_cast<typename D::T*>(dy);
+  if (dy) {
+    hipLaunchKernelGGL(moe_clear_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, stream, count, rows);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (T * K > 0)
+      hipLaunchKernelGGL(moe_named_kernel, dim3((unsigned)((T * K + 255) / 256)), dim3(256), 0, stream, pos, T * K, rows,
+                         count);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int tpt = items > 128 ? 256 : 64;
+  const int64_t tb = (T + 256 / tpt - 1) / (256 / tpt);
+  const int64_t blocks = tb + (dy ? (rows + 255) / 256 : 0);
+  if (blocks == 0) return hipSuccess;
+#define MOE_BACK(VE, TP)                                                                                                 \
+  hipLaunchKernelGGL((moe_combine_backward_kernel<D, VE, TP>), dim3((unsigned)blocks), dim3(256), 0, stream, yy, rows, ldy, \
+                     pos, w, T, K, H, g, ldd, o, dw, count, tb)
+  if (vec) { if (tpt == 256) MOE_BACK(true, 256); else MOE_BACK(true, 64); }
+  else { if (tpt == 256) MOE_BACK(false, 256); else MOE_BACK(false, 64); }
+#undef MOE_BACK
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const void* y, int dtype, int64_t rows, int64_t ldy, const int32_t* pos,
+                                       const float* w, int64_t T, int K, int64_t H, const void* dout, int64_t ldd,
+                                       void* dy, float* dw, int32_t* count, hipStream_t stream) {
+  return dtype == 0 ? combine_back_t<Fp32>(y, rows, ldy, pos, w, T, K, H, dout, ldd, dy, dw, count, stream)
+       : dtype == 1 ? combine_back_t<Bf16>(y, rows, ldy, pos, w, T, K, H, dout, ldd, dy, dw, count, stream)
+                    : combine_back_t<Fp16>(y, rows, ldy, pos, w, T, K, H, dout, ldd, dy, dw, count, stream);
+}
+
+}  // namespace mx

@@ -1,0 +1,270 @@
+"""MXFP4 quantize, dequantize and products against the plain implementation in
+64 bits."""
+
+import numpy as np
+import pytest
+
+import mx4_util as ref
+from gpu_util import bf16_to_f64, log, need_gpu, to_dev, to_dev_bf16, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+def _mxfp4():
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import mxfp4
+    return torch, mxfp4
+
+
+def _words(a):
+    return to_dev(a.view(np.int32))
+
+
+def _every_pattern():
+    """Rows of one amax exponent each, whose other values are every BF16 pattern
+    of the five exponents from it down, with both signs."""
+    rows = []
+    for e in range(255):
+        top = (e << 7) | 0x7F
+        lo = max(0, e - 4) << 7
+        near = np.arange(lo, top + 1, dtype=np.uint16)
+        near = np.concatenate((near, near | 0x8000))
+        near = np.resize(near, -(-near.size // 31) * 31).reshape(-1, 31)
+        block = np.concatenate((np.full((near.shape[0], 1), top, np.uint16), near), 1).reshape(-1)
+        rows.append(np.resize(block, 32 * 44))
+    return np.stack(rows)
+
+
+def test_quantize_every_bf16_pattern_under_every_scale():
+    torch, mxfp4 = _mxfp4()
+    bits = _every_pattern()
+    log("mxfp4 quantize of %s" % (bits.shape,))
+    got = mxfp4.quantize(to_dev_bf16(bits), packed=True)
+    codes, scales = ref.quantize(bits)
+    assert np.array_equal(to_host(got["p_row"]), ref.pack(scales))
+    assert np.array_equal(to_host(got["q_row"]), codes)
+
+
+def test_dequantize_every_code_under_every_scale():
+    torch, mxfp4 = _mxfp4()
+    codes = np.tile((np.arange(16, dtype=np.uint8) * 17), (254, 2)).reshape(254, 32)[:, :16]
+    codes = np.concatenate((codes, codes[:, ::-1], codes ^ 0x50, codes ^ 0x0A), 1)     # [254, 64]: 4 blocks
+    scales = np.repeat(np.arange(254, dtype=np.uint8)[:, None], 4, 1)
+    want = ref.dequantize(codes, scales)
+    for s in (to_dev(scales), _words(ref.pack(scales))):
+        got = bf16_to_f64(to_host(mxfp4.dequantize(to_dev(codes), s)))
+        # E2M1 value times a power of two: exact in BF16 up to its largest value
+        fits = np.abs(want) < 2.0 ** 128
+        assert np.array_equal(got[fits], want[fits])
+        assert np.all(np.isinf(got[~fits]) & (np.sign(got[~fits]) == np.sign(want[~fits])))
+    zero = to_host(mxfp4.dequantize(to_dev(codes), to_dev(scales)))[want == 0]
+    assert set(np.unique(zero)) == {0, 0x8000}
+
+
+@pytest.mark.parametrize("R,C,ld", [(1, 32, 32), (1, 128, 128), (3, 96, 104), (33, 640, 640), (130, 1056, 1064), (32, 4096, 4096),
+                                    (257, 512, 512), (4100, 2080, 2080)])
+@pytest.mark.parametrize("packed", [False, True])
+def test_quantize_rowwise(R, C, ld, packed):
+    torch, mxfp4 = _mxfp4()
+    if packed and C % 128:
+        C += 128 - C % 128
+        ld = max(ld, C)
+    bits = ref.heavy_bits((R, ld), R + C)
+    log("mxfp4 rowwise R=%d C=%d ld=%d packed=%s" % (R, C, ld, packed))
+    got = mxfp4.quantize(to_dev_bf16(bits)[:, :C], packed=packed)
+    codes, scales = ref.quantize(bits[:, :C])
+    assert np.array_equal(to_host(got["q_row"]), codes)
+    if packed:
+        assert np.array_equal(to_host(got["p_row"]), ref.pack(scales))
+    else:
+        assert np.array_equal(to_host(got["s_row"]), scales)
+
+
+@pytest.mark.parametrize("R,C", [(32, 32), (128, 128), (160, 96), (384, 640), (1024, 416), (512, 1152)])
+@pytest.mark.parametrize("packed", [False, True])
+@pytest.mark.parametrize("rowwise", [False, True])
+def test_quantize_colwise(R, C, packed, rowwise):
+    torch, mxfp4 = _mxfp4()
+    if packed:
+        R, C = -(-R // 128) * 128, -(-C // 128) * 128 if rowwise else C
+    bits = ref.heavy_bits((R, C), R * 3 + C)
+    log("mxfp4 colwise R=%d C=%d packed=%s rowwise=%s" % (R, C, packed, rowwise))
+    got = mxfp4.quantize(to_dev_bf16(bits), rowwise=rowwise, colwise=True, packed=packed)
+    for name, b in (("row", bits), ("colT", np.ascontiguousarray(bits.T)))[0 if rowwise else 1:]:
+        codes, scales = ref.quantize(b)
+        assert np.array_equal(to_host(got["q_" + name]), codes), name
+        if packed:
+            assert np.array_equal(to_host(got["p_" + name]), ref.pack(scales)), name
+        else:
+            assert np.array_equal(to_host(got["s_" + name]), scales), name
+
+
+def test_quantize_gathered_rows():
+    torch, mxfp4 = _mxfp4()
+    bits = ref.heavy_bits((50, 384), 5)
+    index = np.array([3, 3, -1, 49, 50, 0, 7, 2 ** 31 - 1, -2 ** 31, 12, 48] * 7, np.int32)
+    ok = (index >= 0) & (index < 50)
+    gathered = np.where(ok[:, None], bits[np.where(ok, index, 0)], np.uint16(0))
+    codes, scales = ref.quantize(gathered)
+    for packed in (False, True):
+        got = mxfp4.quantize(to_dev_bf16(bits), packed=packed, index=to_dev(index))
+        assert np.array_equal(to_host(got["q_row"]), codes)
+        want = ref.pack(scales) if packed else scales
+        assert np.array_equal(to_host(got["p_row" if packed else "s_row"]), want)
+
+
+def test_empty_inputs():
+    torch, mxfp4 = _mxfp4()
+    z = torch.empty((0, 256), dtype=torch.bfloat16, device="cuda")
+    got = mxfp4.quantize(z, packed=True)
+    assert got["q_row"].shape == (0, 128) and got["p_row"].shape == (2, 0)
+    assert mxfp4.dequantize(got["q_row"], got["p_row"]).shape == (0, 256)
+    b = mxfp4.quantize(torch.ones((64, 256), dtype=torch.bfloat16, device="cuda"), packed=True)
+    assert mxfp4.gemm(got["q_row"], got["p_row"], b["q_row"], b["p_row"]).shape == (0, 64)
+    # no reduction: zeros, or the old values with accumulate
+    a0 = torch.empty((5, 0), dtype=torch.uint8, device="cuda")
+    b0 = torch.empty((64, 0), dtype=torch.uint8, device="cuda")
+    pa, pb = (torch.empty((0, n), dtype=torch.int32, device="cuda") for n in (5, 64))
+    out = torch.full((5, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(mxfp4.gemm(a0, pa, b0, pb, out=out, accumulate=True), torch.full_like(out, 3.0))
+    assert torch.equal(mxfp4.gemm(a0, pa, b0, pb, out=out), torch.zeros_like(out))
+
+
+# The fp32 sum of K products is within K 2^-24 of the sum of their magnitudes
+# whatever the order; the BF16 rounding adds 2^-8 of the value.
+def _bounds(x, y):
+    want = x @ y.T
+    return want, x.shape[1] * 2.0 ** -24 * (np.abs(x) @ np.abs(y).T)
+
+
+def _swiglu(gate, up):
+    (g, dg), (u, du) = gate, up
+    with np.errstate(over="ignore"):
+        s = g / (1 + np.exp(-g))
+    # |SiLU'| <= 1.1; silu_f32 is within 1.14 (4 + |g|) 2^-23 of its value
+    return s * u, 1.1 * dg * (np.abs(u) + du) + np.abs(s) * du + 1.14 * (4 + np.abs(g)) * 2.0 ** -23 * np.abs(s * u)
+
+
+def _close(got, want, err, label):
+    tol = err + 2.0 ** -8 * (np.abs(want) + err)
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), "%s: %d off, first at %s: %g for %g (tol %g)" % (
+        label, bad.sum(), np.argwhere(bad)[0], got[bad][0], want[bad][0], tol[bad][0])
+
+
+SHAPES = [(1, 32, 128), (1, 1024, 4096), (3, 96, 384), (16, 64, 640), (17, 160, 256), (37, 32, 1152), (64, 256, 2048),
+          (65, 288, 512), (100, 1024, 1280), (129, 544, 896), (255, 256, 256), (300, 800, 640), (513, 1056, 384),
+          (1000, 2080, 768), (2049, 1312, 512)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_gemm(M, N, K, mode):
+    torch, mxfp4 = _mxfp4()
+    rng = np.random.default_rng(M * 7 + N * 3 + K)
+    a, sa, va = ref.random_operand(rng, M, K)
+    b, sb, vb = ref.random_operand(rng, N * (2 if mode == "swiglu" else 1), K)
+    if mode == "swiglu":   # gates of a few units
+        sa, va = sa - 3, va / 8
+        sb, vb = sb - 3, vb / 8
+    log("mxfp4 gemm M=%d N=%d K=%d %s" % (M, N, K, mode))
+    args = (to_dev(a), _words(ref.pack(sa)), to_dev(b), _words(ref.pack(sb)))
+    want, err = _bounds(va, vb)
+    if mode == "accumulate":
+        old = ref.heavy_bits((M, N + 8), 3)
+        out = to_dev_bf16(old)
+        got = to_host(mxfp4.gemm(*args, out=out[:, :N], accumulate=True))
+        assert np.array_equal(to_host(out)[:, N:], old[:, N:])
+        o = bf16_to_f64(old[:, :N])
+        want, err = want + o, err + 2.0 ** -24 * (np.abs(want) + np.abs(o))
+    else:
+        got = to_host(mxfp4.gemm(*args, swiglu=mode == "swiglu"))
+        if mode == "swiglu":
+            want, err = _swiglu((want[:, :N], err[:, :N]), (want[:, N:], err[:, N:]))
+    _close(bf16_to_f64(got), want, err, "M=%d N=%d K=%d %s" % (M, N, K, mode))
+
+
+COUNTS = [[5], [0, 0, 7, 0], [1, 0, 16, 17, 33, 0, 2, 64], [300, 0, 1, 257, 40], [0] * 65 + [3] + [0] * 4 + [130, 1],
+          [700, 600, 0, 513]]
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=[str(i) for i in range(len(COUNTS))])
+@pytest.mark.parametrize("N,K", [(64, 256), (288, 640)])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_grouped_gemm(counts, N, K, mode):
+    torch, mxfp4 = _mxfp4()
+    G, M = len(counts), sum(counts) + 3           # three rows outside every group
+    rng = np.random.default_rng(M + N + K)
+    rows = N * (2 if mode == "swiglu" else 1)
+    a, sa, va = ref.random_operand(rng, M, K)
+    b, sb, vb = ref.random_operand(rng, G * rows, K)
+    if mode == "swiglu":
+        sa, va, sb, vb = sa - 3, va / 8, sb - 3, vb / 8
+    offsets = np.concatenate(([0], np.cumsum(counts))).astype(np.int32)
+    old = ref.heavy_bits((M, N), 9)
+    out = to_dev_bf16(old)
+    log("mxfp4 grouped %s N=%d K=%d %s" % (counts[:8], N, K, mode))
+    got = mxfp4.grouped_gemm(to_dev(a), _words(ref.pack(sa)), to_dev(b.reshape(G, rows, K // 2)), _words(ref.pack(sb)),
+                             to_dev(offsets), out=out, accumulate=mode == "accumulate", swiglu=mode == "swiglu")
+    got = to_host(got)
+    assert np.array_equal(got[M - 3:], old[M - 3:])
+    for g in range(G):
+        r = slice(offsets[g], offsets[g + 1])
+        want, err = _bounds(va[r], vb[g * rows:(g + 1) * rows])
+        if mode == "accumulate":
+            o = bf16_to_f64(old[r])
+            want, err = want + o, err + 2.0 ** -24 * (np.abs(want) + np.abs(o))
+        if mode == "swiglu":
+            want, err = _swiglu((want[:, :N], err[:, :N]), (want[:, N:], err[:, N:]))
+        _close(bf16_to_f64(got[r]), want, err, "group %d" % g)
+
+
+def test_grouped_gemm_invalid_offsets_stay_inside():
+    """Bounds are clamped into [0, M] and raised to the largest one before."""
+    torch, mxfp4 = _mxfp4()
+    M, N, K, G = 70, 64, 256, 5
+    rng = np.random.default_rng(4)
+    a, sa, va = ref.random_operand(rng, M, K)
+    b, sb, vb = ref.random_operand(rng, G * N, K)
+    offsets = np.array([-7, 20, 4, 1000, 60, 2 ** 31 - 1], np.int32)
+    edges = np.maximum.accumulate(np.clip(offsets, 0, M))
+    old = ref.heavy_bits((M, N), 2)
+    got = bf16_to_f64(to_host(mxfp4.grouped_gemm(to_dev(a), _words(ref.pack(sa)), to_dev(b.reshape(G, N, K // 2)),
+                                                 _words(ref.pack(sb)), to_dev(offsets), out=to_dev_bf16(old))))
+    for g in range(G):
+        r = slice(edges[g], edges[g + 1])
+        _close(got[r], *_bounds(va[r], vb[g * N:(g + 1) * N]), "group %d" % g)
+
+
+def test_gemm_extreme_scales():
+    """Scale bytes over the whole range: sums past BF16's range are infinite,
+    the others keep their tolerance."""
+    torch, mxfp4 = _mxfp4()
+    rng = np.random.default_rng(8)
+    M, N, K = 40, 64, 256
+    a, sa, _ = ref.random_operand(rng, M, K)
+    b, sb, _ = ref.random_operand(rng, N, K)
+    sa = np.repeat(rng.integers(60, 250, (M, 1), dtype=np.uint8), K // 32, 1)
+    sb = np.repeat(rng.integers(60, 140, (N, 1), dtype=np.uint8), K // 32, 1)
+    va, vb = ref.dequantize(a, sa), ref.dequantize(b, sb)
+    got = bf16_to_f64(to_host(mxfp4.gemm(to_dev(a), _words(ref.pack(sa)), to_dev(b), _words(ref.pack(sb)))))
+    want, err = _bounds(va, vb)
+    mags = np.abs(va) @ np.abs(vb).T
+    fits = (mags < 2.0 ** 127) & (mags > 2.0 ** -100)
+    assert fits.any()
+    _close(got[fits], want[fits], err[fits], "extreme scales")
+
+
+def test_round_trip_of_a_linear_layer_in_mxfp4():
+    """quantize -> gemm -> quantize -> gemm on a stream of its own, against the
+    values that codes and scales stand for."""
+    torch, mxfp4 = _mxfp4()
+    x, w = (torch.randn(n, 512, device="cuda").bfloat16() for n in (200, 384))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qx, qw = (mxfp4.quantize(t, packed=True, stream=side) for t in (x, w))
+    y = mxfp4.gemm(qx["q_row"], qx["p_row"], qw["q_row"], qw["p_row"], stream=side)
+    vx, vw = (mxfp4.dequantize(q["q_row"], q["p_row"], stream=side) for q in (qx, qw))
+    side.synchronize()
+    vx, vw = (bf16_to_f64(to_host(t)) for t in (vx, vw))
+    _close(bf16_to_f64(to_host(y)), *_bounds(vx, vw), "linear layer")
