@@ -88,6 +88,8 @@ struct Mx4Gemm {
 };
 bool mx4_gemm_grid_fits(const Mx4Gemm& g);
 hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream);
+bool mx4_gemm_tile_fits(const Mx4Gemm& g);
+hipError_t launch_mx4_gemm_tile(const Mx4Gemm& g, hipStream_t stream);
 
 // ---- mixture of experts (sizes as checked by the C ABI of include/moe.h)
 bool moe_route_grid_fits(int64_t T);

@@ -174,9 +174,14 @@ static hipError_t launch_rows(const Mx4Gemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-bool mx4_gemm_grid_fits(const Mx4Gemm& g) { return grid_fits(g.M + g.G, g.N / 16, 256) ; }
+// Rows of a group on average (dense: all rows).
+static int64_t rows_per_group(const Mx4Gemm& g) { return g.offsets ? (g.M + g.G - 1) / g.G : g.M; }
+static bool few_rows(const Mx4Gemm& g) { return rows_per_group(g) <= 256; }
+
+bool mx4_gemm_grid_fits(const Mx4Gemm& g) { return few_rows(g) ? grid_fits(g.M + g.G, g.N / 16, 256) : mx4_gemm_tile_fits(g); }
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream) {
+  if (!few_rows(g)) return launch_mx4_gemm_tile(g, stream);
   const bool grouped = g.offsets != nullptr;
   if (grouped) {
     if (g.epilogue == EPI_SWIGLU) return launch_rows<2, 2, 4, true, EPI_SWIGLU>(g, stream);
