@@ -1,17 +1,19 @@
-"""Argument checks and stream handling shared by the tensor-level operators."""
+"""The extension module of the tensor-level operators, their C functions and
+their use on another stream."""
 
 from __future__ import annotations
+
+import ctypes
 
 import torch
 
 from . import MXFP8Error, lib
 
 
-def declare(name, argtypes, restype=None):
+def declare(name, argtypes, restype=ctypes.c_int):
     """The C function `name` of libmxfp8 with its argument types set."""
-    import ctypes
     f = getattr(lib(), name)
-    f.restype = ctypes.c_int if restype is None else restype
+    f.restype = restype
     f.argtypes = argtypes
     return f
 
@@ -21,33 +23,13 @@ def check(status, where):
         raise MXFP8Error(status, where)
 
 
-def need(t, name, dtype, shape, device=None):
-    """A dense GPU tensor of this type and shape (on `device`, when given)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch tensor" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA (HIP) tensor, got %s" % (name, t.device))
-    if t.dtype is not dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if device is not None and t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-
-
-def launch(f, where, device, *args):
-    """Call a C entry point with the current stream of `device` (its last
-    argument), that device being current during the call."""
-    index = device.index
-    if torch._C._cuda_getDevice() == index:
-        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    else:
-        with torch.cuda.device(index):
-            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
-    if status != 0:
-        raise MXFP8Error(status, where)
+def extension():
+    """The module _mx_torch; raises if it has not been built."""
+    try:
+        from . import _mx_torch
+    except ImportError as e:
+        raise RuntimeError("_mx_torch.so is not built (run mxfp8_block_scaled_quantize_amd.build.build()): %s" % e) from e
+    return _mx_torch
 
 
 def on_stream(stream, tensors, call):

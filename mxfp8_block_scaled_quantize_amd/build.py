@@ -1,12 +1,16 @@
-"""Build libmxfp8.so (gfx950 HIP kernels + C ABI) in-tree with hipcc, and
+"""Build libmxfp8.so (gfx950 HIP kernels + C ABI) in-tree with hipcc,
 libmxfp8_calib.so, the benchmark's measurement aid (the register-only MFMA
-rate; not part of the library)."""
+rate; not part of the library), and _mx_torch.so, the extension module of the
+tensor-level MXFP4 and mixture-of-experts operators (host C++ against PyTorch's
+headers, linked to libmxfp8.so)."""
 
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -16,6 +20,8 @@ CALIB_PATH = os.path.join(HERE, "libmxfp8_calib.so")
 SOURCES = ["api.hip", "quantize.hip", "pack_scales.hip", "gemm.hip", "api_mx4.hip", "mx4_quantize.hip", "mx4_gemm.hip",
            "mx4_gemm_tile.hip", "moe.hip"]
 CALIB_SOURCES = ["calib.hip"]
+TORCH_PATH = os.path.join(HERE, "_mx_torch.so")
+TORCH_SOURCE = "torch_binding.cpp"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Packed-FP32 VALU forms are disabled for all device code; hipcc's host pass
@@ -23,6 +29,18 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 DEVICE_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                 "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
                 "-Wall", "-Wno-unused-function", "-Wno-unknown-warning-option"]
+
+
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _host_compile(obj: str) -> list:
+    """Compile command of the extension module (HIP's headers want the platform named)."""
+    inc = os.path.join(_torch_dir(), "include")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
+            "-I" + sysconfig.get_path("include"), "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
 
 
 def build(verbose: bool = False) -> str:
@@ -34,6 +52,9 @@ def build(verbose: bool = False) -> str:
         objs.append(obj)
         cmd = [HIPCC, *DEVICE_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
         procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    binding = os.path.join(BUILD_DIR, TORCH_SOURCE.replace(".cpp", ".o"))
+    cmd = _host_compile(binding)
+    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = False
     for cmd, p in procs:
         out, _ = p.communicate()
@@ -51,6 +72,10 @@ def build(verbose: bool = False) -> str:
         tmp = path + ".tmp%d" % os.getpid()
         subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *parts, "-o", tmp])
         os.replace(tmp, path)
+    tmp = TORCH_PATH + ".tmp%d" % os.getpid()
+    subprocess.check_call(["g++", "-shared", binding, "-o", tmp, "-L" + HERE, "-lmxfp8", "-L" + os.path.join(_torch_dir(), "lib"),
+                           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, TORCH_PATH)
     return LIB_PATH
 
 

@@ -2,8 +2,8 @@
 the block-scaled products, dense and grouped.
 
 ``mxfp4_*`` mirror the C ABI of ``include/mxfp4.h``; ``quantize``,
-``dequantize``, ``gemm`` and ``grouped_gemm`` allocate outputs with torch and
-call them.  Codes are uint8, two to a byte (lower index in the low nibble);
+``dequantize``, ``gemm`` and ``grouped_gemm`` check their tensors, allocate the
+outputs and call it (in the extension module ``_mx_torch``).  Codes are uint8, two to a byte (lower index in the low nibble);
 packed scale words are int32 [K / 128, rows], as for MXFP8.  Every step runs in
 the HIP kernels of ``libmxfp8.so``; there is no fallback.
 """
@@ -14,7 +14,7 @@ import ctypes
 
 import torch
 
-from ._tensors import check, declare, launch, need, on_stream
+from ._tensors import check, declare, extension, on_stream
 
 MXFP4_ROWWISE = 1
 MXFP4_COLWISE = 2
@@ -78,6 +78,15 @@ def mxfp4_grouped_gemm(a, a_packed, b, b_packed, offsets, G, c, ldc, M_total, N,
 
 # ------------------------------------------------------ allocating helpers
 
+_ops = None
+
+
+def _load():
+    global _ops
+    _ops = extension()
+    return _ops
+
+
 def quantize(x, rowwise=True, colwise=False, packed=False, index=None, stream=None):
     """MXFP4 copies of a BF16 [R, C] tensor (unit column stride) as a dict.
 
@@ -89,33 +98,7 @@ def quantize(x, rowwise=True, colwise=False, packed=False, index=None, stream=No
     ``moe.dispatch`` name them."""
     if stream is not None:
         return on_stream(stream, (x, index), lambda: quantize(x, rowwise, colwise, packed, index))
-    if not isinstance(x, torch.Tensor) or x.dtype is not torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
-        raise ValueError("x must be a BF16 [rows, cols] tensor with unit column stride")
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA (HIP) tensor, got %s" % x.device)
-    X, C = x.shape
-    dev = x.device
-    R = X
-    if index is not None:
-        if colwise:
-            raise ValueError("index goes with the rowwise copy alone")
-        R = index.numel()
-        need(index, "index", torch.int32, (R,), dev)
-    flags = (MXFP4_ROWWISE if rowwise else 0) | (MXFP4_COLWISE if colwise else 0) | (MXFP4_PACKED_SCALES if packed else 0)
-    out, q, s, qT, sT = {}, None, None, None, None
-    if rowwise:
-        out["q_row"] = q = torch.empty((R, C // 2), dtype=torch.uint8, device=dev)
-        s = (torch.empty((C // 128, R), dtype=torch.int32, device=dev) if packed
-             else torch.empty((R, C // 32), dtype=torch.uint8, device=dev))
-        out["p_row" if packed else "s_row"] = s
-    if colwise:
-        out["q_colT"] = qT = torch.empty((C, R // 2), dtype=torch.uint8, device=dev)
-        sT = (torch.empty((R // 128, C), dtype=torch.int32, device=dev) if packed
-              else torch.empty((C, R // 32), dtype=torch.uint8, device=dev))
-        out["p_colT" if packed else "s_colT"] = sT
-    launch(_functions()["mxfp4_quantize"], "mxfp4_quantize", dev, x.data_ptr(), X, R, C, max(x.stride(0), C),
-           None if index is None else index.data_ptr(), flags, _address(q), _address(s), _address(qT), _address(sT))
-    return out
+    return (_ops or _load()).quantize(x, rowwise, colwise, packed, index)
 
 
 def dequantize(q, scales, out=None, stream=None):
@@ -123,44 +106,7 @@ def dequantize(q, scales, out=None, stream=None):
     [K / 128, R] or scale bytes uint8 [R, K / 32]."""
     if stream is not None:
         return on_stream(stream, (q, scales, out), lambda: dequantize(q, scales, out))
-    if not isinstance(q, torch.Tensor) or q.dim() != 2 or not isinstance(scales, torch.Tensor):
-        raise ValueError("q must be a 2-D tensor of MXFP4 codes, scales a tensor")
-    R, half = q.shape
-    K = 2 * half
-    dev = q.device
-    need(q, "q", torch.uint8, (R, half))
-    packed = scales.dtype is torch.int32
-    if packed:
-        need(scales, "scales", torch.int32, (K // 128, R), dev)
-    else:
-        need(scales, "scales", torch.uint8, (R, K // 32), dev)
-    if out is None:
-        out = torch.empty((R, K), dtype=torch.bfloat16, device=dev)
-    elif out.dtype is not torch.bfloat16 or out.shape != (R, K) or out.stride(1) != 1 or out.device != dev:
-        raise ValueError("out must be a BF16 [R, K] tensor with unit column stride on q's device")
-    launch(_functions()["mxfp4_dequantize"], "mxfp4_dequantize", dev, q.data_ptr(), scales.data_ptr(), R, K,
-           out.data_ptr(), max(out.stride(0), K), MXFP4_PACKED_SCALES if packed else 0)
-    return out
-
-
-def _product(a, a_packed, b, b_packed, b_rows, N, out, accumulate, swiglu):
-    """Checks common to both products; returns M, K, the output and the flags."""
-    M, half = a.shape
-    K = 2 * half
-    dev = a.device
-    need(a, "a", torch.uint8, (M, half))
-    need(a_packed, "a_packed", torch.int32, (K // 128, M), dev)
-    need(b_packed, "b_packed", torch.int32, (K // 128, b_rows), dev)
-    if accumulate:
-        if swiglu:
-            raise ValueError("accumulate and swiglu exclude each other")
-        if out is None:
-            raise ValueError("accumulate=True needs out")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    elif out.dtype is not torch.bfloat16 or out.shape != (M, N) or out.stride(1) != 1 or out.device != dev:
-        raise ValueError("out must be a BF16 [M, N] tensor with unit column stride on the operands' device")
-    return M, K, out, MXFP4_GEMM_ACCUMULATE if accumulate else MXFP4_GEMM_SWIGLU if swiglu else 0
+    return (_ops or _load()).dequantize(q, scales, out)
 
 
 def gemm(a, a_packed, b, b_packed, out=None, accumulate=False, swiglu=False, stream=None):
@@ -171,17 +117,7 @@ def gemm(a, a_packed, b, b_packed, out=None, accumulate=False, swiglu=False, str
     if stream is not None:
         return on_stream(stream, (a, a_packed, b, b_packed, out),
                          lambda: gemm(a, a_packed, b, b_packed, out, accumulate, swiglu))
-    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 2:
-        raise ValueError("a and b must be 2-D tensors of MXFP4 codes")
-    rows = b.shape[0]
-    if swiglu and rows % 2:
-        raise ValueError("swiglu=True needs b with an even number of rows (gate rows, then up rows)")
-    N = rows // 2 if swiglu else rows
-    M, K, c, flags = _product(a, a_packed, b, b_packed, rows, N, out, accumulate, swiglu)
-    need(b, "b", torch.uint8, (rows, K // 2), a.device)
-    launch(_functions()["mxfp4_gemm"], "mxfp4_gemm", a.device, a.data_ptr(), a_packed.data_ptr(), b.data_ptr(),
-           b_packed.data_ptr(), c.data_ptr(), max(c.stride(0), N), M, N, K, flags)
-    return c
+    return (_ops or _load()).gemm(a, a_packed, b, b_packed, out, accumulate, swiglu)
 
 
 def grouped_gemm(a, a_packed, b, b_packed, offsets, out=None, accumulate=False, swiglu=False, stream=None):
@@ -192,15 +128,4 @@ def grouped_gemm(a, a_packed, b, b_packed, offsets, out=None, accumulate=False, 
     if stream is not None:
         return on_stream(stream, (a, a_packed, b, b_packed, offsets, out),
                          lambda: grouped_gemm(a, a_packed, b, b_packed, offsets, out, accumulate, swiglu))
-    if not isinstance(a, torch.Tensor) or a.dim() != 2 or not isinstance(b, torch.Tensor) or b.dim() != 3:
-        raise ValueError("a must be 2-D [M, K / 2] and b 3-D [G, N, K / 2] tensors of MXFP4 codes")
-    G, rows, _ = b.shape
-    if swiglu and rows % 2:
-        raise ValueError("swiglu=True needs experts with an even number of rows (gate rows, then up rows)")
-    N = rows // 2 if swiglu else rows
-    M, K, c, flags = _product(a, a_packed, b, b_packed, G * rows, N, out, accumulate, swiglu)
-    need(b, "b", torch.uint8, (G, rows, K // 2), a.device)
-    need(offsets, "offsets", torch.int32, (G + 1,), a.device)
-    launch(_functions()["mxfp4_grouped_gemm"], "mxfp4_grouped_gemm", a.device, a.data_ptr(), a_packed.data_ptr(),
-           b.data_ptr(), b_packed.data_ptr(), offsets.data_ptr(), G, c.data_ptr(), max(c.stride(0), N), M, N, K, flags)
-    return c
+    return (_ops or _load()).grouped_gemm(a, a_packed, b, b_packed, offsets, out, accumulate, swiglu)
