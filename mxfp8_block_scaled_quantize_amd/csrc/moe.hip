@@ -276,10 +276,12 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, in
       const int g = g0 + l / lg;
       F m1 = -INFINITY, m2 = -INFINITY;
       if (g < a.groups)
+#pragma unroll 4
         for (int i = l % lg; i < a.per; i += lg) {
           const F v = vals[g * a.per + i];
-          if (v > m1) { m2 = m1; m1 = v; }
-          else if (v > m2) m2 = v;
+          const F less = v > m1 ? m1 : v;
+          m1 = v > m1 ? v : m1;
+          m2 = less > m2 ? less : m2;
         }
       for (int d = 1; d < lg; d *= 2) {
         const F o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
@@ -294,6 +296,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, in
     for (int g = l; g < a.groups; g += LPR) {
       const F v = gval[g];
       int rank = 0;
+#pragma unroll 8
       for (int h = 0; h < a.groups; h++) {
         const F o = gval[h];
         rank += o > v || (o == v && h < g);
@@ -486,10 +489,17 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(const typename 
 }
 
 // Lanes per row and experts per lane: the fewest lanes whose registers hold
-// the row (fewer lanes: more rows share a wave's selection rounds).
+// the row (fewer lanes: more rows share a wave's selection rounds), but where a
+// row per wave still leaves SIMDs without one, the most (fewer experts per lane:
+// each round is shorter).
+constexpr int64_t kFewRows = 512;
 #define MOE_ROUTE_SHAPE(CALL)            \
   do {                                   \
-    if (a.E <= 64) CALL(16, 4);          \
+    if (T <= kFewRows && a.E > 64) {     \
+      if (a.E <= 256) CALL(64, 4);       \
+      else if (a.E <= 512) CALL(64, 8);  \
+      else CALL(64, 16);                 \
+    } else if (a.E <= 64) CALL(16, 4);   \
     else if (a.E <= 128) CALL(16, 8);    \
     else if (a.E <= 256) CALL(32, 8);    \
     else if (a.E <= 384) CALL(32, 12);   \
@@ -512,10 +522,10 @@ static RouteArgs route_args(int64_t E, int32_t K, int32_t groups, int32_t top_gr
   return a;
 }
 
-// Whether rows of stride ld and lanes of any VPL (a multiple of 4) can be read
-// in whole vectors: 16 bytes, or the 8 of four two-byte elements.
-static bool wide_rows(const void* p, int64_t ld, int esize, int64_t E) {
-  const int unit = (E > 64 && E <= 256) || E > 384 || esize == 4 ? 16 : 8;
+// Whether rows of stride ld and lanes of vpl (a multiple of 4) can be read in
+// whole vectors: 16 bytes, or the 8 of four two-byte elements.
+static bool wide_rows(const void* p, int64_t ld, int esize, int vpl) {
+  const int unit = esize == 4 ? 16 : vpl % 8 ? 8 : 16;
   return reinterpret_cast<uintptr_t>(p) % unit == 0 && (ld * esize) % unit == 0;
 }
 
@@ -523,11 +533,11 @@ template <typename D>
 static hipError_t route_t(const void* logits, int64_t T, int64_t ld, RouteArgs a, float* weights, int32_t* ids,
                           hipStream_t stream) {
   const auto* x = static_cast<const typename D::T*>(logits);
-  a.wide = wide_rows(logits, ld, sizeof(typename D::T), a.E);
   const bool sure = !a.bias && (a.groups == 1 || a.group_top == 1 || a.per == 1);
 #define MOE_CALL(L, V)                                                                                               \
   do {                                                                                                               \
     const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));                                                 \
+    a.wide = wide_rows(logits, ld, sizeof(typename D::T), V);                                                        \
     if (sure)                                                                                                        \
       hipLaunchKernelGGL((moe_route_kernel<D, L, V, true>), dim3(grid), dim3(256), 0, stream, x, T, ld, a, weights, ids); \
     else                                                                                                             \
@@ -543,11 +553,12 @@ static hipError_t route_back_t(const void* logits, int64_t T, int64_t ld, RouteA
                                const float* dw, void* dlogits, hipStream_t stream) {
   const auto* x = static_cast<const typename D::T*>(logits);
   auto* o = static_cast<typename D::T*>(dlogits);
-  a.wide = wide_rows(logits, ld, sizeof(typename D::T), a.E);
-  const bool wide_out = wide_rows(dlogits, a.E, sizeof(typename D::T), a.E);
 #define MOE_CALL(L, V)                                                                                             \
-  hipLaunchKernelGGL((moe_route_backward_kernel<D, L, V>), dim3((unsigned)((T + 256 / L - 1) / (256 / L))), dim3(256), \
-                     0, stream, x, T, ld, a, ids, dw, o, wide_out)
+  do {                                                                                                             \
+    a.wide = wide_rows(logits, ld, sizeof(typename D::T), V);                                                      \
+    hipLaunchKernelGGL((moe_route_backward_kernel<D, L, V>), dim3((unsigned)((T + 256 / L - 1) / (256 / L))), dim3(256), \
+                       0, stream, x, T, ld, a, ids, dw, o, wide_rows(dlogits, a.E, sizeof(typename D::T), V));    \
+  } while (0)
   MOE_ROUTE_SHAPE(MOE_CALL);
 #undef MOE_CALL
   return hipGetLastError();
@@ -584,10 +595,14 @@ hipError_t launch_moe_route_backward(const void* logits, int dtype, int64_t T, i
 // of waves or workgroups.  Up to kOneBlock slots a single workgroup does it
 // all; beyond that a first launch leaves every run's counts in the workspace
 // and each workgroup of the second adds up what it needs of them (at most 256
-// runs, so that this stays a few hundred KB of L2 reads).
+// runs, so that this stays a few hundred KB of L2 reads).  A few MB at most:
+// latency decides, so ids are loaded four 64-slot pieces at a time and the
+// first batch stays in registers between counting and placing.
 // Ids outside [0, E) are counted as expert E, whose rows come last.
 constexpr int DW = 8;                    // waves
-constexpr int64_t kOneBlock = 4096;
+constexpr int DB = 4;                    // 64-slot pieces in a batch
+constexpr int64_t kRun = 64 * DW * DB;   // slots of a workgroup with one batch a wave
+constexpr int64_t kOneBlock = 2 * kRun;
 constexpr int64_t kMaxRuns = 256;
 
 __device__ __forceinline__ int bucket_of(int id, int E) { return id >= 0 && id < E ? id : E; }
@@ -598,7 +613,14 @@ __global__ __launch_bounds__(64 * DW) void moe_count_kernel(const int32_t* __res
   for (int e = threadIdx.x; e <= E; e += 64 * DW) hist[e] = 0;
   __syncthreads();
   const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
-  for (int64_t i = lo + threadIdx.x; i < hi; i += 64 * DW) atomicAdd(&hist[bucket_of(ids[i], E)], 1);
+  for (int64_t i0 = lo + threadIdx.x; i0 < hi; i0 += kRun) {
+    int id[DB];
+#pragma unroll
+    for (int b = 0; b < DB; b++) id[b] = i0 + 64 * DW * b < hi ? ids[i0 + 64 * DW * b] : 0;
+#pragma unroll
+    for (int b = 0; b < DB; b++)
+      if (i0 + 64 * DW * b < hi) atomicAdd(&hist[bucket_of(id[b], E)], 1);
+  }
   __syncthreads();
   for (int e = threadIdx.x; e <= E; e += 64 * DW) counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
 }
@@ -609,36 +631,68 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
                                                             const int32_t* __restrict__ counts,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ token,
                                                             int32_t* __restrict__ position) {
-  extern __shared__ int32_t next[];   // [DW][E + 1], then [E + 1] first rows of this run
+  // next row of (wave, expert) [DW][E + 1]; of all runs the total and of the
+  // runs before this one the count per expert [E + 1] each
+  extern __shared__ int32_t next[];
   __shared__ int32_t wave_sum[DW];
-  int32_t* const first = next + DW * (E + 1);
+  int32_t* const total = next + DW * (E + 1);
+  int32_t* const before = total + (E + 1);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
-  const int64_t part = run / DW;      // a multiple of 64
+  const int64_t part = run / DW;      // a multiple of a batch
   const int64_t plo = lo + w * part;
   const int64_t phi = plo + part < hi ? plo + part : hi;
-  for (int i = tid; i < DW * (E + 1); i += 64 * DW) next[i] = 0;
+  int first[DB];                      // the wave's first batch
+#pragma unroll
+  for (int b = 0; b < DB; b++) first[b] = plo + 64 * b + lane < phi ? bucket_of(ids[plo + 64 * b + lane], E) : 0;
+  for (int i = tid; i < (DW + 2) * (E + 1); i += 64 * DW) next[i] = 0;
   __syncthreads();
-  for (int64_t i = plo + lane; i < phi; i += 64) atomicAdd(&next[w * (E + 1) + bucket_of(ids[i], E)], 1);
+  if (!ONE) {
+    // threads in groups of a whole number of waves, each for every q-th run
+    const int width = (E + 64) / 64 * 64;
+    const int groups = width <= 64 * DW ? 64 * DW / width : 1;
+    const int q = width <= 64 * DW ? tid / width : 0;
+    if (q < groups)
+      for (int e = tid - q * width; e <= E; e += groups > 1 ? width : 64 * DW) {
+        int32_t all = 0, mine = 0;
+#pragma unroll 8
+        for (int r = q; r < runs; r += groups) {
+          const int32_t c = counts[(int64_t)r * (E + 1) + e];
+          all += c;
+          mine += r < (int)blockIdx.x ? c : 0;
+        }
+        atomicAdd(&total[e], all);
+        atomicAdd(&before[e], mine);
+      }
+  }
+  int32_t* const row = next + w * (E + 1);
+  for (int64_t i0 = plo; i0 < phi; i0 += 64 * DB) {
+    int id[DB];
+#pragma unroll
+    for (int b = 0; b < DB; b++) {
+      const int64_t i = i0 + 64 * b + lane;
+      id[b] = i0 == plo ? first[b] : i < phi ? bucket_of(ids[i], E) : 0;
+    }
+#pragma unroll
+    for (int b = 0; b < DB; b++)
+      if (i0 + 64 * b + lane < phi) atomicAdd(&row[id[b]], 1);
+  }
   __syncthreads();
-  // totals of all runs, scanned over the experts; 64 * DW experts at a time
+  // scan of the totals over the experts, 64 * DW at a time; then the first row
+  // of every wave
   int32_t carry = 0;
   for (int e0 = 0; e0 <= E; e0 += 64 * DW) {
     const int e = e0 + tid;
-    int32_t total = 0, before = 0;
+    int32_t here[DW], all = 0;
     if (e <= E) {
-      if (ONE) {
-        for (int v = 0; v < DW; v++) total += next[v * (E + 1) + e];
-      } else {
-#pragma unroll 8
-        for (int r = 0; r < runs; r++) {
-          const int32_t c = counts[(int64_t)r * (E + 1) + e];
-          total += c;
-          before += r < (int)blockIdx.x ? c : 0;
-        }
+#pragma unroll
+      for (int v = 0; v < DW; v++) {
+        here[v] = next[v * (E + 1) + e];
+        if (ONE) all += here[v];
       }
+      if (!ONE) all = total[e];
     }
-    int32_t incl = total;
+    int32_t incl = all;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int32_t o = __shfl_up(incl, d, 64);
@@ -646,7 +700,8 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     }
     if (lane == 63) wave_sum[w] = incl;
     __syncthreads();
-    int32_t start = carry + incl - total;
+    int32_t start = carry + incl - all;
+#pragma unroll
     for (int v = 0; v < DW; v++) {
       const int32_t c = wave_sum[v];
       if (v < w) start += c;
@@ -654,45 +709,49 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     }
     if (e <= E) {
       if (blockIdx.x == 0) offsets[e] = start;
-      first[e] = start + before;
+      int32_t at = start + (ONE ? 0 : before[e]);
+#pragma unroll
+      for (int v = 0; v < DW; v++) {
+        next[v * (E + 1) + e] = at;
+        at += here[v];
+      }
     }
     __syncthreads();
   }
-  for (int e = tid; e <= E; e += 64 * DW) {
-    int32_t at = first[e];
-    for (int v = 0; v < DW; v++) {
-      const int32_t c = next[v * (E + 1) + e];
-      next[v * (E + 1) + e] = at;
-      at += c;
+  for (int64_t i0 = plo; i0 < phi; i0 += 64 * DB) {
+    int id[DB];
+    uint64_t same[DB];
+#pragma unroll
+    for (int b = 0; b < DB; b++) {
+      const int64_t i = i0 + 64 * b + lane;
+      id[b] = i0 == plo ? first[b] : i < phi ? bucket_of(ids[i], E) : 0;
+      same[b] = __ballot(i < phi);
     }
-  }
-  __syncthreads();
-  for (int64_t i0 = plo; i0 < phi; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const bool ok = i < phi;
-    const int id = ok ? bucket_of(ids[i], E) : 0;
-    uint64_t same = __ballot(ok);
-    for (int b = 0; b < bits; b++) {
-      const uint64_t m = __ballot((id >> b) & 1);
-      same &= ((id >> b) & 1) ? m : ~m;
+    for (int bit = 0; bit < bits; bit++)
+#pragma unroll
+      for (int b = 0; b < DB; b++) {
+        const uint64_t m = __ballot((id[b] >> bit) & 1);
+        same[b] &= ((id[b] >> bit) & 1) ? m : ~m;
+      }
+#pragma unroll
+    for (int b = 0; b < DB; b++) {
+      const int64_t i = i0 + 64 * b + lane;
+      if (i < phi) {
+        const int32_t at = row[id[b]] + __popcll(same[b] & (((uint64_t)1 << lane) - 1));
+        // i < 2^31
+        token[at] = id[b] < E ? (int32_t)((uint32_t)i / (uint32_t)top_k) : -1;
+        position[i] = id[b] < E ? at : -1;
+        if ((same[b] >> lane) == 1) row[id[b]] = at + 1;   // the last lane of this id
+      }
+      wave_lds_fence();
     }
-    if (ok) {
-      const int32_t at = next[w * (E + 1) + id];
-      const int rank = __popcll(same & (((uint64_t)1 << lane) - 1));
-      const int32_t row = at + rank;
-      // the slots before i: i / top_k, in 32 bits (n < 2^31)
-      token[row] = id < E ? (int32_t)((uint32_t)i / (uint32_t)top_k) : -1;
-      position[i] = id < E ? row : -1;
-      if ((same >> lane) == 1) next[w * (E + 1) + id] = row + 1;   // the last lane of this id
-    }
-    wave_lds_fence();
   }
 }
 
+// Slots of a workgroup: one batch a wave, more batches beyond kMaxRuns runs.
 static int64_t dispatch_run(int64_t n) {
   if (n <= kOneBlock) return kOneBlock;
-  const int64_t r = ((n + kMaxRuns - 1) / kMaxRuns + 64 * DW - 1) / (64 * DW) * (64 * DW);
-  return r > kOneBlock ? r : kOneBlock;
+  return ((n + kMaxRuns - 1) / kMaxRuns + kRun - 1) / kRun * kRun;
 }
 
 size_t moe_dispatch_workspace(int64_t n, int64_t E) {
@@ -707,8 +766,8 @@ hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t
   while ((1ll << bits) <= E) bits++;   // ids 0 .. E
   const int64_t run = dispatch_run(n);
   const int runs = n <= kOneBlock ? 1 : (int)((n + run - 1) / run);
-  const size_t lds = (size_t)(DW + 1) * (size_t)(E + 1) * 4u;
-  if (runs == 1) {
+  const size_t lds = (size_t)(DW + 2) * (size_t)(E + 1) * 4u;   // at most 41 KB
+  if (n <= kOneBlock) {
     hipLaunchKernelGGL((moe_place_kernel<true>), dim3(1), dim3(64 * DW), lds, stream, ids, n, run, (int)E, top_k, bits, 1,
                        nullptr, offsets, token, position);
     return hipGetLastError();
