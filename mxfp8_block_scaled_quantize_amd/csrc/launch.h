@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mx {
 
 int64_t quantize_row_tiles(int64_t R);
@@ -88,8 +90,12 @@ struct Mx4Gemm {
 };
 bool mx4_gemm_grid_fits(const Mx4Gemm& g);
 hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream);
+enum class Mx4Tile { kRows, k64x64, k64x128, k128x128, k256x256 };   // rows: the kernel for few rows
 bool mx4_gemm_tile_fits(const Mx4Gemm& g);
 hipError_t launch_mx4_gemm_tile(const Mx4Gemm& g, hipStream_t stream);
+bool mx4_gemm_mid_fits(const Mx4Gemm& g);
+hipError_t launch_mx4_gemm_mid(const Mx4Gemm& g, Mx4Tile tile, hipStream_t stream);
+hipError_t allow_dynamic_lds(const void* kernel, int bytes, std::atomic<uint64_t>* done, hipStream_t stream);
 
 // ---- mixture of experts (sizes as checked by the C ABI of include/moe.h)
 bool moe_route_grid_fits(int64_t T);

@@ -7,20 +7,13 @@
 // block), and supplies that block's scale byte.  Result register i of lane l is
 // row 4 (l / 16) + i of the first operand, row l % 16 of the second.  The
 // kernels pass B first: a lane holds four consecutive columns of one row of C.
-#include "mx_device.h"
 #include "launch.h"
+#include "mx4_gemm.h"
 
 namespace mx {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
+using namespace mx4;
 typedef float v4f __attribute__((ext_vector_type(4)));
-
-__device__ __forceinline__ v8i fp4_operand(u32x4 d) {   // an FP4 operand takes the low four registers
-  v8i r;
-  r.lo = __builtin_bit_cast(v4i, d);
-  return r;
-}
 
 // Rows [lo, hi) of group g: e_i = max over j <= i of offsets[j] clamped into
 // [0, M]; every wave of the workgroup computes the same.
@@ -126,7 +119,7 @@ __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(const uint8_t* __
 #pragma unroll
             for (int j = 0; j < NB; j++)
               acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                  fp4_operand(b[u][j]), fp4_operand(a[u]), acc[i][j], 4, 4, 0, (int)(sb[u][j] >> (8 * kg)), 0,
+                  operand(b[u][j]), operand(a[u]), acc[i][j], 4, 4, 0, (int)(sb[u][j] >> (8 * kg)), 0,
                   (int)(sa[u] >> (8 * kg)));
           }
       }
@@ -174,23 +167,101 @@ static hipError_t launch_rows(const Mx4Gemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Rows of a group on average (dense: all rows).
-static int64_t rows_per_group(const Mx4Gemm& g) { return g.offsets ? (g.M + g.G - 1) / g.G : g.M; }
-static bool few_rows(const Mx4Gemm& g) { return rows_per_group(g) <= 256; }
+// ---- choice of the kernel.  Every variant was timed over M x N (1 .. 4096
+// rows, 512 .. 14336 columns) and over ragged groups, K 512 .. 8192, as launches
+// in a graph.  A tile's time follows
+//   K steps * max(one workgroup's time for a step,
+//                 a full compute unit's time for it * tiles / 256),
+// or that of reading B where it is longer, and the variant with the smallest
+// estimate is taken.  In microseconds for a 256-element step (latency / share):
+// 64 x 64 0.38 / 0.28, 64 x 128 0.54 / 0.47, 128 x 128 0.77 / 0.68, 256 x 256
+// 1.35 / 2.2 in whole rounds of 256 tiles.  E.g. K = 4096, 512 x 4096: 11 us
+// with 64 x 64 (512 tiles), 15 with 128 x 128, 24 with 256 x 256, 26 with the
+// few-rows kernel; 4096 x 4096: 71, 45, 38 and over 200.  The few-rows kernel
+// (16 MB rows x 32 columns a workgroup) takes per 256 workgroups a part for the
+// columns and one that grows with the rows in a block: 128 rows x 1024 columns
+// 5.3 us, 8.3 with 64 x 64.  It streams B faster too (32 experts of 2048 x 4096,
+// one row each: 20 us, 28 with 64 x 128).
+struct Choice {
+  Mx4Tile tile;
+  int mb;   // few rows: blocks of 16 rows
+};
 
-bool mx4_gemm_grid_fits(const Mx4Gemm& g) { return few_rows(g) ? grid_fits(g.M + g.G, g.N / 16, 256) : mx4_gemm_tile_fits(g); }
+static Choice choose(const Mx4Gemm& g) {
+  const bool sw = g.epilogue == EPI_SWIGLU;
+  const double groups = g.offsets ? g.G : 1;
+  const double rows = (double)g.M / groups;   // of a group, on average
+  const double n = sw ? 2 * (double)g.N : (double)g.N;
+  // workgroups per compute unit.  Ragged groups end half a block early on
+  // average; the few-rows kernel, whose workgroup goes through all blocks of
+  // its group, waits for the largest ones (`spread`).
+  auto blocks = [&](int bm, int bn, int spread = 1) {
+    double down = g.offsets ? spread * rows / bm + 0.5 : (double)((g.M + bm - 1) / bm);
+    if (down < 1) down = 1;
+    return groups * down * (double)(int64_t)((n + bn - 1) / bn) / 256;
+  };
+  const double steps = (double)((g.K + 255) / 256), k = steps / 16;
+  const double b_bytes = groups * n * (double)g.K * 17 / 32;
+  Choice best{Mx4Tile::k256x256, 0};
+  double least = 1e30;
+  auto offer = [&](Mx4Tile tile, int mb, double work, double read) {
+    const double us = work > read ? work : read;
+    if (us < least) {
+      least = us;
+      best = Choice{tile, mb};
+    }
+  };
+  const double few[3][4] = {{0.45, 1.85, 0.75, -0.15}, {0.55, 1.7, 0.78, 0.77}, {0.75, 1.65, 2.6, 4.0}};
+  for (int i = 0; i < 3; i++) {
+    const int bm = 16 << i;
+    if (g.offsets || (g.M + bm - 1) / bm <= 65535) {   // the grid's second dimension
+      const double b = blocks(bm, 32, 2), fill = rows < bm ? rows / bm : 1;
+      const double* f = few[i];
+      offer(Mx4Tile::kRows, 1 << i, (f[0] + f[1] * k + fill * (f[2] + f[3] * k)) * (b > 1 ? b : 1), b_bytes / 6.5e6);
+    }
+  }
+  auto tiled = [&](Mx4Tile tile, double latency, double share, double b) {
+    offer(tile, 0, steps * (latency > share * b ? latency : share * b), b_bytes / 5.2e6);
+  };
+  if (mx4_gemm_mid_fits(g)) {
+    if (!sw) tiled(Mx4Tile::k64x64, 0.38, 0.28, blocks(64, 64));
+    tiled(Mx4Tile::k64x128, 0.54, 0.47, blocks(64, 128));
+    tiled(Mx4Tile::k128x128, 0.77, 0.68, blocks(128, 128));
+  }
+  if (mx4_gemm_tile_fits(g)) {
+    const double b = blocks(256, 256);
+    tiled(Mx4Tile::k256x256, 1.35, 2.2, b <= 1 ? b : g.offsets ? b + 0.25 : (double)(int64_t)(b + 0.999));
+  }
+  return best;
+}
+
+bool mx4_gemm_grid_fits(const Mx4Gemm& g) {
+  // a grid's dimensions are limited one by one: 2^32 - 1 work-items, 65535 workgroups of the second
+  return choose(g).tile != Mx4Tile::kRows || (grid_fits(g.N / 16, 1, 512) && (g.offsets || (g.M + 15) / 16 <= 65535));
+}
+
+template <int MB, int W, bool GROUPED>
+static hipError_t launch_rows_e(const Mx4Gemm& g, hipStream_t stream) {
+  return g.epilogue == EPI_SWIGLU ? launch_rows<MB, 2, W, GROUPED, EPI_SWIGLU>(g, stream)
+       : g.epilogue == EPI_ACC   ? launch_rows<MB, 2, W, GROUPED, EPI_ACC>(g, stream)
+                                 : launch_rows<MB, 2, W, GROUPED, EPI_NONE>(g, stream);
+}
+template <int MB>
+static hipError_t launch_rows_w(const Mx4Gemm& g, hipStream_t stream) {
+  // eight waves where K is long enough to be split and workgroups are few (one
+  // row x 2048 columns, K = 8192: 6.3 us, with four waves 6.8; K = 1024, 256 x
+  // 4096: 10.4 and 9.8; 32 experts of 2048 x 4096: 23 and 20)
+  const int64_t tn = g.N / (g.epilogue == EPI_SWIGLU ? 16 : 32);
+  const int64_t groups = g.offsets ? g.G : (g.M + 16 * MB - 1) / (16 * MB);
+  if (g.K >= 2048 && tn * groups < 1024) return g.offsets ? launch_rows_e<MB, 8, true>(g, stream) : launch_rows_e<MB, 8, false>(g, stream);
+  return g.offsets ? launch_rows_e<MB, 4, true>(g, stream) : launch_rows_e<MB, 4, false>(g, stream);
+}
 
 hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream) {
-  if (!few_rows(g)) return launch_mx4_gemm_tile(g, stream);
-  const bool grouped = g.offsets != nullptr;
-  if (grouped) {
-    if (g.epilogue == EPI_SWIGLU) return launch_rows<2, 2, 4, true, EPI_SWIGLU>(g, stream);
-    if (g.epilogue == EPI_ACC) return launch_rows<2, 2, 4, true, EPI_ACC>(g, stream);
-    return launch_rows<2, 2, 4, true, EPI_NONE>(g, stream);
-  }
-  if (g.epilogue == EPI_SWIGLU) return launch_rows<2, 2, 4, false, EPI_SWIGLU>(g, stream);
-  if (g.epilogue == EPI_ACC) return launch_rows<2, 2, 4, false, EPI_ACC>(g, stream);
-  return launch_rows<2, 2, 4, false, EPI_NONE>(g, stream);
+  const Choice c = choose(g);
+  if (c.tile == Mx4Tile::k256x256) return launch_mx4_gemm_tile(g, stream);
+  if (c.tile != Mx4Tile::kRows) return launch_mx4_gemm_mid(g, c.tile, stream);
+  return c.mb == 1 ? launch_rows_w<1>(g, stream) : c.mb == 2 ? launch_rows_w<2>(g, stream) : launch_rows_w<4>(g, stream);
 }
 
 }  // namespace mx

@@ -23,24 +23,16 @@
 //
 // Rows past the end of an operand read as zero (buffer range check), results
 // past the end are not stored.
-#include <atomic>
-
-#include "mx_device.h"
 #include "launch.h"
+#include "mx4_gemm.h"
 
 namespace mx {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(3))) uint8_t lds_u8;
-typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+using namespace mx4;
 
 namespace {
 
 constexpr int TM = 256, TNB = 256;               // rows of A and of B in a tile
-constexpr int STEP = 128;                        // bytes of a row in a step
 constexpr int A_BYTES = TM * STEP, B_BYTES = TNB * STEP;
 constexpr int SA_OFF = A_BYTES + B_BYTES;        // two words for each of 256 rows
 constexpr int SB_OFF = SA_OFF + 2 * TM * 4;
@@ -50,29 +42,6 @@ constexpr int C_STRIDE = 2 * TNB + 16;           // staged BF16 output row
 constexpr int SW_COLS = 128;                     // SwiGLU: output columns of a tile
 constexpr int SW_STRIDE = 2 * SW_COLS + 16;
 static_assert(TM * C_STRIDE <= LDS_BYTES && LDS_BYTES <= 160 * 1024, "LDS");
-constexpr int GROUP = 4;                         // tiles that share an operand in an XCD's L2
-constexpr uint32_t RSRC_FLAGS = 0x00020000u;     // raw buffer, 32-bit data
-constexpr uint32_t HOLE = 0x40000000u;           // past every buffer (at most 2^29 bytes)
-
-template <int N>
-__device__ __forceinline__ void wait_vm() {
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-template <int V>
-struct ic {
-  static constexpr int value = V;
-};
-__device__ __forceinline__ v8i operand(u32x4 d) {
-  v8i r;
-  r.lo = __builtin_bit_cast(v4i, d);
-  return r;
-}
 
 }  // namespace
 
@@ -91,73 +60,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
   const int wm = wave >> 1, wn = wave & 1;
   const int64_t Kb = K / 2;
 
-  // Workgroup ids are dealt to the 8 XCDs in turn: each XCD gets a contiguous
-  // range of tiles, walked in groups of GROUP tiles along the larger side
-  // (grouped: along N, so that an expert's B is read once).
-  const int64_t nblk = tiles_m * tiles_n;
-  const int64_t bid = blockIdx.x;
-  const int64_t full = (nblk / 8) * 8;
-  const int64_t lid = bid < full ? (bid & 7) * (full >> 3) + (bid >> 3) : bid;
   int64_t tm, tn;
-  if (!(GROUPED || tiles_n > tiles_m)) {
-    const int64_t per = (int64_t)GROUP * tiles_n;
-    const int64_t first = lid / per * GROUP;
-    const int64_t n = (tiles_m - first) < GROUP ? (tiles_m - first) : GROUP;
-    const int64_t rem = lid % per;
-    tm = first + rem % n;
-    tn = rem / n;
-  } else {
-    const int64_t per = (int64_t)GROUP * tiles_m;
-    const int64_t first = lid / per * GROUP;
-    const int64_t n = (tiles_n - first) < GROUP ? (tiles_n - first) : GROUP;
-    const int64_t rem = lid % per;
-    tn = first + rem % n;
-    tm = rem / n;
-  }
-
+  tile_of_block<GROUPED>(tiles_m, tiles_n, &tm, &tn);
   int64_t m_lo = tm * TM, m_hi = M, b_row0 = 0;
   if (GROUPED) {
-    // Row tile tm among the groups' tiles, 64 groups at a time: bounds clamped
-    // into [0, M] and raised to the running maximum, a prefix sum of the tile
-    // counts, and the lane whose range holds tm.
-    int found = -1;
-    int carry = 0;
-    for (int g0 = 0; g0 < G; g0 += 64) {
-      const int g = g0 + lane;
-      int lo = 0, hi = 0;
-      if (g < G) {
-        const int64_t l = offsets[g], h = offsets[g + 1];
-        lo = (int)(l < 0 ? 0 : (l > M ? M : l));
-        hi = (int)(h < 0 ? 0 : (h > M ? M : h));
-      }
-      lo = lo > carry ? lo : carry;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int t = __shfl_up(lo, d, 64);
-        if (lane >= d) lo = lo > t ? lo : t;
-      }
-      hi = hi > lo ? hi : lo;
-      carry = __builtin_amdgcn_readlane(hi, 63);
-      const int nt = (hi - lo + TM - 1) / TM;
-      int incl = nt;
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int t = __shfl_up(incl, d, 64);
-        if (lane >= d) incl += t;
-      }
-      const int total = __builtin_amdgcn_readlane(incl, 63);
-      if (tm < total) {
-        const int fl = __builtin_ctzll(__ballot(incl > tm));
-        const int before = __builtin_amdgcn_readlane(incl - nt, fl);
-        found = g0 + fl;
-        m_lo = (int64_t)__builtin_amdgcn_readlane(lo, fl) + (tm - before) * TM;
-        m_hi = (int64_t)__builtin_amdgcn_readlane(hi, fl);
-        break;
-      }
-      tm -= total;
-    }
-    if (found < 0) return;   // the whole workgroup
-    b_row0 = (int64_t)found * N * BMUL;
+    const int g = group_of_tile<TM>(offsets, G, M, tm, &m_lo, &m_hi);
+    if (g < 0) return;   // the whole workgroup
+    b_row0 = (int64_t)g * N * BMUL;
   }
   const int64_t n0 = tn * (SW ? SW_COLS : TNB);
   const int64_t brows = (GROUPED ? (int64_t)G : 1) * N * BMUL;
@@ -360,7 +269,6 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
   // over the main loop.
   const int el = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
   const bool full_rows = m_lo + TM <= m_hi;
-  typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
   if constexpr (SW) {
     // blocks j = 0, 1 hold the gate and j + 2 the up sums of the same columns
 #pragma unroll
@@ -374,10 +282,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
           float v[4];
 #pragma unroll
           for (int t = 0; t < 4; t++) v[t] = silu_f32(acc[i][j][4 * g + t]) * acc[i][j + 2][4 * g + t];
-          const bf16x2 h0 = {(__bf16)v[0], (__bf16)v[1]};
-          const bf16x2 h1 = {(__bf16)v[2], (__bf16)v[3]};
-          *(lds_u32x2*)(smem + row * SW_STRIDE + 2 * col) =
-              u32x2{__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
+          *(lds_u32x2*)(smem + row * SW_STRIDE + 2 * col) = bf16x4(v);
         }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -408,7 +313,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
       if (col < N && r < m_hi) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(C + r * ldc + col));
     }
 #pragma unroll
-    for (int k = 0; k < 32; k++) *(__attribute__((address_space(3))) u32x4*)(smem + (row0 + 8 * k) * C_STRIDE + 16 * ch) = v[k];
+    for (int k = 0; k < 32; k++) *(lds_u32x4*)(smem + (row0 + 8 * k) * C_STRIDE + 16 * ch) = v[k];
     wait_lds();
     barrier();
   }
@@ -428,9 +333,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
 #pragma unroll
           for (int t = 0; t < 4; t++) v[t] += bf16_half2(o, t);
         }
-        const bf16x2 h0 = {(__bf16)v[0], (__bf16)v[1]};
-        const bf16x2 h1 = {(__bf16)v[2], (__bf16)v[3]};
-        *p = u32x2{__builtin_bit_cast(uint32_t, h0), __builtin_bit_cast(uint32_t, h1)};
+        *p = bf16x4(v);
       }
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -456,29 +359,33 @@ static int64_t tiles_n(const Mx4Gemm& g) { return (g.N + tile_cols(g) - 1) / til
 static int64_t tiles_m(const Mx4Gemm& g) { return (g.M + TM - 1) / TM + (g.offsets ? g.G : 0); }
 bool mx4_gemm_tile_fits(const Mx4Gemm& g) { return grid_fits(tiles_m(g), tiles_n(g), 256); }
 
-template <bool GROUPED, int EPI>
-static hipError_t launch_tile(const Mx4Gemm& g, hipStream_t stream) {
-  // More than 64 KB of dynamic LDS has to be asked for, once per device (the
-  // stream's, made current for it).
-  static std::atomic<uint64_t> done{0};
+// More than 64 KB of dynamic LDS has to be asked for, once per kernel and device
+// (the stream's, made current for it); `done` holds a bit per device below 64.
+hipError_t allow_dynamic_lds(const void* kernel, int bytes, std::atomic<uint64_t>* done, hipStream_t stream) {
   int dev = 0;
   hipError_t e = stream ? hipStreamGetDevice(stream, &dev) : hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
-  if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-    int cur = 0;
-    e = hipGetDevice(&cur);
-    if (e != hipSuccess) return e;
-    if (cur != dev && (e = hipSetDevice(dev)) != hipSuccess) return e;
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx4_gemm_tile_kernel<GROUPED, EPI>),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
-    if (cur != dev) {
-      const hipError_t back = hipSetDevice(cur);
-      if (e == hipSuccess) e = back;
-    }
-    if (e != hipSuccess) return e;
-    done.fetch_or(bit, std::memory_order_release);
+  if (bit && (done->load(std::memory_order_acquire) & bit)) return hipSuccess;
+  int cur = 0;
+  e = hipGetDevice(&cur);
+  if (e != hipSuccess) return e;
+  if (cur != dev && (e = hipSetDevice(dev)) != hipSuccess) return e;
+  e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (cur != dev) {
+    const hipError_t back = hipSetDevice(cur);
+    if (e == hipSuccess) e = back;
   }
+  if (e == hipSuccess) done->fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+template <bool GROUPED, int EPI>
+static hipError_t launch_tile(const Mx4Gemm& g, hipStream_t stream) {
+  static std::atomic<uint64_t> done{0};
+  const hipError_t e =
+      allow_dynamic_lds(reinterpret_cast<const void*>(&mx4_gemm_tile_kernel<GROUPED, EPI>), LDS_BYTES, &done, stream);
+  if (e != hipSuccess) return e;
   const int64_t tm = tiles_m(g), tn = tiles_n(g);
   hipLaunchKernelGGL((mx4_gemm_tile_kernel<GROUPED, EPI>), dim3((unsigned)(tm * tn)), dim3(256), LDS_BYTES, stream, g.a, g.ap,
                      g.b, g.bp, g.c, g.ldc, g.M, g.N, g.K, g.offsets, g.G, tm, tn);
