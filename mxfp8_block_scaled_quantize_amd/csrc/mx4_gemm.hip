@@ -211,8 +211,8 @@ static Choice choose(const Mx4Gemm& g) {
       best = Choice{tile, mb};
     }
   };
-  const double few[3][4] = {{0.45, 1.85, 0.75, -0.15}, {0.55, 1.7, 0.78, 0.77}, {0.75, 1.65, 2.6, 4.0}};
-  for (int i = 0; i < 3; i++) {
+  const double few[2][4] = {{0.45, 1.85, 0.75, -0.15}, {0.55, 1.7, 0.78, 0.77}};
+  for (int i = 0; i < 2; i++) {
     const int bm = 16 << i;
     if (g.offsets || (g.M + bm - 1) / bm <= 65535) {   // the grid's second dimension
       const double b = blocks(bm, 32, 2), fill = rows < bm ? rows / bm : 1;
@@ -261,7 +261,7 @@ hipError_t launch_mx4_gemm(const Mx4Gemm& g, hipStream_t stream) {
   const Choice c = choose(g);
   if (c.tile == Mx4Tile::k256x256) return launch_mx4_gemm_tile(g, stream);
   if (c.tile != Mx4Tile::kRows) return launch_mx4_gemm_mid(g, c.tile, stream);
-  return c.mb == 1 ? launch_rows_w<1>(g, stream) : c.mb == 2 ? launch_rows_w<2>(g, stream) : launch_rows_w<4>(g, stream);
+  return c.mb == 1 ? launch_rows_w<1>(g, stream) : launch_rows_w<2>(g, stream);
 }
 
 }  // namespace mx

@@ -128,7 +128,9 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, c10::Device device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(device));
 }
 void* stream_of(c10::Device d) { return c10::hip::getCurrentHIPStream(d.index()).stream(); }
-int64_t ld(const Tensor& t) { return std::max(t.stride(0), t.size(1)); }   // rows of a matrix with unit column stride
+// Stride between the rows of a matrix with unit column stride; of one row it
+// says nothing.  Rows that overlap (expanded ones) are refused by the C ABI.
+int64_t ld(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject* pair(Tensor a, Tensor b) {
   PyObject* r = PyTuple_New(2);

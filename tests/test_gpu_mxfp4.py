@@ -184,6 +184,33 @@ def test_gemm(M, N, K, mode):
     _close(bf16_to_f64(got), want, err, "M=%d N=%d K=%d %s" % (M, N, K, mode))
 
 
+# Enough tiles for the larger ones: 64 x 128, 128 x 128 and 256 x 256, with ends
+# inside a tile, half steps of K and a single one.
+LARGE = [(1100, 2080, 256), (1300, 3104, 384), (2100, 2080, 640), (3000, 4128, 128), (4000, 2080, 384)]
+
+
+@pytest.mark.parametrize("M,N,K", LARGE)
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_gemm_of_many_tiles(M, N, K, mode):
+    test_gemm(M, N, K, mode)
+
+
+def test_gemm_is_the_same_for_every_tile_choice():
+    """Rows of a product do not depend on how many rows there are: the codes'
+    products and 32-element sums are exact, only their fp32 order differs."""
+    torch, mxfp4 = _mxfp4()
+    rng = np.random.default_rng(12)
+    N, K = 1056, 2048
+    a, sa, va = ref.random_operand(rng, 3000, K)
+    b, sb, vb = ref.random_operand(rng, N, K)
+    want, err = _bounds(va, vb)
+    bd, pb = to_dev(b), _words(ref.pack(sb))
+    for M in (1, 15, 16, 31, 33, 64, 127, 200, 255, 257, 640, 1111, 3000):
+        log("mxfp4 gemm of the first %d rows" % M)
+        got = mxfp4.gemm(to_dev(a[:M]), _words(ref.pack(sa[:M])), bd, pb)
+        _close(bf16_to_f64(to_host(got)), want[:M], err[:M], "M=%d" % M)
+
+
 COUNTS = [[5], [0, 0, 7, 0], [1, 0, 16, 17, 33, 0, 2, 64], [300, 0, 1, 257, 40], [0] * 65 + [3] + [0] * 4 + [130, 1],
           [700, 600, 0, 513]]
 
@@ -219,6 +246,20 @@ def test_grouped_gemm(counts, N, K, mode):
         _close(bf16_to_f64(got[r]), want, err, "group %d" % g)
 
 
+@pytest.mark.parametrize("counts,N,K", [([2500, 0, 1, 1900, 300, 505], 2080, 384), ([5000, 200], 4128, 128), ([17] * 39 + [40], 1056, 384),
+                                        ([0, 4100, 0, 0, 4700, 1], 2080, 384), ([1500, 1003], 1600, 640)],
+                         ids=["6", "2", "40", "6empty", "2b"])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_grouped_gemm_of_many_tiles(counts, N, K, mode):
+    test_grouped_gemm(counts, N, K, mode)
+
+
+def test_grouped_gemm_with_one_group_of_nearly_all_rows():
+    """The choice of kernel goes by the average; the rows may all be one expert's."""
+    test_grouped_gemm([0] * 20 + [900] + [0] * 10 + [1], 288, 640, "plain")
+    test_grouped_gemm([0] * 3 + [700] + [0] * 60, 96, 384, "swiglu")
+
+
 def test_grouped_gemm_invalid_offsets_stay_inside():
     """Bounds are clamped into [0, M] and raised to the largest one before."""
     torch, mxfp4 = _mxfp4()
@@ -234,6 +275,49 @@ def test_grouped_gemm_invalid_offsets_stay_inside():
     for g in range(G):
         r = slice(edges[g], edges[g + 1])
         _close(got[r], *_bounds(va[r], vb[g * N:(g + 1) * N]), "group %d" % g)
+
+
+def test_grouped_gemm_invalid_offsets_with_many_rows():
+    torch, mxfp4 = _mxfp4()
+    for M, N, K, G in ((3000, 1056, 384, 6), (9000, 2080, 384, 6), (700, 96, 256, 6)):
+        rng = np.random.default_rng(M)
+        a, sa, va = ref.random_operand(rng, M, K)
+        b, sb, vb = ref.random_operand(rng, G * N, K)
+        offsets = np.array([-2 ** 31, M // 3, M // 5, M // 2, 2 ** 31 - 1, 7, -1], np.int32)
+        edges = np.maximum.accumulate(np.clip(offsets, 0, M))
+        log("mxfp4 grouped, offsets %s" % offsets)
+        got = bf16_to_f64(to_host(mxfp4.grouped_gemm(to_dev(a), _words(ref.pack(sa)), to_dev(b.reshape(G, N, K // 2)),
+                                                     _words(ref.pack(sb)), to_dev(offsets))))
+        for g in range(G):
+            r = slice(edges[g], edges[g + 1])
+            _close(got[r], *_bounds(va[r], vb[g * N:(g + 1) * N]), "group %d" % g)
+
+
+def test_overlapping_rows_are_refused():
+    torch, mxfp4 = _mxfp4()
+    import mxfp8_block_scaled_quantize_amd as mx
+    from mxfp8_block_scaled_quantize_amd import moe
+    one = torch.ones((1, 256), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(mx.MXFP8Error, match="SHAPE"):
+        mxfp4.quantize(one.expand(64, 256))
+    with pytest.raises(mx.MXFP8Error, match="SHAPE"):
+        moe.route(one.expand(64, 256), 4)
+    position = torch.zeros((2, 4), dtype=torch.int32, device="cuda")
+    with pytest.raises(mx.MXFP8Error, match="SHAPE"):
+        moe.combine(one.expand(64, 256), position, position.float())
+    # one row has no stride to speak of
+    odd = torch.ones((3, 300), dtype=torch.bfloat16, device="cuda").as_strided((1, 256), (3, 1))
+    assert torch.equal(mxfp4.quantize(odd)["q_row"], mxfp4.quantize(one)["q_row"])
+
+
+def test_infinities_and_nan_do_not_fault():
+    torch, mxfp4 = _mxfp4()
+    x = torch.randn((64, 256), device="cuda").bfloat16()
+    x[1, 3], x[2, 40], x[3] = float("inf"), float("nan"), float("-inf")
+    q = mxfp4.quantize(x, colwise=False, packed=True)
+    clean = torch.tensor([r for r in range(64) if r not in (1, 2, 3)], device="cuda")
+    want = mxfp4.quantize(x[clean], packed=True)
+    assert torch.equal(q["q_row"][clean], want["q_row"]) and torch.equal(q["p_row"][:, clean], want["p_row"])
 
 
 def test_gemm_extreme_scales():
