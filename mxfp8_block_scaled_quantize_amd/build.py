@@ -74,7 +74,8 @@ def build(verbose: bool = False) -> str:
         os.replace(tmp, path)
     tmp = TORCH_PATH + ".tmp%d" % os.getpid()
     subprocess.check_call(["g++", "-shared", binding, "-o", tmp, "-L" + HERE, "-lmxfp8", "-L" + os.path.join(_torch_dir(), "lib"),
-                           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip", "-Wl,-rpath,$ORIGIN"])
+                           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip",
+                           "-ltorch_hip", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, TORCH_PATH)
     return LIB_PATH
 

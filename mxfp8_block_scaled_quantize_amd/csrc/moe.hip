@@ -244,7 +244,7 @@ __device__ __forceinline__ bool close_f32(float a, float b) { return a - b <= 4e
 // whether (in F = float) the order of two choices that matter is in doubt.
 // SURE: the order is the logits' own, so nothing is in doubt.
 template <int LPR, int VPL, bool SURE, typename F>
-__device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, int l, char* lds, float* __restrict__ w_out,
+__device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, const float* bias, int l, char* lds, float* __restrict__ w_out,
                                           int32_t* __restrict__ id_out, bool live) {
   typedef typename std::conditional<sizeof(F) == 8 && !SURE, uint64_t, uint32_t>::type Key;
   F* const vals = reinterpret_cast<F*>(lds);                                   // [LPR * VPL]
@@ -261,14 +261,14 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, in
   for (int j = 0; j < VPL; j++) {
     if (e0 + j >= a.E) key[j] = 0;
     else if (SURE || !a.bias) key[j] = key_of(x[j]);
-    else if constexpr (!SURE) key[j] = key_of((F)(s[j] + (F)a.bias[e0 + j]));
+    else if constexpr (!SURE) key[j] = key_of((F)(s[j] + (F)bias[j]));
   }
   if (a.groups > 1) {
     // the value of a group comes from the choices; with group_top 1 and no
     // bias the largest logit says the same
 #pragma unroll
     for (int j = 0; j < VPL; j++)
-      if (e0 + j < a.E) vals[e0 + j] = SURE ? (F)x[j] : a.bias ? (F)(s[j] + (F)a.bias[e0 + j]) : s[j];
+      if (e0 + j < a.E) vals[e0 + j] = SURE ? (F)x[j] : (F)(s[j] + (F)bias[j]);
     wave_lds_fence();
     int lg = 1;   // lanes per group
     while (2 * lg * a.groups <= LPR) lg *= 2;
@@ -392,11 +392,14 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __r
   const bool live = t < T;   // rows past the end repeat the last one and write nothing
   const int64_t tr = live ? t : T - 1;
   float x[VPL];
+  float bias[VPL];   // with the logits, so that one latency covers both
+#pragma unroll
+  for (int j = 0; j < VPL; j++) bias[j] = !SURE && a.bias && l * VPL + j < a.E ? a.bias[l * VPL + j] : 0.0f;
   load_logits<VPL, D>(logits + tr * ld, l * VPL, a.E, a.wide, x);
-  const bool doubt = route_row<LPR, VPL, SURE, float>(a, x, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+  const bool doubt = route_row<LPR, VPL, SURE, float>(a, x, bias, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
   if constexpr (!SURE) {
     if (__any(doubt))
-      route_row<LPR, VPL, SURE, double>(a, x, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+      route_row<LPR, VPL, SURE, double>(a, x, bias, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
   }
 }
 
@@ -655,11 +658,15 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     if (q < groups)
       for (int e = tid - q * width; e <= E; e += groups > 1 ? width : 64 * DW) {
         int32_t all = 0, mine = 0;
-#pragma unroll 8
-        for (int r = q; r < runs; r += groups) {
-          const int32_t c = counts[(int64_t)r * (E + 1) + e];
-          all += c;
-          mine += r < (int)blockIdx.x ? c : 0;
+        for (int r0 = q; r0 < runs; r0 += 32 * groups) {   // 32 loads under one latency
+          int32_t c[32];
+#pragma unroll
+          for (int i = 0; i < 32; i++) c[i] = r0 + i * groups < runs ? counts[(int64_t)(r0 + i * groups) * (E + 1) + e] : 0;
+#pragma unroll
+          for (int i = 0; i < 32; i++) {
+            all += c[i];
+            mine += r0 + i * groups < (int)blockIdx.x ? c[i] : 0;
+          }
         }
         atomicAdd(&total[e], all);
         atomicAdd(&before[e], mine);

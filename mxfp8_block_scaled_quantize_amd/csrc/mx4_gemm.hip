@@ -212,7 +212,7 @@ static Choice choose(const Mx4Gemm& g) {
     }
   };
   const double few[2][4] = {{0.45, 1.85, 0.75, -0.15}, {0.55, 1.7, 0.78, 0.77}};
-  for (int i = 0; i < 2; i++) {
+  for (int i = 1; i >= 0; i--) {   // the larger block where both wait for B: ragged groups pass 16 rows
     const int bm = 16 << i;
     if (g.offsets || (g.M + bm - 1) / bm <= 65535) {   // the grid's second dimension
       const double b = blocks(bm, 32, 2), fill = rows < bm ? rows / bm : 1;

@@ -8,7 +8,7 @@
 // its gradient: 85 -> 48 us a step, of which 42 are PyTorch's engine's own).
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -124,8 +124,10 @@ void need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRe
 }
 
 // ------------------------------------------------------------------- the call
+// From the caching allocator of the current stream, without a round through the
+// dispatcher (0.4 us each).
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, c10::Device device) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(device));
+  return at::detail::empty_cuda(shape, type, device, std::nullopt);
 }
 void* stream_of(c10::Device d) { return c10::hip::getCurrentHIPStream(d.index()).stream(); }
 // Stride between the rows of a matrix with unit column stride; of one row it
