@@ -80,66 +80,70 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
   const int64_t b_base = SW ? b_row0 : b_row0 + n0;
   const int64_t b_span = SW ? 2 * N : (N - n0 < BN ? N - n0 : BN);
   uint32_t off[T::DATA];   // instruction i of a wave: LDS rows 8 (4 i + wave) + lane / 8, A's for i < BM / 32, then B's
-  uint32_t hole[T::DATA];
+  uint32_t hole[BM / 32];  // the second half of a half step, zero in A: set bits push the offset past the buffer
 #pragma unroll
   for (int i = 0; i < T::DATA; i++) {
     const int r = 8 * (4 * i + wave) + (lane >> 3);
     const int c = (lane & 7) ^ ((r >> 1) & 7);
     if (i < BM / 32) {
       off[i] = r < rows_a ? (uint32_t)r * (uint32_t)Kb + 16u * (uint32_t)c : PAST;
-      hole[i] = c >= 4 ? 1u : 0u;   // a half step's second half, zero in A
+      hole[i < BM / 32 ? i : 0] = c >= 4 ? PAST : 0u;
     } else {
       bool ok;
       const int64_t row = b_row(r - BM, &ok);
       off[i] = ok ? (uint32_t)((row - b_base) * Kb) + 16u * (uint32_t)c : PAST;
-      hole[i] = 0u;
     }
   }
-  // Scale instruction i of a wave: 64 words; word t of A's rows, then of B's.
+  // Scale instruction i of a wave: 64 words of one operand and one of its two
+  // words of a step, from words(i) on, two words of K further each step.
   uint32_t soff[T::WORDS];
+  const uint32_t* words[T::WORDS];
+  int64_t stride[T::WORDS];
+  int sbytes[T::WORDS], second[T::WORDS];
 #pragma unroll
   for (int i = 0; i < T::WORDS; i++) {
-    const int at = 64 * (4 * i + wave) + lane;   // word index in the slot's scale area
-    if (at < 2 * BM) {
+    const int first = 64 * (4 * i + wave);   // word index in the slot's scale area, uniform
+    const int at = first + lane;
+    const bool is_a = first < 2 * BM, none = first >= 2 * (BM + BN);
+    if (is_a) {
       const int r = at % BM;
       soff[i] = 4u * (uint32_t)(r < rows_a ? r : rows_a - 1);
+      second[i] = first / BM;
     } else {
       bool ok;
       soff[i] = 4u * (uint32_t)(b_row((at - 2 * BM) % BN, &ok) - b_base);
+      second[i] = (first - 2 * BM) / BN;
     }
+    stride[i] = is_a ? M : brows;
+    words[i] = (is_a ? Ap + m_lo : Bp + b_base) + (none ? 0 : second[i] * stride[i]);
+    sbytes[i] = none ? 0 : is_a ? rows_a * 4 : (int)(b_span * 4);
+    stride[i] = none ? 0 : 2 * stride[i];
   }
   const int nk = (int)((K + 255) / 256);
-  const int words = (int)(K / 128);
   const bool half_end = (K & 128) != 0;
   const __amdgpu_buffer_rsrc_t ra =
       __builtin_amdgcn_make_buffer_rsrc((void*)(A + m_lo * Kb), 0, (int)((int64_t)rows_a * Kb), RSRC_FLAGS);
   const __amdgpu_buffer_rsrc_t rb =
       __builtin_amdgcn_make_buffer_rsrc((void*)(B + b_base * Kb), 0, (int)(uint32_t)(b_span * Kb), RSRC_FLAGS);
-  const __amdgpu_buffer_rsrc_t r_none = __builtin_amdgcn_make_buffer_rsrc((void*)A, 0, 0, RSRC_FLAGS);
-  auto issue = [&](int s) {
-    lds_u8* base = smem + (s % NS) * T::SLOT;
-    const bool valid = s < nk;
-    const int k0 = valid ? s * STEP : 0;
+  auto issue = [&](int s, int slot) {   // in the order of steps
+    lds_u8* base = smem + slot * T::SLOT;
+    const int k0 = s * STEP;
     const bool cut = half_end && s == nk - 1;
+    const uint32_t mask = cut ? 0xFFFFFFFFu : 0u;
 #pragma unroll
     for (int i = 0; i < T::DATA; i++) {
-      const uint32_t o = cut && hole[i] ? PAST : off[i];
       lds_void* to = (lds_void*)(base + 1024 * (4 * i + wave));
-      if (i < BM / 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? ra : r_none, to, 16, o, k0, 0, 0);
-      else __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? rb : r_none, to, 16, o, k0, 0, 0);
+      const uint32_t o = i < BM / 32 ? off[i] | (hole[i < BM / 32 ? i : 0] & mask) : off[i];
+      if (i < BM / 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to, 16, o, k0, 0, 0);
+      else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to, 16, o, k0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < T::WORDS; i++) {
-      const int at = 64 * (4 * i + wave);   // uniform
-      const bool is_a = at < 2 * BM;
-      const int t = 2 * s + (is_a ? at / BM : (at - 2 * BM) / BN);
-      const bool have = t < words && at < 2 * (BM + BN);
-      const int64_t tt = have ? t : 0;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          is_a ? (void*)(Ap + tt * M + m_lo) : (void*)(Bp + tt * brows + b_base), 0,
-          have ? (is_a ? rows_a * 4 : (int)(b_span * 4)) : 0, RSRC_FLAGS);
       const uint32_t o = soff[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + T::SA_OFF + 4 * at), 4, o, 0, 0, 0);
+      const __amdgpu_buffer_rsrc_t r =
+          __builtin_amdgcn_make_buffer_rsrc((void*)words[i], 0, cut && second[i] ? 0 : sbytes[i], RSRC_FLAGS);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(base + T::SA_OFF + 256 * (4 * i + wave)), 4, o, 0, 0, 0);
+      words[i] += stride[i];
     }
   };
 
@@ -155,20 +159,25 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
 #pragma unroll
     for (int j = 0; j < WN; j++) acc[i][j] = v16f{};
 #pragma unroll
-  for (int s = 0; s < NS - 1; s++) issue(s);
-  for (int t = 0; t < nk; t++) {
-    wait_vm<(NS - 2) * T::PIECES>();
+  for (int s = 0; s < NS - 1; s++)
+    if (s < nk) issue(s, s);
+  // Step t in slot u (a constant: every LDS address is a register plus an
+  // immediate).  What the step reads is asked for first, then the loads of the
+  // step NS - 1 further on, into the slot that every wave has left.
+  auto step = [&](int t, auto SL) {
+    constexpr int u = decltype(SL)::value;
+    if (t + NS - 2 < nk) wait_vm<(NS - 2) * T::PIECES>();   // NS - 2 later steps are under way
+    else wait_vm<0>();
     wait_lds();      // this wave's reads of the slot that is filled next
     barrier();
-    issue(t + NS - 1);
-    const lds_u8* base = smem + (t % NS) * T::SLOT;
+    const lds_u8* base = smem + u * T::SLOT;
     uint32_t sa[2][WM], sb[2][WN];
 #pragma unroll
     for (int h = 0; h < 2; h++) {
 #pragma unroll
-      for (int i = 0; i < WM; i++) sa[h][i] = *(lds_u32*)(base + sa_at + 4 * BM * h + 128 * i) >> (8 * lg);
+      for (int i = 0; i < WM; i++) sa[h][i] = *(lds_u32*)(base + sa_at + 4 * BM * h + 128 * i);
 #pragma unroll
-      for (int j = 0; j < WN; j++) sb[h][j] = *(lds_u32*)(base + sb_at + 4 * BN * h + 128 * j) >> (8 * lg);
+      for (int j = 0; j < WN; j++) sb[h][j] = *(lds_u32*)(base + sb_at + 4 * BN * h + 128 * j);
     }
     u32x4 fa[4][WM], fb[4][WN];
 #pragma unroll
@@ -178,6 +187,15 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
       for (int i = 0; i < WM; i++) fa[sl][i] = *(lds_u32x4*)(base + a_row + 32 * STEP * i + p);
 #pragma unroll
       for (int j = 0; j < WN; j++) fb[sl][j] = *(lds_u32x4*)(base + b_rowo + 32 * STEP * j + p);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + NS - 1 < nk) issue(t + NS - 1, (u + NS - 1) % NS);
+#pragma unroll
+    for (int h = 0; h < 2; h++) {
+#pragma unroll
+      for (int i = 0; i < WM; i++) sa[h][i] >>= 8 * lg;
+#pragma unroll
+      for (int j = 0; j < WN; j++) sb[h][j] >>= 8 * lg;
     }
 #pragma unroll
     for (int sl = 0; sl < 4; sl++)
@@ -192,8 +210,17 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
             acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fb[sl][j]), operand(fa[sl][i]), acc[i][j], 4, 4,
                                                                         0, (int)sb[sl >> 1][j], 0, (int)sa[sl >> 1][i]);
         }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int t = 0;
+  for (; t + NS <= nk; t += NS) {
+    step(t, ic<0>{});
+    step(t + 1, ic<1>{});
+    if constexpr (NS > 2) step(t + 2, ic<2>{});
   }
-  wait_vm<0>();   // the tail's empty DMA, before the ring is used again
+  if (t < nk) step(t, ic<0>{});
+  if constexpr (NS > 2)
+    if (t + 1 < nk) step(t + 1, ic<1>{});
   wait_lds();
   barrier();
 
