@@ -174,14 +174,14 @@ static hipError_t launch_rows(const Mx4Gemm& g, hipStream_t stream) {
 //                 a full compute unit's time for it * tiles / 256),
 // or that of reading B where it is longer, and the variant with the smallest
 // estimate is taken.  In microseconds for a 256-element step (latency / share):
-// 64 x 64 0.38 / 0.28, 64 x 128 0.54 / 0.47, 128 x 128 0.77 / 0.68, 256 x 256
-// 1.35 / 2.2 in whole rounds of 256 tiles.  E.g. K = 4096, 512 x 4096: 11 us
-// with 64 x 64 (512 tiles), 15 with 128 x 128, 24 with 256 x 256, 26 with the
-// few-rows kernel; 4096 x 4096: 71, 45, 38 and over 200.  The few-rows kernel
-// (16 MB rows x 32 columns a workgroup) takes per 256 workgroups a part for the
-// columns and one that grows with the rows in a block: 128 rows x 1024 columns
-// 5.3 us, 8.3 with 64 x 64.  It streams B faster too (32 experts of 2048 x 4096,
-// one row each: 20 us, 28 with 64 x 128).
+// 64 x 64 0.27 / 0.25, 64 x 128 0.45 / 0.43, 128 x 128 0.66 / 0.65; 256 x 256
+// 1.3 for a lone tile, 2.2 for a full round of 256.  E.g. K = 4096, 512 x 4096:
+// 10 us with 64 x 64 (512 tiles), 14 with 128 x 128, 24 with 256 x 256, 26 with
+// the few-rows kernel; 4096 x 4096: 60, 43, 38 and over 200.  The few-rows
+// kernel (16 MB rows x 32 columns a workgroup) takes per 256 workgroups a part
+// for the columns and one that grows with the rows in a block: 128 rows x 1024
+// columns 5.3 us, 6.3 with 64 x 64.  It streams B faster too (32 experts of 2048
+// x 4096, one row each: 20 us, 28 with 64 x 128).
 struct Choice {
   Mx4Tile tile;
   int mb;   // few rows: blocks of 16 rows
@@ -224,13 +224,14 @@ static Choice choose(const Mx4Gemm& g) {
     offer(tile, 0, steps * (latency > share * b ? latency : share * b), b_bytes / 5.2e6);
   };
   if (mx4_gemm_mid_fits(g)) {
-    if (!sw) tiled(Mx4Tile::k64x64, 0.38, 0.28, blocks(64, 64));
-    tiled(Mx4Tile::k64x128, 0.54, 0.47, blocks(64, 128));
-    tiled(Mx4Tile::k128x128, 0.77, 0.68, blocks(128, 128));
+    if (!sw) tiled(Mx4Tile::k64x64, 0.27, 0.25, blocks(64, 64));
+    tiled(Mx4Tile::k64x128, 0.45, 0.43, blocks(64, 128));
+    tiled(Mx4Tile::k128x128, 0.66, 0.65, blocks(128, 128));
   }
   if (mx4_gemm_tile_fits(g)) {
     const double b = blocks(256, 256);
-    tiled(Mx4Tile::k256x256, 1.35, 2.2, b <= 1 ? b : g.offsets ? b + 0.25 : (double)(int64_t)(b + 0.999));
+    const double rounds = g.offsets ? b + 0.25 : (double)(int64_t)(b + 0.999);
+    offer(Mx4Tile::k256x256, 0, steps * (b <= 1 ? 1.3 + 0.9 * b : 2.1 * rounds), b_bytes / 5.2e6);
   }
   return best;
 }

@@ -212,7 +212,7 @@ def test_dispatch_all_to_one_expert():
 
 # tokens, rows, top_k, hidden
 COMBINES = [(1, 1, 1, 1), (3, 24, 8, 256), (16, 128, 8, 4096), (5, 12, 2, 100), (70, 700, 9, 264), (33, 99, 3, 1000),
-            (129, 258, 2, 2056), (40, 700, 17, 512), (7, 20, 2, 2049)]
+            (129, 258, 2, 2056), (40, 700, 17, 512), (7, 20, 2, 2049), (1025, 8200, 8, 64), (2050, 5000, 5, 72)]
 
 
 @pytest.mark.parametrize("T,rows,K,H", COMBINES)
