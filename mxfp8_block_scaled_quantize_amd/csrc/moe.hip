@@ -376,8 +376,10 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
 }
 
 // A wave holds 64 / LPR rows.  The choice is made in 32 bits; a wave in which
-// the order of two values is within the rounding (about one row in a thousand
-// with a bias) makes it again in 64.
+// the order of two values is within the rounding (a row in a few hundred with a
+// bias) makes it again in 64.  Bound by the rounds' latency for few rows (16
+// tokens, 256 experts in 8 groups: 5.8 us) and by their instructions for many
+// (16384 tokens, 128 experts, top 8: 7.3 us for 5 MB).
 template <typename D, int LPR, int VPL, bool SURE>
 __global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __restrict__ logits, int64_t T, int64_t ld,
                                                         RouteArgs a, float* __restrict__ weights,
@@ -405,7 +407,9 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __r
 
 // d logits of a row: with g' = dw of the chosen experts (renormalized weights:
 // (g - <g, w>) / total), softmax d_j = s_j (g'_j - <g', s>), sigmoid
-// d_j = g'_j s_j (1 - s_j) with s (1 - s) = e / (1 + e)^2, e = exp(-|x|).
+// d_j = g'_j s_j (1 - s_j) with s (1 - s) = e / (1 + e)^2, e = exp(-|x|).  Who is
+// chosen goes through LDS, so that a lane looks at its own experts alone.  16384
+// tokens, 128 experts: 6.0 us for 9 MB.
 template <typename D, int LPR, int VPL>
 __global__ __launch_bounds__(256) void moe_route_backward_kernel(const typename D::T* __restrict__ logits, int64_t T,
                                                                  int64_t ld, RouteArgs a,
@@ -600,7 +604,10 @@ hipError_t launch_moe_route_backward(const void* logits, int dtype, int64_t T, i
 // and each workgroup of the second adds up what it needs of them (at most 256
 // runs, so that this stays a few hundred KB of L2 reads).  A few MB at most:
 // latency decides, so ids are loaded four 64-slot pieces at a time and the
-// first batch stays in registers between counting and placing.
+// first batch stays in registers between counting and placing.  128 slots: 3.5
+// us; 131064: 2.7 + 7.5 us, of which 2 are the counts of all runs coming back from
+// behind the other XCDs' L2, 1.5 the ranks (two or sixteen waves, 1024 or 4096
+// slots a run: within 5 %).
 // Ids outside [0, E) are counted as expert E, whose rows come last.
 constexpr int DW = 8;                    // waves
 constexpr int DB = 4;                    // 64-slot pieces in a batch
@@ -793,7 +800,7 @@ hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t
 // HBM.  A thread owns 16 bytes of a token's row (VEC; single elements where
 // rows are not 16-byte aligned) and has the loads of eight slots in flight.
 // tpt threads (a power of two, 64 .. 256, so that a wave has one token) share
-// a token.
+// a token.  8191 tokens x 8 x 4096: 107 us for 604 MB, 5.6 TB/s.
 template <typename D, bool VEC>
 __global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* __restrict__ y, int64_t rows, int64_t ldy,
                                                           const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -844,7 +851,7 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* _
 constexpr int64_t kOneCount = 8192;
 __global__ __launch_bounds__(1024) void moe_count_rows_kernel(const int32_t* __restrict__ pos, int n, int rows, int32_t* count) {
   for (int i = threadIdx.x; i < rows; i += 1024) count[i] = 0;
-  __threadfence_block();
+  __threadfence();   // the zeros are in L2, where the atomics work
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += 1024) {
     const int p = pos[i];
@@ -869,7 +876,8 @@ __global__ __launch_bounds__(256) void moe_named_kernel(const int32_t* __restric
 // w * dout; one that several name is summed by the lowest of its slots (which
 // finds the others by going through the positions: right, and slow, for what
 // no dispatch produces).  The workgroups behind the tokens' own zero the rows
-// that nobody names.
+// that nobody names.  8191 tokens x 8 x 4096: 219 us for 1.14 GB, 5.2 TB/s, and
+// 10 us to count who names whom.
 template <typename D, bool VEC, int TPT>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const typename D::T* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ pos,

@@ -3,10 +3,16 @@
 //
 // The same scheme as the large tile (32x32x64 MFMA, B first, 256-element K
 // steps DMAd into LDS, chunks swizzled by (row >> 1) & 7) with BM x BN tiles,
-// 2 x 2 waves of (BM / 2) x (BN / 2), and a ring of NS slots: a step waits for
-// its own slot's loads only, so that NS - 1 steps of loads cover the latency
-// that few waves cannot hide.  Two workgroups or more share a compute unit, and
-// one's epilogue runs beside the other's MFMAs.
+// 2 x 2 waves of (BM / 2) x (BN / 2), and a ring of NS slots, unrolled so that
+// every slot is a constant.  A step waits for its own slot's loads, reads all its
+// fragments, asks for the step NS - 1 further on and multiplies.  Few tiles: the
+// time is the steps' own latency (barrier, LDS reads, MFMA chain: 0.27 us a step
+// of 64 x 64), and two workgroups of a compute unit fill each other's gaps.
+// K = 4096: 512 x 4096 10.0 us with 64 x 64, 1024 x 4096 15.3 with 128 x 128.
+// Measured and not kept: deeper rings (64 x 64 with six slots 8.6 us where three
+// took 8.3; 128 x 128 with four, one workgroup a compute unit, 60 us where two
+// took 45), fragments read one step ahead into a second set of registers (7.1 us
+// where 6.3), 128 x 256 tiles (51 us where 128 x 128 takes 45).
 #include "launch.h"
 #include "mx4_gemm.h"
 
