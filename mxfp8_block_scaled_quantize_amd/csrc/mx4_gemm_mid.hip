@@ -86,14 +86,17 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
   const int64_t b_base = SW ? b_row0 : b_row0 + n0;
   const int64_t b_span = SW ? 2 * N : (N - n0 < BN ? N - n0 : BN);
   uint32_t off[T::DATA];   // instruction i of a wave: LDS rows 8 (4 i + wave) + lane / 8, A's for i < BM / 32, then B's
-  uint32_t hole[BM / 32];  // the second half of a half step, zero in A: set bits push the offset past the buffer
+  // The second half of a half step reads as zero: its lanes' own offsets are put
+  // past the buffer (the range check may leave out the step's scalar offset).
+  // The lane's chunk is the same in every instruction: 32 rows further on the
+  // swizzle repeats.
+  const bool late = ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7)) & 4;
 #pragma unroll
   for (int i = 0; i < T::DATA; i++) {
     const int r = 8 * (4 * i + wave) + (lane >> 3);
     const int c = (lane & 7) ^ ((r >> 1) & 7);
     if (i < BM / 32) {
       off[i] = r < rows_a ? (uint32_t)r * (uint32_t)Kb + 16u * (uint32_t)c : PAST;
-      hole[i < BM / 32 ? i : 0] = c >= 4 ? PAST : 0u;
     } else {
       bool ok;
       const int64_t row = b_row(r - BM, &ok);
@@ -135,11 +138,11 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
     lds_u8* base = smem + slot * T::SLOT;
     const int k0 = s * STEP;
     const bool cut = half_end && s == nk - 1;
-    const uint32_t mask = cut ? 0xFFFFFFFFu : 0u;
+    const bool skip = cut && late;
 #pragma unroll
     for (int i = 0; i < T::DATA; i++) {
       lds_void* to = (lds_void*)(base + 1024 * (4 * i + wave));
-      const uint32_t o = i < BM / 32 ? off[i] | (hole[i < BM / 32 ? i : 0] & mask) : off[i];
+      const uint32_t o = skip ? PAST : off[i];
       if (i < BM / 32) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, to, 16, o, k0, 0, 0);
       else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, to, 16, o, k0, 0, 0);
     }

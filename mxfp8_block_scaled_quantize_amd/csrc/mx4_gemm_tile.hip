@@ -94,7 +94,10 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
     dma_off[i] = (uint32_t)r * (uint32_t)Kb + 16u * (uint32_t)c;
   }
   // Half step: chunks 4 .. 7 lie past the row; of instruction i that is bit 2
-  // of the lane, flipped for odd i.  A's read as zero, so B's do not matter.
+  // of the lane, flipped for odd i.  They read as zero in both operands.  (The
+  // range check may leave out a load's scalar offset, here the step's: what has
+  // to read as zero is past the range by its lane offset alone, and an empty
+  // range goes with a scalar offset of zero.)
   const uint32_t hole_even = (lane & 4) ? HOLE : 0u, hole_odd = (lane & 4) ? 0u : HOLE;
   // Scale words: position p = 128 half + 4 lr + i holds row 128 half + 32 i + lr,
   // so that a lane's four words are one 16-byte read; rows past the end repeat
@@ -116,12 +119,14 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
   const __amdgpu_buffer_rsrc_t ra_v =
       __builtin_amdgcn_make_buffer_rsrc((void*)(A + m_lo * Kb), 0, (int)((int64_t)rows_a * Kb), RSRC_FLAGS);
   __amdgpu_buffer_rsrc_t rb_v;
+  bool have_b = true;   // whether the wave's rows of B begin before its end
   if (SW) {
     // wave w fills rows 64 w .. of the slot: its resource starts 64 w rows
     // before the segment's first row, so that the shared offsets land on it
     const int64_t oc0 = n0 + 64 * (wave >> 1);
     const int64_t seg = N - oc0 < 0 ? 0 : (N - oc0 < 64 ? N - oc0 : 64);
     const int64_t src = b_row0 + (wave & 1) * N + oc0;
+    have_b = seg > 0;
     rb_v = __builtin_amdgcn_make_buffer_rsrc((void*)((uintptr_t)B + (uintptr_t)((src - 64 * wave) * Kb)), 0,
                                              seg ? (int)((64 * wave + seg) * Kb) : 0, RSRC_FLAGS);
   } else {
@@ -136,14 +141,15 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
     lds_u8* base = smem + decltype(SL)::value * SLOT;
     const bool valid = s < nk;
     const int k0 = valid ? s * STEP : 0;
-    if (q < 8) {
+    if (q < 16) {
       const bool cut = half_end && s == nk - 1;
-      const uint32_t off = dma_off[q] + (cut ? ((q & 1) ? hole_odd : hole_even) : 0u);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? ra_v : r_none, (lds_void*)(base + 1024 * (8 * wave + q)), 16, off, k0,
-                                               0, 0);
-    } else if (q < 16) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? rb_v : r_none, (lds_void*)(base + A_BYTES + 1024 * (8 * wave + q - 8)),
-                                               16, dma_off[q - 8], k0, 0, 0);
+      const uint32_t off = dma_off[q & 7] + (cut ? ((q & 1) ? hole_odd : hole_even) : 0u);
+      if (q < 8)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? ra_v : r_none, (lds_void*)(base + 1024 * (8 * wave + q)), 16, off, k0,
+                                                 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(valid ? rb_v : r_none, (lds_void*)(base + A_BYTES + 1024 * (8 * wave + q - 8)),
+                                                 16, off, have_b ? k0 : 0, 0, 0);
     } else {
       const int t = 2 * s + (q & 1);
       const bool have = t < words;
@@ -368,7 +374,10 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
 static int64_t tile_cols(const Mx4Gemm& g) { return g.epilogue == 2 ? SW_COLS : TNB; }
 static int64_t tiles_n(const Mx4Gemm& g) { return (g.N + tile_cols(g) - 1) / tile_cols(g); }
 static int64_t tiles_m(const Mx4Gemm& g) { return (g.M + TM - 1) / TM + (g.offsets ? g.G : 0); }
-bool mx4_gemm_tile_fits(const Mx4Gemm& g) { return grid_fits(tiles_m(g), tiles_n(g), 256); }
+// An expert's scale words (SwiGLU: 2N of them) lie in one buffer of 32-bit offsets.
+bool mx4_gemm_tile_fits(const Mx4Gemm& g) {
+  return (g.epilogue != 2 || g.N < (int64_t(1) << 28)) && grid_fits(tiles_m(g), tiles_n(g), 256);
+}
 
 // More than 64 KB of dynamic LDS has to be asked for, once per kernel and device
 // (the stream's, made current for it); `done` holds a bit per device below 64.
