@@ -155,9 +155,7 @@ __device__ __forceinline__ float exp_of(float x) {
   // h of +-inf (or beyond the range) leaves l undefined: the result is e itself
   return fabsf(h) < 150.0f ? fmaf(e * l, 0.69314718055994531f, e) : e;
 }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
 __device__ __forceinline__ float rcp_of(float x) { return __builtin_amdgcn_rcpf(x); }
-__device__ __forceinline__ double rcp_of(double x) { return 1.0 / x; }
 
 // Order-preserving integers: NaN 2, -inf and up above it, +-0 the same; 1 is
 // left for experts of closed groups and 0 for those that are out.
@@ -173,9 +171,6 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 }
 __device__ __forceinline__ float value_of(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-__device__ __forceinline__ double value_of(uint64_t k) {
-  return __builtin_bit_cast(double, k ^ ((k >> 63) ? 0x8000000000000000ull : ~0ull));
 }
 
 template <int VPL, typename D>
@@ -202,12 +197,12 @@ __device__ __forceinline__ void load_logits(const typename D::T* __restrict__ ro
   }
 }
 
-// Scores in F of the lane's experts (those past E: 0).
-template <int LPR, int VPL, typename F>
-__device__ __forceinline__ void scores_of(const float* x, bool sigmoid, F* s) {
+// Scores of the lane's experts (those past E: 0).
+template <int LPR, int VPL>
+__device__ __forceinline__ void scores_of(const float* x, bool sigmoid, float* s) {
   if (sigmoid) {
 #pragma unroll
-    for (int j = 0; j < VPL; j++) s[j] = rcp_of((F)1 + exp_of(-(F)x[j]));
+    for (int j = 0; j < VPL; j++) s[j] = rcp_of(1.0f + exp_of(-x[j]));
     return;
   }
   float m = x[0];
@@ -215,193 +210,397 @@ __device__ __forceinline__ void scores_of(const float* x, bool sigmoid, F* s) {
   for (int j = 1; j < VPL; j++) m = fmaxf(m, x[j]);
   m = lanes_reduce<LPR>(m, OpMax{});
   if (m == -INFINITY) m = 0.0f;   // a row of -inf alone: every exp is 0
-  F sum = 0;
+  float sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < VPL; j++) {
-    s[j] = exp_of((F)x[j] - (F)m);
+    s[j] = exp_of(x[j] - m);
     sum += s[j];
   }
   sum = lanes_reduce<LPR>(sum, OpAdd{});
-  const F r = sum == (F)0 ? (F)0 : rcp_of(sum);
+  const float r = sum == 0.0f ? 0.0f : rcp_of(sum);
 #pragma unroll
   for (int j = 0; j < VPL; j++) s[j] *= r;
 }
 
-constexpr int kMaxGroups = 64;
+constexpr int kMaxGroups = 64, kMaxTopK = 64;
 
 struct RouteArgs {
   int E, K, groups, top_groups, group_top, per;
-  bool sigmoid, renorm, wide;
+  int group_lanes;   // lanes that hold a group and nothing else (1, 2, 4, 8, 16); 0: groups do not end with lanes
+  bool sigmoid, renorm, wide, wide_bias;
   const float* bias;
 };
 
-// Two values whose 32-bit evaluation may be in the wrong order: their distance
-// is within the error of both.  A score's is below 1e-6 (scores are at most 1),
-// the bias adds half an ulp.
-__device__ __forceinline__ bool close_f32(float a, float b) { return a - b <= 4e-6f * (1.0f + fabsf(a)); }
+// The two largest of a lane's values and of another lane's.
+struct Top2 {
+  float m1, m2;
+  __device__ __forceinline__ void add(float v) {
+    v = v == v ? v : -INFINITY;   // NaN is last
+    m2 = __builtin_amdgcn_fmed3f(m1, m2, v);
+    m1 = fmaxf(m1, v);
+  }
+  __device__ __forceinline__ void merge(float o1, float o2) {
+    m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+    m1 = fmaxf(m1, o1);
+  }
+  template <int CTRL>
+  __device__ __forceinline__ void merge_dpp() {
+    merge(dppx<float, CTRL>(m1), dppx<float, CTRL>(m2));
+  }
+};
 
-// One row on LPR lanes, lane l holding experts l VPL .. + VPL - 1.  Returns
-// whether (in F = float) the order of two choices that matter is in doubt.
-// SURE: the order is the logits' own, so nothing is in doubt.
-template <int LPR, int VPL, bool SURE, typename F>
+// How many of `n` group values (padded with -inf to a multiple of four) come
+// before group g with value v: the larger ones, and equal ones of lower index.
+__device__ __forceinline__ int rank_of(const float* gval, int n, int g, float v) {
+  int rank = 0;
+  for (int h0 = 0; h0 < n; h0 += 4) {
+    const float4 o = *reinterpret_cast<const float4*>(gval + h0);
+    rank += (o.x > v || (o.x == v && h0 < g)) + (o.y > v || (o.y == v && h0 + 1 < g)) +
+            (o.z > v || (o.z == v && h0 + 2 < g)) + (o.w > v || (o.w == v && h0 + 3 < g));
+  }
+  return rank;
+}
+
+// LDS of a row: a score (before that: choice) per expert, then the groups'
+// values and who is open, and in their place the picks.
+template <int LPR, int VPL>
+struct RouteLds {
+  static constexpr int NV = LPR * VPL;
+  static constexpr int PICKS = (kMaxTopK + 2) * 8;
+  static constexpr int ROW = NV * 4 + (PICKS > kMaxGroups * 8 ? PICKS : kMaxGroups * 8);
+  static constexpr int EXACT = NV * 8 + kMaxGroups * 12 + kMaxTopK * 4;   // of a wave that chooses again
+  static constexpr int ROWS = 64 / LPR * ROW;
+  static constexpr int WAVE = ((ROWS > EXACT ? ROWS : EXACT) + 15) / 16 * 16;
+};
+
+// One row on LPR lanes, lane l holding experts l VPL .. + VPL - 1.  SURE: the
+// order is the logits' own.  Else the choice is made in 32 bits, and nothing is
+// written for a row in which two values that matter are closer than what they
+// can be off by (returned for all its lanes):
+//   u = 2^-24.  exp_of is within 4 u of its value, rcp_of within 2 u.
+//   softmax  a score s is within (18 + VPL) u s: 4 u of its own exp, 4 u of the
+//            sum's terms, (VPL + 6) u of adding them up, 3 u of 1 / sum and the
+//            product, and the rounding of x - max, |d| e^-|d| u <= 0.4 u.  The
+//            scores of two experts add up to 1 at most, and to twice the
+//            largest (of two pairs: four times).
+//   sigmoid  e / (1 + e)^2 4 u + 3 u s <= 4 u, two of them 8 u, two pairs 16 u.
+//   each sum with the bias, and of two choices, rounds by u of its value more.
+template <int LPR, int VPL, bool SURE>
 __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, const float* bias, int l, char* lds, float* __restrict__ w_out,
                                           int32_t* __restrict__ id_out, bool live) {
-  typedef typename std::conditional<sizeof(F) == 8 && !SURE, uint64_t, uint32_t>::type Key;
-  F* const vals = reinterpret_cast<F*>(lds);                                   // [LPR * VPL]
-  F* const gval = vals + LPR * VPL;                                            // [64]
-  uint32_t* const keep = reinterpret_cast<uint32_t*>(gval + kMaxGroups);       // [64]
-  F* const picked = vals;                                                      // [64], after the groups are done
-  int32_t* const picked_id = reinterpret_cast<int32_t*>(keep);
+  constexpr float U = 5.9604645e-8f;
+  float* const vals = reinterpret_cast<float*>(lds);                  // [LPR * VPL]
+  float* const gval = vals + LPR * VPL;                               // [64]
+  uint32_t* const keep = reinterpret_cast<uint32_t*>(gval + kMaxGroups);
+  u32x2* const pick = reinterpret_cast<u32x2*>(gval);                 // [66] (expert, key), after the groups are done
   const int e0 = l * VPL;
+  const int seg = (threadIdx.x & 63) & ~(LPR - 1);
   bool doubt = false;
-  F s[VPL];
-  scores_of<LPR, VPL, F>(x, a.sigmoid, s);
-  Key key[VPL];
+  float s[VPL], v[VPL];
+  scores_of<LPR, VPL>(x, a.sigmoid, s);
+  uint32_t key[VPL];
 #pragma unroll
   for (int j = 0; j < VPL; j++) {
-    if (e0 + j >= a.E) key[j] = 0;
-    else if (SURE || !a.bias) key[j] = key_of(x[j]);
-    else if constexpr (!SURE) key[j] = key_of((F)(s[j] + (F)bias[j]));
+    v[j] = SURE ? x[j] : s[j] + bias[j];
+    key[j] = e0 + j >= a.E ? 0 : key_of(SURE || !a.bias ? x[j] : v[j]);
+  }
+  float largest = 1.0f;   // score of the row
+  if (!SURE && !a.sigmoid) {
+    largest = s[0];
+#pragma unroll
+    for (int j = 1; j < VPL; j++) largest = fmaxf(largest, s[j]);
+    largest = lanes_reduce<LPR>(largest, OpMax{});
   }
   if (a.groups > 1) {
     // the value of a group comes from the choices; with group_top 1 and no
     // bias the largest logit says the same
+    const bool two = a.group_top == 2 && a.per > 1;
+    const float off = a.sigmoid ? 8 * U : (9 + VPL / 2) * U * fminf(1.0f, 4.0f * largest);   // of one group
+    auto value = [&](const Top2& t) { return two ? t.m1 + t.m2 : t.m1; };
+    auto error = [&](const Top2& t) { return off + 2 * U * (fabsf(t.m1) + (two ? fabsf(t.m2) : 0.0f)); };
+    float low = INFINITY, high = -INFINITY;   // smallest an open group may be, largest a closed one
+    if (l < 4 && a.groups + l < kMaxGroups) gval[a.groups + l] = -INFINITY;
+    if (a.group_lanes) {   // in registers
+      Top2 t{-INFINITY, -INFINITY};
 #pragma unroll
-    for (int j = 0; j < VPL; j++)
-      if (e0 + j < a.E) vals[e0 + j] = SURE ? (F)x[j] : (F)(s[j] + (F)bias[j]);
-    wave_lds_fence();
-    int lg = 1;   // lanes per group
-    while (2 * lg * a.groups <= LPR) lg *= 2;
-    for (int g0 = 0; g0 < a.groups; g0 += LPR / lg) {
-      const int g = g0 + l / lg;
-      F m1 = -INFINITY, m2 = -INFINITY;
-      if (g < a.groups)
+      for (int j = 0; j < VPL; j++) t.add(v[j]);
+      if (a.group_lanes > 1) t.merge_dpp<0xB1>();
+      if (a.group_lanes > 2) t.merge_dpp<0x4E>();
+      if (a.group_lanes > 4) t.merge_dpp<0x141>();
+      if (a.group_lanes > 8) t.merge_dpp<0x140>();
+      const int g = l / a.group_lanes;
+      const float mine = value(t);
+      if (g < a.groups && (l & (a.group_lanes - 1)) == 0) gval[g] = mine;
+      wave_lds_fence();
+      const bool open = rank_of(gval, a.groups, g, mine) < a.top_groups;
+      if (g < a.groups) {
+        if (open) low = mine - error(t);
+        else high = mine + error(t);
+      }
+#pragma unroll
+      for (int j = 0; j < VPL; j++)
+        if (!open && e0 + j < a.E) key[j] = 1;
+    } else {               // through LDS
+#pragma unroll
+      for (int j = 0; j < VPL; j++) vals[e0 + j] = v[j];
+      wave_lds_fence();
+      int lg = 1;   // lanes per group, 16 at most
+      while (lg < 16 && 2 * lg * a.groups <= LPR) lg *= 2;
+      for (int g0 = 0; g0 < a.groups; g0 += LPR / lg) {
+        const int g = g0 + l / lg;
+        Top2 t{-INFINITY, -INFINITY};
+        if (g < a.groups)
 #pragma unroll 4
-        for (int i = l % lg; i < a.per; i += lg) {
-          const F v = vals[g * a.per + i];
-          const F less = v > m1 ? m1 : v;
-          m1 = v > m1 ? v : m1;
-          m2 = less > m2 ? less : m2;
+          for (int i = l & (lg - 1); i < a.per; i += lg) t.add(vals[g * a.per + i]);
+        if (lg > 1) t.merge_dpp<0xB1>();
+        if (lg > 2) t.merge_dpp<0x4E>();
+        if (lg > 4) t.merge_dpp<0x141>();
+        if (lg > 8) t.merge_dpp<0x140>();
+        if (g < a.groups && (l & (lg - 1)) == 0) {
+          gval[g] = value(t);
+          keep[g] = __float_as_uint(error(t));
         }
-      for (int d = 1; d < lg; d *= 2) {
-        const F o1 = __shfl_xor(m1, d, 64), o2 = __shfl_xor(m2, d, 64);
-        const F lo = m1 < o1 ? m1 : o1, hi2 = m2 > o2 ? m2 : o2;
-        m1 = m1 > o1 ? m1 : o1;
-        m2 = lo > hi2 ? lo : hi2;
       }
-      if (g < a.groups && l % lg == 0) gval[g] = a.group_top == 2 && a.per > 1 ? m1 + m2 : m1;
-    }
-    wave_lds_fence();
-    F low = INFINITY, high = -INFINITY;   // smallest open, largest closed
-    for (int g = l; g < a.groups; g += LPR) {
-      const F v = gval[g];
-      int rank = 0;
-#pragma unroll 8
-      for (int h = 0; h < a.groups; h++) {
-        const F o = gval[h];
-        rank += o > v || (o == v && h < g);
+      wave_lds_fence();
+      for (int g = l; g < a.groups; g += LPR) {
+        const float mine = gval[g], e = __uint_as_float(keep[g]);
+        const bool open = rank_of(gval, a.groups, g, mine) < a.top_groups;
+        keep[g] = open;
+        if (open) low = fminf(low, mine - e);
+        else high = fmaxf(high, mine + e);
       }
-      keep[g] = rank < a.top_groups;
-      if (rank < a.top_groups) low = low < v ? low : v;
-      else high = high > v ? high : v;
-    }
-    wave_lds_fence();
-    if (!SURE && sizeof(F) == 4 && a.top_groups < a.groups) {
-      low = lanes_reduce<LPR>(low, OpMin{});
-      high = lanes_reduce<LPR>(high, OpMax{});
-      doubt = close_f32((float)low, (float)high);
-    }
-    int g = e0 / a.per, next = (g + 1) * a.per;
-    uint32_t open = g < a.groups ? keep[g] : 0;
+      wave_lds_fence();
+      int g = e0 / a.per, next = (g + 1) * a.per;
+      uint32_t open = g < a.groups ? keep[g] : 0;
 #pragma unroll
-    for (int j = 0; j < VPL; j++) {
-      if (e0 + j == next) {
-        g++;
-        next += a.per;
-        open = g < a.groups ? keep[g] : 0;
+      for (int j = 0; j < VPL; j++) {
+        if (e0 + j == next) {
+          g++;
+          next += a.per;
+          open = g < a.groups ? keep[g] : 0;
+        }
+        if (!open && e0 + j < a.E) key[j] = 1;
       }
-      if (!open && e0 + j < a.E) key[j] = 1;
+    }
+    if (!SURE) {   // an infinite value leaves NaN, which says nothing: infinities are equal in 64 bits too
+      low = lanes_reduce<LPR>(fminf(low, INFINITY), OpMin{});
+      high = lanes_reduce<LPR>(fmaxf(high, -INFINITY), OpMax{});
+      doubt = low < high;
     }
     wave_lds_fence();
   }
+#pragma unroll
+  for (int j = 0; j < VPL; j++) vals[e0 + j] = s[j];
   // top_k rounds of the largest key, ties to the lowest lane and then the
   // lowest register, i.e. the lowest expert; one more round says how far the
   // first one left out is.
-  const bool check = !SURE && sizeof(F) == 4 && a.bias;
+  const bool check = !SURE && a.bias;
   const int rounds = check && a.K < a.E ? a.K + 1 : a.K;
-  const int seg = (threadIdx.x & 63) & ~(LPR - 1);
-  F before = INFINITY;
   for (int k = 0; k < rounds; k++) {
-    Key lm = key[0];
+    uint32_t lm = key[0];
 #pragma unroll
     for (int j = 1; j < VPL; j++) lm = key[j] > lm ? key[j] : lm;
-    const Key m = lanes_reduce<LPR>(lm, OpMax{});
+    const uint32_t m = lanes_reduce<LPR>(lm, OpMax{});
     uint64_t who = __ballot(lm == m) >> seg;
     if (LPR < 64) who &= ((uint64_t)1 << (LPR & 63)) - 1;
-    if constexpr (!SURE) {
-      if (check) {
-        const F v = value_of(m);
-        if (k > 0 && m > 2) doubt = doubt || close_f32((float)before, (float)v);
-        before = v;
-      }
-    }
-    if (k < a.K && l == (int)__builtin_ctzll(who)) {
+    if (l == (int)__builtin_ctzll(who)) {
       int at = 0;
-      F sv = 0;
 #pragma unroll
-      for (int j = VPL - 1; j >= 0; j--)
-        if (key[j] == m) {
-          at = j;
-          sv = s[j];
-        }
+      for (int j = VPL - 1; j >= 0; j--) at = key[j] == m ? j : at;
 #pragma unroll
-      for (int j = 0; j < VPL; j++)
-        if (j == at) key[j] = 0;
-      picked[k] = sv;
-      picked_id[k] = e0 + at;
+      for (int j = 0; j < VPL; j++) key[j] = j == at ? 0 : key[j];
+      pick[k] = u32x2{(uint32_t)(e0 + at), m};
     }
   }
   wave_lds_fence();
-  F total = 0;
-  for (int k = l; k < a.K; k += LPR) total += picked[k];
-  total = lanes_reduce<LPR>(total, OpAdd{});
-  const F r = a.renorm ? (F)1 / (total + (F)1e-20) : (F)1;
-  if (live)
+  if (check) {
+    const float off = a.sigmoid ? 8 * U : (18 + VPL) * U * fminf(1.0f, 2.0f * largest);
+    for (int k = l; k + 1 < rounds; k += LPR) {
+      const uint32_t k0 = pick[k].y, k1 = pick[k + 1].y;
+      const float v0 = value_of(k0), v1 = value_of(k1);
+      doubt = doubt || (k1 > 2 && v0 - v1 <= off + 2 * U * fmaxf(fabsf(v0), fabsf(v1)));
+    }
+  }
+  if constexpr (!SURE) {
+    uint64_t any = __ballot(doubt) >> seg;
+    if (LPR < 64) any &= ((uint64_t)1 << (LPR & 63)) - 1;
+    doubt = any != 0;
+  }
+  float total = 0.0f;
+  if (a.renorm) {
+    for (int k = l; k < a.K; k += LPR) total += vals[pick[k].x];
+    total = lanes_reduce<LPR>(total, OpAdd{});
+  }
+  const float r = a.renorm ? 1.0f / (total + 1e-20f) : 1.0f;
+  if (live && !doubt)
     for (int k = l; k < a.K; k += LPR) {
-      w_out[k] = (float)(picked[k] * r);
-      id_out[k] = picked_id[k];
+      const int e = (int)pick[k].x;
+      w_out[k] = vals[e] * r;
+      id_out[k] = e;
     }
   wave_lds_fence();
   return doubt;
 }
 
-// A wave holds 64 / LPR rows.  The choice is made in 32 bits; a wave in which
-// the order of two values is within the rounding (a row in a few hundred with a
-// bias) makes it again in 64.  Bound by the rounds' latency for few rows (16
-// tokens, 256 experts in 8 groups: 5.8 us) and by their instructions for many
-// (16384 tokens, 128 experts, top 8: 7.3 us for 5 MB).
+// One row again in 64 bits, on a whole wave: lane l holds experts l N .. + N - 1.
+// The kernel waits for the last such row, so it is made short: one exp per
+// expert (in a loop that turns the registers, as the code is fetched for it
+// alone), groups by several lanes each, rounds on the keys' upper words.
+template <int N, typename D>
+__device__ __forceinline__ void route_exact(const RouteArgs& a, const typename D::T* __restrict__ row, char* lds,
+                                            float* __restrict__ w_out, int32_t* __restrict__ id_out) {
+  double* const vals = reinterpret_cast<double*>(lds);              // [64 N] choices, then scores
+  double* const gval = vals + 64 * N;                               // [64]
+  uint32_t* const keep = reinterpret_cast<uint32_t*>(gval + kMaxGroups);
+  int32_t* const picked = reinterpret_cast<int32_t*>(keep + kMaxGroups);
+  const int lane = threadIdx.x & 63, e0 = lane * N;
+  float x[N], b[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) {
+    x[j] = e0 + j < a.E ? to_f32<D>(row[e0 + j]) : -INFINITY;
+    b[j] = a.bias && e0 + j < a.E ? a.bias[e0 + j] : 0.0f;
+  }
+  float m = x[0];
+#pragma unroll
+  for (int j = 1; j < N; j++) m = fmaxf(m, x[j]);
+  m = lanes_reduce<64>(m, OpMax{});
+  if (m == -INFINITY) m = 0.0f;
+  double s[N];
+#pragma unroll 1
+  for (int i = 0; i < N; i++) {
+    const float first = x[0];
+    double t = exp(a.sigmoid ? -(double)first : (double)first - (double)m);
+    if (a.sigmoid) t = 1.0 / (1.0 + t);
+#pragma unroll
+    for (int j = 0; j + 1 < N; j++) {
+      x[j] = x[j + 1];
+      s[j] = s[j + 1];
+    }
+    x[N - 1] = first;
+    s[N - 1] = t;
+  }
+  if (!a.sigmoid) {
+    double sum = 0.0;
+#pragma unroll
+    for (int j = 0; j < N; j++) sum += s[j];
+    sum = lanes_reduce<64>(sum, OpAdd{});
+    const double r = sum == 0.0 ? 0.0 : 1.0 / sum;
+#pragma unroll
+    for (int j = 0; j < N; j++) s[j] *= r;
+  }
+  // without a bias the order is the logits' own
+  uint64_t key[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) key[j] = e0 + j >= a.E ? 0 : key_of(a.bias ? s[j] + (double)b[j] : (double)x[j]);
+  if (a.groups > 1) {
+#pragma unroll
+    for (int j = 0; j < N; j++) vals[e0 + j] = s[j] + (double)b[j];
+    wave_lds_fence();
+    int lg = 1;   // lanes per group, 16 at most
+    while (lg < 16 && 2 * lg * a.groups <= 64) lg *= 2;
+    const int mine = lane / lg;
+    double m1 = -INFINITY, m2 = -INFINITY;
+    auto add = [&](double v1, double v2) {   // v1 >= v2
+      const double less = v1 > m1 ? m1 : v1;
+      m1 = v1 > m1 ? v1 : m1;
+      m2 = v2 > m2 ? v2 : m2;
+      m2 = less > m2 ? less : m2;
+    };
+    if (mine < a.groups)
+#pragma unroll 2
+      for (int i = lane & (lg - 1); i < a.per; i += lg) add(vals[mine * a.per + i], -INFINITY);
+    if (lg > 1) add(dppx<double, 0xB1>(m1), dppx<double, 0xB1>(m2));
+    if (lg > 2) add(dppx<double, 0x4E>(m1), dppx<double, 0x4E>(m2));
+    if (lg > 4) add(dppx<double, 0x141>(m1), dppx<double, 0x141>(m2));
+    if (lg > 8) add(dppx<double, 0x140>(m1), dppx<double, 0x140>(m2));
+    if (mine < a.groups && (lane & (lg - 1)) == 0) gval[mine] = a.group_top == 2 && a.per > 1 ? m1 + m2 : m1;
+    wave_lds_fence();
+    if (lane < a.groups) {
+      const double v = gval[lane];
+      int rank = 0;
+#pragma unroll 4
+      for (int h = 0; h < a.groups; h++) {
+        const double o = gval[h];
+        rank += o > v || (o == v && h < lane);
+      }
+      keep[lane] = rank < a.top_groups;
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      if (e0 + j < a.E && !keep[(e0 + j) / a.per]) key[j] = 1;
+  }
+#pragma unroll
+  for (int j = 0; j < N; j++) vals[e0 + j] = s[j];
+#pragma unroll 1
+  for (int k = 0; k < a.K; k++) {
+    uint64_t best = key[0];
+#pragma unroll
+    for (int j = 1; j < N; j++) best = key[j] > best ? key[j] : best;
+    const uint32_t hi = (uint32_t)(best >> 32), top = lanes_reduce<64>(hi, OpMax{});
+    uint64_t who = __ballot(hi == top);
+    if (who & (who - 1)) {   // several lanes: by the lower words
+      const uint32_t lo = hi == top ? (uint32_t)best : 0;
+      const uint32_t low = lanes_reduce<64>(lo, OpMax{});
+      who = __ballot(hi == top && lo == low);
+    }
+    if (lane == (int)__builtin_ctzll(who)) {
+      int at = 0;
+#pragma unroll
+      for (int j = N - 1; j >= 0; j--) at = key[j] == best ? j : at;
+#pragma unroll
+      for (int j = 0; j < N; j++) key[j] = j == at ? 0 : key[j];
+      picked[k] = e0 + at;
+    }
+  }
+  wave_lds_fence();
+  const int id = lane < a.K ? picked[lane] : 0;
+  const double mine = lane < a.K ? vals[id] : 0.0;
+  const double total = lanes_reduce<64>(mine, OpAdd{});
+  if (lane < a.K) {
+    w_out[lane] = (float)(a.renorm ? mine / (total + 1e-20) : mine);
+    id_out[lane] = id;
+  }
+  wave_lds_fence();
+}
+
+// A wave holds 64 / LPR rows.  The choice is made in 32 bits; a row in which
+// the order of two values is within the rounding (one in a few thousand with a
+// bias) is chosen again in 64, which the kernel then waits 2.5 us for.  Bound by
+// the rounds' latency for few rows (16 tokens, 256 experts, top 8: 3.1 us, 4.5
+// with a bias and 8 groups) and by their instructions for many (16384 tokens, 128
+// experts, top 8: 6.0 us for 5 MB, 8.1 with a bias; 0.35 a round).
 template <typename D, int LPR, int VPL, bool SURE>
 __global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __restrict__ logits, int64_t T, int64_t ld,
                                                         RouteArgs a, float* __restrict__ weights,
                                                         int32_t* __restrict__ ids) {
-  constexpr int ROWS = 256 / LPR;
-  typedef typename std::conditional<SURE, float, double>::type Wide;
-  constexpr int NEED = LPR * VPL > 64 ? LPR * VPL : 64;
-  __shared__ __attribute__((aligned(16))) char lds[ROWS][(NEED + kMaxGroups) * sizeof(Wide) + kMaxGroups * 4];
+  typedef RouteLds<LPR, VPL> L;
+  constexpr int ROWS = 256 / LPR, WROWS = 64 / LPR;
+  constexpr int WAVE = SURE ? L::ROWS : L::WAVE;
+  __shared__ __attribute__((aligned(16))) char lds[4][WAVE];
   const int l = threadIdx.x & (LPR - 1);
-  const int sub = threadIdx.x / LPR;
-  const int64_t t = (int64_t)blockIdx.x * ROWS + sub;
+  const int w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t first = (int64_t)blockIdx.x * ROWS + w * WROWS;   // the wave's rows
+  const int sub = (threadIdx.x & 63) / LPR;
+  const int64_t t = first + sub;
   const bool live = t < T;   // rows past the end repeat the last one and write nothing
   const int64_t tr = live ? t : T - 1;
   float x[VPL];
   float bias[VPL];   // with the logits, so that one latency covers both
 #pragma unroll
-  for (int j = 0; j < VPL; j++) bias[j] = !SURE && a.bias && l * VPL + j < a.E ? a.bias[l * VPL + j] : 0.0f;
+  for (int j = 0; j < VPL; j++) bias[j] = 0.0f;
+  if (!SURE && a.bias) load_logits<VPL, Fp32>(a.bias, l * VPL, a.E, a.wide_bias, bias);
   load_logits<VPL, D>(logits + tr * ld, l * VPL, a.E, a.wide, x);
-  const bool doubt = route_row<LPR, VPL, SURE, float>(a, x, bias, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+  const bool doubt =
+      route_row<LPR, VPL, SURE>(a, x, bias, l, lds[w] + sub * L::ROW, weights + tr * a.K, ids + tr * a.K, live);
   if constexpr (!SURE) {
-    if (__any(doubt))
-      route_row<LPR, VPL, SURE, double>(a, x, bias, l, lds[sub], weights + tr * a.K, ids + tr * a.K, live);
+    uint64_t again = __ballot(doubt && live && l == 0);
+#pragma unroll 1
+    while (again) {
+      const int64_t row = first + __builtin_ctzll(again) / LPR;
+      again &= again - 1;
+      route_exact<L::NV / 64, D>(a, logits + row * ld, lds[w], weights + row * a.K, ids + row * a.K);
+    }
   }
 }
 
@@ -436,7 +635,7 @@ __global__ __launch_bounds__(256) void moe_route_backward_kernel(const typename 
   }
   wave_lds_fence();
   float s[VPL], g[VPL];
-  scores_of<LPR, VPL, float>(x, a.sigmoid, s);
+  scores_of<LPR, VPL>(x, a.sigmoid, s);
   uint32_t chosen = 0;
   float total = 0.0f, gs = 0.0f;
 #pragma unroll
@@ -522,11 +721,20 @@ static RouteArgs route_args(int64_t E, int32_t K, int32_t groups, int32_t top_gr
   a.top_groups = top_groups;
   a.group_top = group_top;
   a.per = (int)(E / groups);
+  a.group_lanes = 0;
   a.sigmoid = sigmoid;
   a.renorm = renorm;
   a.wide = false;
+  a.wide_bias = reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   a.bias = bias;
   return a;
+}
+
+// Lanes of vpl experts that hold one group, where that is a power of two up to
+// a DPP row (16384 tokens, 128 experts: 8 groups add 1.0 us, through LDS 2.2).
+static int lanes_of_group(const RouteArgs& a, int vpl) {
+  const int n = a.per % vpl ? 0 : a.per / vpl;
+  return n <= 16 && (n & (n - 1)) == 0 ? n : 0;
 }
 
 // Whether rows of stride ld and lanes of vpl (a multiple of 4) can be read in
@@ -545,6 +753,7 @@ static hipError_t route_t(const void* logits, int64_t T, int64_t ld, RouteArgs a
   do {                                                                                                               \
     const unsigned grid = (unsigned)((T + 256 / L - 1) / (256 / L));                                                 \
     a.wide = wide_rows(logits, ld, sizeof(typename D::T), V);                                                        \
+    a.group_lanes = lanes_of_group(a, V);                                                                            \
     if (sure)                                                                                                        \
       hipLaunchKernelGGL((moe_route_kernel<D, L, V, true>), dim3(grid), dim3(256), 0, stream, x, T, ld, a, weights, ids); \
     else                                                                                                             \

@@ -1,0 +1,90 @@
+"""moe.route's order of experts where their choices lie within the rounding of
+32 bits: it is the order of the exact scores (ties: lowest index)."""
+
+import numpy as np
+import pytest
+
+from gpu_util import log, need_gpu, to_host
+
+pytestmark = pytest.mark.gpu
+
+
+def _order(x, top_k, scores, bias, groups, top_groups, group_top):
+    """Expert ids in 64 bits, by stable sorts."""
+    x = x.astype(np.float64)
+    if scores == "softmax":
+        s = np.exp(x - x.max(1, keepdims=True))
+        s /= s.sum(1, keepdims=True)
+    else:
+        s = 1 / (1 + np.exp(-x))
+    v = s if bias is None else s + bias.astype(np.float64)
+    if groups > 1:
+        inside = -np.sort(-v.reshape(len(v), groups, -1), axis=2)
+        best = inside[:, :, :group_top].sum(2)
+        keep = np.argsort(-best, axis=1, kind="stable")[:, :top_groups]
+        open_ = np.zeros_like(best, dtype=bool)
+        np.put_along_axis(open_, keep, True, 1)
+        # closed experts behind every open one, whatever its value
+        order = np.argsort(-v, axis=1, kind="stable")
+        shut = ~np.take_along_axis(np.repeat(open_, v.shape[1] // groups, 1), order, 1)
+        order = np.take_along_axis(order, np.argsort(shut, axis=1, kind="stable"), 1)
+        return order[:, :top_k]
+    return np.argsort(-v, axis=1, kind="stable")[:, :top_k]
+
+
+# few rows (a wave each) and many, every number of experts a lane holds, groups
+# that end with lanes (1, 2, 4, 8, 16 of them) and groups that do not
+SHAPES = [(400, 64, 8, 8, 3), (400, 256, 8, 8, 4), (400, 256, 8, 4, 2), (400, 192, 6, 3, 2), (400, 500, 8, 4, 2),
+          (400, 1000, 12, 8, 3), (3000, 40, 12, 8, 3), (3000, 64, 9, 16, 5), (3000, 128, 8, 8, 4), (3000, 128, 8, 1, 1),
+          (3000, 128, 4, 2, 1), (3000, 256, 8, 32, 9), (3000, 384, 8, 8, 3), (3000, 384, 8, 1, 1), (3000, 640, 10, 10, 4),
+          (3000, 96, 1, 6, 1)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=["%dx%d_k%d_g%d_%d" % s for s in SHAPES])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("spread", [1.0, 2.0 ** -10, 2.0 ** -17])
+def test_order_is_that_of_the_exact_scores(shape, scores, spread):
+    """The smaller the logits' spread, the more choices lie within the rounding:
+    of a few rows in a thousand, of most, of all."""
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe
+
+    T, E, K, groups, top_groups = shape
+    log("order %s %s spread=%g" % (shape, scores, spread))
+    rng = np.random.default_rng(E + K)
+    x = (rng.standard_normal((T, E)) * spread).astype(np.float32)
+    # the choices spread like the scores do
+    unit = spread if scores == "sigmoid" else spread / E
+    bias = (rng.standard_normal(E) * 0.25 * unit).astype(np.float32)
+    for b in (bias, None):
+        for group_top in (1, 2):
+            kw = dict(groups=groups, top_groups=top_groups, group_top=group_top)
+            want = _order(x, K, scores, b, **kw)
+            w, ids = moe.route(torch.from_numpy(x).cuda(), K, scores=scores,
+                               bias=None if b is None else torch.from_numpy(b).cuda(), **kw)
+            got = to_host(ids).view(np.int32)
+            assert np.array_equal(got, want), (b is not None, group_top, np.flatnonzero((got != want).any(1))[:8])
+            assert torch.isfinite(w).all()
+
+
+@pytest.mark.parametrize("low", [float("-inf"), float(np.finfo(np.float32).min)])
+@pytest.mark.parametrize("E,groups", [(64, 8), (128, 8), (60, 6)])
+@pytest.mark.parametrize("T", [5, 700])
+def test_experts_masked_by_the_bias(low, E, groups, T):
+    """Masked experts come last; whole groups of them lose against any other."""
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe
+
+    per = E // groups
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.05).astype(np.float32)
+    bias[::3] = low                     # some of every group
+    bias[2 * per:4 * per] = low         # two groups
+    for group_top in (1, 2):
+        for top_groups in (1, 2, groups - 1):
+            K = min(4, per)
+            kw = dict(groups=groups, top_groups=top_groups, group_top=group_top)
+            want = _order(x, K, "sigmoid", bias, **kw)
+            _, ids = moe.route(torch.from_numpy(x).cuda(), K, scores="sigmoid", bias=torch.from_numpy(bias).cuda(), **kw)
+            assert np.array_equal(to_host(ids).view(np.int32), want), (group_top, top_groups)
