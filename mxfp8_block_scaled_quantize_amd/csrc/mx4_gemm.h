@@ -74,11 +74,15 @@ __device__ __forceinline__ void tile_of_block(int64_t tiles_m, int64_t tiles_n, 
   }
 }
 
+// Bound on the row tiles of G groups in M rows: a group with rows, of which there
+// are M at most, ends BM - 1 rows into a tile at worst.
+inline int64_t group_tiles(int64_t M, int64_t G, int64_t BM) { return (M + (G < M ? G : M) * (BM - 1)) / BM; }
+
 // Row tile tm (of TM rows) among the groups' tiles, 64 groups at a time: bounds
 // clamped into [0, M] and raised to the running maximum, a prefix sum of the
 // tile counts, and the lane whose range holds tm.  Returns the group (-1: past
 // the last tile) and the tile's rows [lo, hi) to the group's end.  Every wave
-// of the workgroup computes the same.
+// of the workgroup computes the same.  TM = 0: a group with rows is one tile.
 template <int TM>
 __device__ __forceinline__ int group_of_tile(const int32_t* __restrict__ offsets, int G, int64_t M, int64_t tm, int64_t* m_lo,
                                              int64_t* m_hi) {
@@ -100,7 +104,8 @@ __device__ __forceinline__ int group_of_tile(const int32_t* __restrict__ offsets
     }
     hi = hi > lo ? hi : lo;
     carry = __builtin_amdgcn_readlane(hi, 63);
-    const int nt = (hi - lo + TM - 1) / TM;
+    int nt = hi > lo;
+    if constexpr (TM > 0) nt = (hi - lo + TM - 1) / TM;
     int incl = nt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {

@@ -63,8 +63,12 @@ __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(const uint8_t* __
   const int64_t n0 = (int64_t)blockIdx.x * TN;
   int64_t lo, hi, b_row0 = 0;
   if (GROUPED) {
-    group_rows(offsets, blockIdx.y, M, &lo, &hi);
-    b_row0 = (int64_t)blockIdx.y * N * (SW ? 2 : 1);
+    // fewer workgroups than groups: one for each group that can have rows
+    int g = blockIdx.y;
+    if (gridDim.y < (unsigned)G) g = group_of_tile<0>(offsets, G, M, blockIdx.y, &lo, &hi);
+    else group_rows(offsets, g, M, &lo, &hi);
+    if (g < 0) return;
+    b_row0 = (int64_t)g * N * (SW ? 2 : 1);
   } else {
     lo = (int64_t)blockIdx.y * 16 * MB;
     hi = lo + 16 * MB < M ? lo + 16 * MB : M;
@@ -163,7 +167,7 @@ __global__ __launch_bounds__(64 * W) void mx4_gemm_rows_kernel(const uint8_t* __
 template <int MB, int NB, int W, bool GROUPED, int EPI>
 static hipError_t launch_rows(const Mx4Gemm& g, hipStream_t stream) {
   const int64_t tn = g.N / (EPI == EPI_SWIGLU ? 16 : 16 * NB);
-  const int64_t ty = GROUPED ? g.G : (g.M + 16 * MB - 1) / (16 * MB);
+  const int64_t ty = GROUPED ? (g.G < g.M ? g.G : g.M) : (g.M + 16 * MB - 1) / (16 * MB);
   hipLaunchKernelGGL((mx4_gemm_rows_kernel<MB, NB, W, GROUPED, EPI>), dim3((unsigned)tn, (unsigned)ty), dim3(64 * W), 0, stream,
                      g.a, g.ap, g.b, g.bp, g.c, g.ldc, g.M, g.N, g.K, g.offsets, g.G);
   return hipGetLastError();
@@ -255,7 +259,7 @@ static hipError_t launch_rows_w(const Mx4Gemm& g, hipStream_t stream) {
   // row x 2048 columns, K = 8192: 6.3 us, with four waves 6.8; K = 1024, 256 x
   // 4096: 10.4 and 9.8; 32 experts of 2048 x 4096: 23 and 20)
   const int64_t tn = g.N / (g.epilogue == EPI_SWIGLU ? 16 : 32);
-  const int64_t groups = g.offsets ? g.G : (g.M + 16 * MB - 1) / (16 * MB);
+  const int64_t groups = g.offsets ? (g.G < g.M ? g.G : g.M) : (g.M + 16 * MB - 1) / (16 * MB);
   if (g.K >= 2048 && tn * groups < 1024) return g.offsets ? launch_rows_e<MB, 8, true>(g, stream) : launch_rows_e<MB, 8, false>(g, stream);
   return g.offsets ? launch_rows_e<MB, 4, true>(g, stream) : launch_rows_e<MB, 4, false>(g, stream);
 }

@@ -286,7 +286,7 @@ __global__ __launch_bounds__(256) void mx4_gemm_mid_kernel(const uint8_t* __rest
 template <int BM, int BN>
 static void mid_tiles(const Mx4Gemm& g, int64_t* tm, int64_t* tn) {
   const int cols = g.epilogue == 2 ? BN / 2 : BN;
-  *tm = (g.M + BM - 1) / BM + (g.offsets ? g.G : 0);
+  *tm = g.offsets ? group_tiles(g.M, g.G, BM) : (g.M + BM - 1) / BM;
   *tn = (g.N + cols - 1) / cols;
 }
 

@@ -373,7 +373,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_pe
 
 static int64_t tile_cols(const Mx4Gemm& g) { return g.epilogue == 2 ? SW_COLS : TNB; }
 static int64_t tiles_n(const Mx4Gemm& g) { return (g.N + tile_cols(g) - 1) / tile_cols(g); }
-static int64_t tiles_m(const Mx4Gemm& g) { return (g.M + TM - 1) / TM + (g.offsets ? g.G : 0); }
+static int64_t tiles_m(const Mx4Gemm& g) { return g.offsets ? group_tiles(g.M, g.G, TM) : (g.M + TM - 1) / TM; }
 // An expert's scale words (SwiGLU: 2N of them) lie in one buffer of 32-bit offsets.
 bool mx4_gemm_tile_fits(const Mx4Gemm& g) {
   return (g.epilogue != 2 || g.N < (int64_t(1) << 28)) && grid_fits(tiles_m(g), tiles_n(g), 256);

@@ -352,3 +352,36 @@ def test_round_trip_of_a_linear_layer_in_mxfp4():
     side.synchronize()
     vx, vw = (bf16_to_f64(to_host(t)) for t in (vx, vw))
     _close(bf16_to_f64(to_host(y)), *_bounds(vx, vw), "linear layer")
+
+
+# more groups than rows: workgroups only for the groups that can have rows
+@pytest.mark.parametrize("counts", [[0] * 63 + [1], [1] + [0] * 200, [0, 2, 0, 0, 1, 0, 0, 0, 1], [0] * 64 + [3] + [0] * 30 + [1, 1] + [0] * 60,
+                                    [1] * 5 + [0] * 90 + [1] * 20, [0, 0, 0]],
+                         ids=["last", "first", "few", "over64", "ones", "none"])
+@pytest.mark.parametrize("N,K", [(64, 256), (288, 640)])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_grouped_gemm_of_more_groups_than_rows(counts, N, K, mode):
+    test_grouped_gemm(counts, N, K, mode)
+
+
+def test_grouped_gemm_invalid_offsets_of_more_groups_than_rows():
+    torch, mxfp4 = _mxfp4()
+    M, N, K = 3, 64, 256
+    for offsets in ([-7, 2, 1, 1000, 60, 2 ** 31 - 1], [5, 4, 3, 2, 1, 0], [-1, -2 ** 31, 0, 1, -5, 2], [2, 0, 0, 0, 0, 0, 3]):
+        offsets = np.array(offsets, np.int32)
+        G = len(offsets) - 1
+        rng = np.random.default_rng(4)
+        a, sa, va = ref.random_operand(rng, M, K)
+        b, sb, vb = ref.random_operand(rng, G * N, K)
+        edges = np.maximum.accumulate(np.clip(offsets, 0, M))
+        old = ref.heavy_bits((M, N), 2)
+        log("mxfp4 grouped, offsets %s" % offsets)
+        bits = to_host(mxfp4.grouped_gemm(to_dev(a), _words(ref.pack(sa)), to_dev(b.reshape(G, N, K // 2)),
+                                          _words(ref.pack(sb)), to_dev(offsets), out=to_dev_bf16(old)))
+        got = bf16_to_f64(bits)
+        outside = np.ones(M, bool)
+        for g in range(G):
+            r = slice(edges[g], edges[g + 1])
+            outside[r] = False
+            _close(got[r], *_bounds(va[r], vb[g * N:(g + 1) * N]), "group %d" % g)
+        assert np.array_equal(bits[outside], old[outside])
