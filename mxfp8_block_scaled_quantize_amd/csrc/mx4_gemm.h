@@ -78,40 +78,48 @@ __device__ __forceinline__ void tile_of_block(int64_t tiles_m, int64_t tiles_n, 
 // are M at most, ends BM - 1 rows into a tile at worst.
 inline int64_t group_tiles(int64_t M, int64_t G, int64_t BM) { return (M + (G < M ? G : M) * (BM - 1)) / BM; }
 
+// Inclusive scan over the wave of values that are not negative: shifts inside
+// the 16-lane rows, then each row's last lane to the rows after it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+template <typename Op>
+__device__ __forceinline__ int scan64(int v, Op op) {
+  v = op(v, dpp_or_zero<0x111, 0xF>(v));
+  v = op(v, dpp_or_zero<0x112, 0xF>(v));
+  v = op(v, dpp_or_zero<0x114, 0xF>(v));
+  v = op(v, dpp_or_zero<0x118, 0xF>(v));
+  v = op(v, dpp_or_zero<0x142, 0xA>(v));
+  v = op(v, dpp_or_zero<0x143, 0xC>(v));
+  return v;
+}
+
 // Row tile tm (of TM rows) among the groups' tiles, 64 groups at a time: bounds
 // clamped into [0, M] and raised to the running maximum, a prefix sum of the
 // tile counts, and the lane whose range holds tm.  Returns the group (-1: past
 // the last tile) and the tile's rows [lo, hi) to the group's end.  Every wave
-// of the workgroup computes the same.  TM = 0: a group with rows is one tile.
+// of the workgroup computes the same.
 template <int TM>
 __device__ __forceinline__ int group_of_tile(const int32_t* __restrict__ offsets, int G, int64_t M, int64_t tm, int64_t* m_lo,
                                              int64_t* m_hi) {
   const int lane = threadIdx.x & 63;
+  const int end = (int)M;
   int carry = 0;
   for (int g0 = 0; g0 < G; g0 += 64) {
     const int g = g0 + lane;
     int lo = 0, hi = 0;
     if (g < G) {
-      const int64_t l = offsets[g], h = offsets[g + 1];
-      lo = (int)(l < 0 ? 0 : (l > M ? M : l));
-      hi = (int)(h < 0 ? 0 : (h > M ? M : h));
+      const int l = offsets[g], h = offsets[g + 1];
+      lo = l < 0 ? 0 : (l > end ? end : l);
+      hi = h < 0 ? 0 : (h > end ? end : h);
     }
     lo = lo > carry ? lo : carry;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int t = __shfl_up(lo, d, 64);
-      if (lane >= d) lo = lo > t ? lo : t;
-    }
+    lo = scan64(lo, [](int a, int b) { return a > b ? a : b; });
     hi = hi > lo ? hi : lo;
     carry = __builtin_amdgcn_readlane(hi, 63);
-    int nt = hi > lo;
-    if constexpr (TM > 0) nt = (hi - lo + TM - 1) / TM;
-    int incl = nt;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int t = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += t;
-    }
+    const int nt = (int)(((unsigned)(hi - lo) + TM - 1) / TM);
+    const int incl = scan64(nt, [](int a, int b) { return a + b; });
     const int total = __builtin_amdgcn_readlane(incl, 63);
     if (tm < total) {
       const int fl = __builtin_ctzll(__ballot(incl > tm));

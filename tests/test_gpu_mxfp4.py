@@ -385,3 +385,21 @@ def test_grouped_gemm_invalid_offsets_of_more_groups_than_rows():
             outside[r] = False
             _close(got[r], *_bounds(va[r], vb[g * N:(g + 1) * N]), "group %d" % g)
         assert np.array_equal(bits[outside], old[outside])
+
+
+# Sizes that the other lists leave without some tile: few rows in blocks of 32
+# and of 16, 64 x 64, 64 x 128, 128 x 128 and 256 x 256, with and without half
+# steps of K, ends of groups inside tiles.
+@pytest.mark.parametrize("M,N,K", [(40, 3104, 256), (40, 1600, 128), (200, 1312, 128), (300, 5152, 1920), (2900, 4128, 256),
+                                   (2900, 2080, 128), (2900, 4128, 128), (1500, 1312, 384)])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_gemm_of_other_tiles(M, N, K, mode):
+    test_gemm(M, N, K, mode)
+
+
+@pytest.mark.parametrize("counts,N,K", [([1500, 298], 96, 256), ([1] * 7 + [0, 5] * 11 + [0], 288, 1920), ([12, 0, 3] * 8 + [1, 0, 4, 2, 0, 0], 4128, 640),
+                                        ([4000, 1998], 4128, 1920), ([1701, 2296], 5152, 1152), ([2, 0, 0, 30, 9, 96] * 5, 1056, 256)],
+                         ids=["2", "30", "30wide", "2large", "2larger", "30uneven"])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_grouped_gemm_of_other_tiles(counts, N, K, mode):
+    test_grouped_gemm(counts, N, K, mode)
