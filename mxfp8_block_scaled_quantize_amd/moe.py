@@ -136,11 +136,14 @@ class Dispatch(NamedTuple):
     position: torch.Tensor
 
 
+_new_tuple = tuple.__new__
+
+
 def dispatch(ids, experts, stream=None):
     """Stable counting sort of the slots of ids (int32 [T, K]) by expert."""
     if stream is not None:
         return on_stream(stream, (ids,), lambda: dispatch(ids, experts))
-    return Dispatch._make((_ops or _load()).dispatch(ids, experts))
+    return _new_tuple(Dispatch, (_ops or _load()).dispatch(ids, experts))
 
 
 def combine(y, position, weights, stream=None):
