@@ -858,7 +858,7 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
   int32_t* const before = total + (E + 1);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
-  const int64_t part = run / DW;      // a multiple of a batch
+  const int64_t part = run / DW;      // a multiple of a piece
   const int64_t plo = lo + w * part;
   const int64_t phi = plo + part < hi ? plo + part : hi;
   int first[DB];                      // the wave's first batch
@@ -915,12 +915,7 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
       }
       if (!ONE) all = total[e];
     }
-    int32_t incl = all;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int32_t o = __shfl_up(incl, d, 64);
-      if (lane >= d) incl += o;
-    }
+    const int32_t incl = scan64(all, OpAdd{});
     if (lane == 63) wave_sum[w] = incl;
     __syncthreads();
     int32_t start = carry + incl - all;
@@ -941,23 +936,24 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     }
     __syncthreads();
   }
-  for (int64_t i0 = plo; i0 < phi; i0 += 64 * DB) {
-    int id[DB];
-    uint64_t same[DB];
+  auto place = [&](int64_t i0, auto pieces) {
+    constexpr int P = decltype(pieces)::value;
+    int id[P];
+    uint64_t same[P];
 #pragma unroll
-    for (int b = 0; b < DB; b++) {
+    for (int b = 0; b < P; b++) {
       const int64_t i = i0 + 64 * b + lane;
       id[b] = i0 == plo ? first[b] : i < phi ? bucket_of(ids[i], E) : 0;
       same[b] = __ballot(i < phi);
     }
     for (int bit = 0; bit < bits; bit++)
 #pragma unroll
-      for (int b = 0; b < DB; b++) {
+      for (int b = 0; b < P; b++) {
         const uint64_t m = __ballot((id[b] >> bit) & 1);
         same[b] &= ((id[b] >> bit) & 1) ? m : ~m;
       }
 #pragma unroll
-    for (int b = 0; b < DB; b++) {
+    for (int b = 0; b < P; b++) {
       const int64_t i = i0 + 64 * b + lane;
       if (i < phi) {
         const int32_t at = row[id[b]] + __popcll(same[b] & (((uint64_t)1 << lane) - 1));
@@ -968,12 +964,17 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
       }
       wave_lds_fence();
     }
+  };
+  for (int64_t i0 = plo; i0 < phi; i0 += 64 * DB) {
+    if (phi - i0 <= 64) place(i0, std::integral_constant<int, 1>{});
+    else place(i0, std::integral_constant<int, DB>{});
   }
 }
 
-// Slots of a workgroup: one batch a wave, more batches beyond kMaxRuns runs.
+// Slots of a workgroup: one batch a wave, more batches beyond kMaxRuns runs; alone
+// in whole pieces for every wave.
 static int64_t dispatch_run(int64_t n) {
-  if (n <= kOneBlock) return kOneBlock;
+  if (n <= kOneBlock) return (n + 64 * DW - 1) / (64 * DW) * (64 * DW);
   return ((n + kMaxRuns - 1) / kMaxRuns + kRun - 1) / kRun * kRun;
 }
 

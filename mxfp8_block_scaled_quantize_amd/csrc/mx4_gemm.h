@@ -78,23 +78,6 @@ __device__ __forceinline__ void tile_of_block(int64_t tiles_m, int64_t tiles_n, 
 // are M at most, ends BM - 1 rows into a tile at worst.
 inline int64_t group_tiles(int64_t M, int64_t G, int64_t BM) { return (M + (G < M ? G : M) * (BM - 1)) / BM; }
 
-// Inclusive scan over the wave of values that are not negative: shifts inside
-// the 16-lane rows, then each row's last lane to the rows after it.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_or_zero(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-template <typename Op>
-__device__ __forceinline__ int scan64(int v, Op op) {
-  v = op(v, dpp_or_zero<0x111, 0xF>(v));
-  v = op(v, dpp_or_zero<0x112, 0xF>(v));
-  v = op(v, dpp_or_zero<0x114, 0xF>(v));
-  v = op(v, dpp_or_zero<0x118, 0xF>(v));
-  v = op(v, dpp_or_zero<0x142, 0xA>(v));
-  v = op(v, dpp_or_zero<0x143, 0xC>(v));
-  return v;
-}
-
 // Row tile tm (of TM rows) among the groups' tiles, 64 groups at a time: bounds
 // clamped into [0, M] and raised to the running maximum, a prefix sum of the
 // tile counts, and the lane whose range holds tm.  Returns the group (-1: past
