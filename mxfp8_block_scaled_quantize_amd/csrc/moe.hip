@@ -844,35 +844,35 @@ __global__ __launch_bounds__(64 * DW) void moe_count_kernel(const int32_t* __res
   for (int e = threadIdx.x; e <= E; e += 64 * DW) counts[(int64_t)blockIdx.x * (E + 1) + e] = hist[e];
 }
 
-template <bool ONE>
-__global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t run, int E,
+template <bool ONE, int W>
+__global__ __launch_bounds__(64 * W) void moe_place_kernel(const int32_t* __restrict__ ids, int64_t n, int64_t run, int E,
                                                             int32_t top_k, int bits, int runs,
                                                             const int32_t* __restrict__ counts,
                                                             int32_t* __restrict__ offsets, int32_t* __restrict__ token,
                                                             int32_t* __restrict__ position) {
-  // next row of (wave, expert) [DW][E + 1]; of all runs the total and of the
+  // next row of (wave, expert) [W][E + 1]; of all runs the total and of the
   // runs before this one the count per expert [E + 1] each
   extern __shared__ int32_t next[];
-  __shared__ int32_t wave_sum[DW];
-  int32_t* const total = next + DW * (E + 1);
+  __shared__ int32_t wave_sum[W];
+  int32_t* const total = next + W * (E + 1);   // not with ONE
   int32_t* const before = total + (E + 1);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   const int64_t lo = blockIdx.x * run, hi = lo + run < n ? lo + run : n;
-  const int64_t part = run / DW;      // a multiple of a piece
+  const int64_t part = run / W;      // a multiple of a piece
   const int64_t plo = lo + w * part;
   const int64_t phi = plo + part < hi ? plo + part : hi;
   int first[DB];                      // the wave's first batch
 #pragma unroll
   for (int b = 0; b < DB; b++) first[b] = plo + 64 * b + lane < phi ? bucket_of(ids[plo + 64 * b + lane], E) : 0;
-  for (int i = tid; i < (DW + 2) * (E + 1); i += 64 * DW) next[i] = 0;
+  for (int i = tid; i < (ONE ? W : W + 2) * (E + 1); i += 64 * W) next[i] = 0;
   __syncthreads();
   if (!ONE) {
     // threads in groups of a whole number of waves, each for every q-th run
     const int width = (E + 64) / 64 * 64;
-    const int groups = width <= 64 * DW ? 64 * DW / width : 1;
-    const int q = width <= 64 * DW ? tid / width : 0;
+    const int groups = width <= 64 * W ? 64 * W / width : 1;
+    const int q = width <= 64 * W ? tid / width : 0;
     if (q < groups)
-      for (int e = tid - q * width; e <= E; e += groups > 1 ? width : 64 * DW) {
+      for (int e = tid - q * width; e <= E; e += groups > 1 ? width : 64 * W) {
         int32_t all = 0, mine = 0;
         for (int r0 = q; r0 < runs; r0 += 32 * groups) {   // 32 loads under one latency
           int32_t c[32];
@@ -901,15 +901,15 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
       if (i0 + 64 * b + lane < phi) atomicAdd(&row[id[b]], 1);
   }
   __syncthreads();
-  // scan of the totals over the experts, 64 * DW at a time; then the first row
+  // scan of the totals over the experts, 64 * W at a time; then the first row
   // of every wave
   int32_t carry = 0;
-  for (int e0 = 0; e0 <= E; e0 += 64 * DW) {
+  for (int e0 = 0; e0 <= E; e0 += 64 * W) {
     const int e = e0 + tid;
-    int32_t here[DW], all = 0;
+    int32_t here[W], all = 0;
     if (e <= E) {
 #pragma unroll
-      for (int v = 0; v < DW; v++) {
+      for (int v = 0; v < W; v++) {
         here[v] = next[v * (E + 1) + e];
         if (ONE) all += here[v];
       }
@@ -920,7 +920,7 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     __syncthreads();
     int32_t start = carry + incl - all;
 #pragma unroll
-    for (int v = 0; v < DW; v++) {
+    for (int v = 0; v < W; v++) {
       const int32_t c = wave_sum[v];
       if (v < w) start += c;
       carry += c;
@@ -929,7 +929,7 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
       if (blockIdx.x == 0) offsets[e] = start;
       int32_t at = start + (ONE ? 0 : before[e]);
 #pragma unroll
-      for (int v = 0; v < DW; v++) {
+      for (int v = 0; v < W; v++) {
         next[v * (E + 1) + e] = at;
         at += here[v];
       }
@@ -949,8 +949,8 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
     for (int bit = 0; bit < bits; bit++)
 #pragma unroll
       for (int b = 0; b < P; b++) {
-        const uint64_t m = __ballot((id[b] >> bit) & 1);
-        same[b] &= ((id[b] >> bit) & 1) ? m : ~m;
+        const int mine = __builtin_amdgcn_sbfe(id[b], bit, 1);   // 0 or -1
+        same[b] &= ~(__ballot(mine) ^ (uint64_t)(int64_t)mine);
       }
 #pragma unroll
     for (int b = 0; b < P; b++) {
@@ -971,16 +971,23 @@ __global__ __launch_bounds__(64 * DW) void moe_place_kernel(const int32_t* __res
   }
 }
 
+// Waves of a lone workgroup: 16 where eight would have more than a piece each, as
+// long as 64 KB of LDS hold their counters.
+static int one_waves(int64_t n, int64_t E) { return n > 64 * DW && E <= 1000 ? 16 : DW; }
+
 // Slots of a workgroup: one batch a wave, more batches beyond kMaxRuns runs; alone
 // in whole pieces for every wave.
-static int64_t dispatch_run(int64_t n) {
-  if (n <= kOneBlock) return (n + 64 * DW - 1) / (64 * DW) * (64 * DW);
+static int64_t dispatch_run(int64_t n, int64_t E) {
+  if (n <= kOneBlock) {
+    const int64_t unit = 64 * one_waves(n, E);
+    return (n + unit - 1) / unit * unit;
+  }
   return ((n + kMaxRuns - 1) / kMaxRuns + kRun - 1) / kRun * kRun;
 }
 
 size_t moe_dispatch_workspace(int64_t n, int64_t E) {
   if (n <= kOneBlock) return 0;
-  const int64_t run = dispatch_run(n);
+  const int64_t run = dispatch_run(n, E);
   return (size_t)((n + run - 1) / run) * (size_t)(E + 1) * 4u;
 }
 
@@ -988,19 +995,23 @@ hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t
                                int32_t* position, int32_t* ws, hipStream_t stream) {
   int bits = 1;
   while ((1ll << bits) <= E) bits++;   // ids 0 .. E
-  const int64_t run = dispatch_run(n);
+  const int64_t run = dispatch_run(n, E);
   const int runs = n <= kOneBlock ? 1 : (int)((n + run - 1) / run);
-  const size_t lds = (size_t)(DW + 2) * (size_t)(E + 1) * 4u;   // at most 41 KB
+  const size_t counters = (size_t)(E + 1) * 4u;
   if (n <= kOneBlock) {
-    hipLaunchKernelGGL((moe_place_kernel<true>), dim3(1), dim3(64 * DW), lds, stream, ids, n, run, (int)E, top_k, bits, 1,
-                       nullptr, offsets, token, position);
+#define MOE_ONE(W)                                                                                                          \
+  hipLaunchKernelGGL((moe_place_kernel<true, W>), dim3(1), dim3(64 * W), W * counters, stream, ids, n, run, (int)E, top_k, \
+                     bits, 1, nullptr, offsets, token, position)
+    if (one_waves(n, E) == 16) MOE_ONE(16);
+    else MOE_ONE(DW);
+#undef MOE_ONE
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)runs), dim3(64 * DW), (size_t)(E + 1) * 4u, stream, ids, n, run,
+  hipLaunchKernelGGL(moe_count_kernel, dim3((unsigned)runs), dim3(64 * DW), counters, stream, ids, n, run,
                      (int)E, ws);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((moe_place_kernel<false>), dim3((unsigned)runs), dim3(64 * DW), lds, stream, ids, n, run, (int)E,
+  hipLaunchKernelGGL((moe_place_kernel<false, DW>), dim3((unsigned)runs), dim3(64 * DW), (DW + 2) * counters, stream, ids, n, run, (int)E,
                      top_k, bits, runs, ws, offsets, token, position);
   return hipGetLastError();
 }
