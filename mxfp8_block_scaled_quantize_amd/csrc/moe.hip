@@ -801,27 +801,30 @@ hipError_t launch_moe_route_backward(const void* logits, int dtype, int64_t T, i
 }
 
 // ------------------------------------------------------------------ dispatch
-// Stable counting sort.  A workgroup owns a run of slots, each of its 8 waves
-// a part of that run.  A wave counts its part per expert in LDS; with the
+// Stable counting sort.  A workgroup owns a run of slots, each of its 8 or 16
+// waves a part of that run.  A wave counts its part per expert in LDS; with the
 // totals of the workgroups before it (and of all experts before this one) the
 // count becomes the next free row of (wave, expert), and the wave walks its
 // part 64 slots at a time: lanes of the same expert find each other with one
 // ballot per bit of the id, a lane's rank is the number of such lanes below
 // it, and the last of them moves the counter on.  Nothing depends on the order
 // of waves or workgroups.  Up to kOneBlock slots a single workgroup does it
-// all; beyond that a first launch leaves every run's counts in the workspace
-// and each workgroup of the second adds up what it needs of them (at most 256
-// runs, so that this stays a few hundred KB of L2 reads).  A few MB at most:
-// latency decides, so ids are loaded four 64-slot pieces at a time and the
-// first batch stays in registers between counting and placing.  128 slots: 3.5
-// us; 131064: 2.7 + 7.5 us, of which 2 are the counts of all runs coming back from
-// behind the other XCDs' L2, 1.5 the ranks (two or sixteen waves, 1024 or 4096
-// slots a run: within 5 %).
+// all.  Up to kOneLaunch every workgroup counts the other runs itself (16384
+// slots: 7.7 us, with a launch of counts before it 8.2 and the host's 2.7; 32768:
+// 10.7 and 8.3).  Beyond that a first launch leaves every run's counts in the
+// workspace and each workgroup of the second adds up what it needs of them (at
+// most 256 runs, so that this stays a few hundred KB of L2 reads).  A few MB at
+// most: latency decides, so ids are loaded four 64-slot pieces at a time and the
+// first batch stays in registers between counting and placing.  128 slots: 2.8
+// us; 4096: 5.6 (with eight waves 7.4); 131064: 2.7 + 6.6 us, of which 2 are the
+// counts of all runs coming back from behind the other XCDs' L2, 1.5 the ranks
+// (two or sixteen waves, 1024 or 4096 slots a run: within 5 %).
 // Ids outside [0, E) are counted as expert E, whose rows come last.
 constexpr int DW = 8;                    // waves
 constexpr int DB = 4;                    // 64-slot pieces in a batch
 constexpr int64_t kRun = 64 * DW * DB;   // slots of a workgroup with one batch a wave
 constexpr int64_t kOneBlock = 2 * kRun;
+constexpr int64_t kOneLaunch = 4 * kOneBlock;
 constexpr int64_t kMaxRuns = 256;
 
 __device__ __forceinline__ int bucket_of(int id, int E) { return id >= 0 && id < E ? id : E; }
@@ -866,7 +869,18 @@ __global__ __launch_bounds__(64 * W) void moe_place_kernel(const int32_t* __rest
   for (int b = 0; b < DB; b++) first[b] = plo + 64 * b + lane < phi ? bucket_of(ids[plo + 64 * b + lane], E) : 0;
   for (int i = tid; i < (ONE ? W : W + 2) * (E + 1); i += 64 * W) next[i] = 0;
   __syncthreads();
-  if (!ONE) {
+  if (!ONE && !counts) {   // every workgroup counts all other runs itself
+    for (int64_t i0 = tid; i0 < n; i0 += 64 * W * 8) {
+      int id[8];
+#pragma unroll
+      for (int b = 0; b < 8; b++) id[b] = i0 + 64 * W * b < n ? bucket_of(ids[i0 + 64 * W * b], E) : 0;
+#pragma unroll
+      for (int b = 0; b < 8; b++) {
+        const int64_t i = i0 + 64 * W * b;
+        if (i < n && (i < lo || i >= hi)) atomicAdd(&(i < lo ? before : total)[id[b]], 1);
+      }
+    }
+  } else if (!ONE) {
     // threads in groups of a whole number of waves, each for every q-th run
     const int width = (E + 64) / 64 * 64;
     const int groups = width <= 64 * W ? 64 * W / width : 1;
@@ -911,9 +925,9 @@ __global__ __launch_bounds__(64 * W) void moe_place_kernel(const int32_t* __rest
 #pragma unroll
       for (int v = 0; v < W; v++) {
         here[v] = next[v * (E + 1) + e];
-        if (ONE) all += here[v];
+        if (ONE || !counts) all += here[v];
       }
-      if (!ONE) all = total[e];
+      if (!ONE) all += counts ? total[e] : before[e] + total[e];
     }
     const int32_t incl = scan64(all, OpAdd{});
     if (lane == 63) wave_sum[w] = incl;
@@ -939,54 +953,60 @@ __global__ __launch_bounds__(64 * W) void moe_place_kernel(const int32_t* __rest
   auto place = [&](int64_t i0, auto pieces) {
     constexpr int P = decltype(pieces)::value;
     int id[P];
-    uint64_t same[P];
+    uint32_t lo32[P], hi32[P];   // lanes of the same id
 #pragma unroll
     for (int b = 0; b < P; b++) {
       const int64_t i = i0 + 64 * b + lane;
       id[b] = i0 == plo ? first[b] : i < phi ? bucket_of(ids[i], E) : 0;
-      same[b] = __ballot(i < phi);
+      const uint64_t m = __ballot(i < phi);
+      lo32[b] = (uint32_t)m;
+      hi32[b] = (uint32_t)(m >> 32);
     }
     for (int bit = 0; bit < bits; bit++)
 #pragma unroll
       for (int b = 0; b < P; b++) {
-        const int mine = __builtin_amdgcn_sbfe(id[b], bit, 1);   // 0 or -1
-        same[b] &= ~(__ballot(mine) ^ (uint64_t)(int64_t)mine);
+        const uint32_t mine = (uint32_t)__builtin_amdgcn_sbfe(id[b], bit, 1);   // all bits of it
+        const uint64_t m = __ballot(mine);
+        lo32[b] &= ~((uint32_t)m ^ mine);
+        hi32[b] &= ~((uint32_t)(m >> 32) ^ mine);
       }
 #pragma unroll
     for (int b = 0; b < P; b++) {
       const int64_t i = i0 + 64 * b + lane;
       if (i < phi) {
-        const int32_t at = row[id[b]] + __popcll(same[b] & (((uint64_t)1 << lane) - 1));
+        const int32_t at = row[id[b]] + __builtin_amdgcn_mbcnt_hi(hi32[b], __builtin_amdgcn_mbcnt_lo(lo32[b], 0));
         // i < 2^31
         token[at] = id[b] < E ? (int32_t)((uint32_t)i / (uint32_t)top_k) : -1;
         position[i] = id[b] < E ? at : -1;
-        if ((same[b] >> lane) == 1) row[id[b]] = at + 1;   // the last lane of this id
+        const uint64_t same = lo32[b] | (uint64_t)hi32[b] << 32;
+        if ((same >> lane) == 1) row[id[b]] = at + 1;   // the last lane of this id
       }
       wave_lds_fence();
     }
   };
   for (int64_t i0 = plo; i0 < phi; i0 += 64 * DB) {
     if (phi - i0 <= 64) place(i0, std::integral_constant<int, 1>{});
+    else if (phi - i0 <= 128) place(i0, std::integral_constant<int, 2>{});
     else place(i0, std::integral_constant<int, DB>{});
   }
 }
 
-// Waves of a lone workgroup: 16 where eight would have more than a piece each, as
+// Waves of a workgroup: 16 where eight would have more than a piece each, as
 // long as 64 KB of LDS hold their counters.
-static int one_waves(int64_t n, int64_t E) { return n > 64 * DW && E <= 1000 ? 16 : DW; }
+static int waves_of(int64_t n, int64_t E) { return n > 64 * DW && n <= kOneLaunch && E <= 900 ? 16 : DW; }
 
 // Slots of a workgroup: one batch a wave, more batches beyond kMaxRuns runs; alone
 // in whole pieces for every wave.
 static int64_t dispatch_run(int64_t n, int64_t E) {
   if (n <= kOneBlock) {
-    const int64_t unit = 64 * one_waves(n, E);
+    const int64_t unit = 64 * waves_of(n, E);
     return (n + unit - 1) / unit * unit;
   }
   return ((n + kMaxRuns - 1) / kMaxRuns + kRun - 1) / kRun * kRun;
 }
 
 size_t moe_dispatch_workspace(int64_t n, int64_t E) {
-  if (n <= kOneBlock) return 0;
+  if (n <= kOneLaunch) return 0;
   const int64_t run = dispatch_run(n, E);
   return (size_t)((n + run - 1) / run) * (size_t)(E + 1) * 4u;
 }
@@ -998,12 +1018,12 @@ hipError_t launch_moe_dispatch(const int32_t* ids, int64_t n, int64_t E, int32_t
   const int64_t run = dispatch_run(n, E);
   const int runs = n <= kOneBlock ? 1 : (int)((n + run - 1) / run);
   const size_t counters = (size_t)(E + 1) * 4u;
-  if (n <= kOneBlock) {
-#define MOE_ONE(W)                                                                                                          \
-  hipLaunchKernelGGL((moe_place_kernel<true, W>), dim3(1), dim3(64 * W), W * counters, stream, ids, n, run, (int)E, top_k, \
-                     bits, 1, nullptr, offsets, token, position)
-    if (one_waves(n, E) == 16) MOE_ONE(16);
-    else MOE_ONE(DW);
+  if (n <= kOneLaunch) {
+#define MOE_ONE(ONE, W)                                                                                               \
+  hipLaunchKernelGGL((moe_place_kernel<ONE, W>), dim3((unsigned)runs), dim3(64 * W), (ONE ? W : W + 2) * counters, stream, \
+                     ids, n, run, (int)E, top_k, bits, runs, nullptr, offsets, token, position)
+    if (n <= kOneBlock) { if (waves_of(n, E) == 16) MOE_ONE(true, 16); else MOE_ONE(true, DW); }
+    else { if (waves_of(n, E) == 16) MOE_ONE(false, 16); else MOE_ONE(false, DW); }
 #undef MOE_ONE
     return hipGetLastError();
   }

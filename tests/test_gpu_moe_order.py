@@ -88,3 +88,18 @@ def test_experts_masked_by_the_bias(low, E, groups, T):
             want = _order(x, K, "sigmoid", bias, **kw)
             _, ids = moe.route(torch.from_numpy(x).cuda(), K, scores="sigmoid", bias=torch.from_numpy(bias).cuda(), **kw)
             assert np.array_equal(to_host(ids).view(np.int32), want), (group_top, top_groups)
+
+
+# around the borders of a lone workgroup, of one launch and of two, and pieces that end inside a wave's part
+@pytest.mark.parametrize("n", [64, 65, 512, 513, 1024, 1025, 1500, 2049, 4096, 4097, 6145, 20000, 32768, 32769, 70001])
+@pytest.mark.parametrize("E", [1, 7, 128, 900, 901, 1024])
+def test_dispatch_of_any_number_of_slots(n, E):
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe
+
+    import mx4_util as ref
+    rng = np.random.default_rng(n + E)
+    ids = rng.integers(-1, E + 1, (n, 1)).astype(np.int32)
+    log("dispatch n=%d E=%d" % (n, E))
+    for g, want in zip(moe.dispatch(torch.from_numpy(ids).cuda(), E), ref.dispatch(ids, E)):
+        assert np.array_equal(to_host(g).view(np.int32), want)
