@@ -1087,17 +1087,32 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* _
   else out[t * H + h] = from_f32<D>(acc[0]);
 }
 
-// How often a row of y is named.  Up to kOneCount rows and slots one workgroup
-// clears and counts (a launch of 3 us saved where the whole step takes 50).
-constexpr int64_t kOneCount = 8192;
-__global__ __launch_bounds__(1024) void moe_count_rows_kernel(const int32_t* __restrict__ pos, int n, int rows, int32_t* count) {
-  for (int i = threadIdx.x; i < rows; i += 1024) count[i] = 0;
-  __threadfence();   // the zeros are in L2, where the atomics work
+// How often a row of y is named.  Up to kOneCount slots a workgroup counts the
+// rows of its range in LDS and goes through all positions for that (a few
+// hundred KB of L2 reads): one launch, and no atomics on memory.  65528 slots and
+// rows: 6.7 us, with a clear and a launch of atomics 9.6; 262144: 22.9 and 16.0.
+constexpr int64_t kOneCount = 1 << 17;
+constexpr int kCountRange = 2048;
+__global__ __launch_bounds__(1024) void moe_count_rows_kernel(const int32_t* __restrict__ pos, int n, int rows,
+                                                              int32_t* __restrict__ count) {
+  __shared__ int32_t hist[kCountRange];
+  const int r0 = blockIdx.x * kCountRange;
+  const int here = rows - r0 < kCountRange ? rows - r0 : kCountRange;
+  for (int i = threadIdx.x; i < kCountRange; i += 1024) hist[i] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += 1024) {
-    const int p = pos[i];
-    if (p >= 0 && p < rows) atomicAdd(&count[p], 1);
+  constexpr int U = 16;   // loads in flight
+  for (int i0 = threadIdx.x; i0 < n; i0 += 1024 * U) {
+    int p[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) p[u] = i0 + 1024 * u < n ? pos[i0 + 1024 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+      const uint32_t at = (uint32_t)p[u] - (uint32_t)r0;   // below r0: far past the range
+      if (p[u] >= 0 && at < (uint32_t)here) atomicAdd(&hist[at], 1);
+    }
   }
+  __syncthreads();
+  for (int i = threadIdx.x; i < here; i += 1024) count[r0 + i] = hist[i];
 }
 __global__ __launch_bounds__(256) void moe_clear_kernel(int32_t* __restrict__ count, int64_t rows) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -1118,7 +1133,8 @@ __global__ __launch_bounds__(256) void moe_named_kernel(const int32_t* __restric
 // finds the others by going through the positions: right, and slow, for what
 // no dispatch produces).  The workgroups behind the tokens' own zero the rows
 // that nobody names.  8191 tokens x 8 x 4096: 219 us for 1.14 GB, 5.2 TB/s, and
-// 10 us to count who names whom.
+// 6.7 us to count who names whom; 8071 x 2 x 304: 7 us (18 with each slot's
+// position, weight and count read by itself).
 template <typename D, bool VEC, int TPT>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
     const typename D::T* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ pos,
@@ -1145,33 +1161,40 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
   const int l = threadIdx.x & (TPT - 1);
   if (t < T) {   // uniform in a wave, and in the workgroup where TPT is 256
     for (int k0 = 0; k0 < K; k0 += 8) {
-      int64_t p[8];
-      float wk[8], acc[8];
-      int own[8];   // 0: no row, 1: this slot's alone, 2: shared
+      // lane k of every eight looks after slot k0 + k: two latencies for all of them
+      const int64_t slot = t * K + k0 + (lane & 7);
+      const bool in = k0 + (lane & 7) < K;
+      int pv = in ? pos[slot] : -1;
+      const float wv = in ? w[slot] : 0.0f;
+      if (pv >= rows) pv = -1;
+      const int cv = dy && pv >= 0 ? count[pv] : 0;
+      const uint32_t named = (uint32_t)__ballot(pv >= 0) & 0xFFu;   // slots with a row,
+      const uint32_t alone = (uint32_t)__ballot(cv == 1) & 0xFFu;   // that nobody else names,
+      uint32_t shared = (uint32_t)__ballot(cv > 1) & 0xFFu;         // that others name too
+      auto row_of = [&](int k) { return (int64_t)__builtin_amdgcn_readlane(pv, k); };
+      auto weight_of = [&](int k) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(wv), k)); };
+      float acc[8];
 #pragma unroll
-      for (int k = 0; k < 8; k++) {
-        p[k] = k0 + k < K ? pos[t * K + k0 + k] : -1;
-        if (p[k] >= rows) p[k] = -1;
-        wk[k] = k0 + k < K ? w[t * K + k0 + k] : 0.0f;
-        own[k] = p[k] >= 0 && dy ? (count[p[k]] == 1 ? 1 : 2) : 0;
-        acc[k] = 0.0f;
-      }
+      for (int k = 0; k < 8; k++) acc[k] = 0.0f;
       for (int64_t h = (int64_t)l * V; h < H; h += TPT * V) {
+        u32x4 v[8], gv;
+        typename D::T sv[8];
         float g[V];
-        if constexpr (VEC) unpack<D>(*reinterpret_cast<const u32x4*>(dout + t * ldd + h), g);
+        if constexpr (VEC) gv = *reinterpret_cast<const u32x4*>(dout + t * ldd + h);
         else g[0] = to_f32<D>(dout[t * ldd + h]);
         if (dw) {
-          u32x4 v[8];
-          typename D::T sv[8];
 #pragma unroll
           for (int k = 0; k < 8; k++)
-            if (p[k] >= 0) {
-              if constexpr (VEC) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(y + p[k] * ldy + h));
-              else sv[k] = y[p[k] * ldy + h];
+            if ((named >> k) & 1) {
+              if constexpr (VEC) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(y + row_of(k) * ldy + h));
+              else sv[k] = y[row_of(k) * ldy + h];
             }
+        }
+        if constexpr (VEC) unpack<D>(gv, g);
+        if (dw) {
 #pragma unroll
           for (int k = 0; k < 8; k++)
-            if (p[k] >= 0) {
+            if ((named >> k) & 1) {
               float f[V];
               if constexpr (VEC) unpack<D>(v[k], f);
               else f[0] = to_f32<D>(sv[k]);
@@ -1181,56 +1204,61 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
         }
 #pragma unroll
         for (int k = 0; k < 8; k++)
-          if (own[k] == 1) {
+          if ((alone >> k) & 1) {
+            const float wk = weight_of(k);
             float f[V];
 #pragma unroll
-            for (int i = 0; i < V; i++) f[i] = wk[k] * g[i];
-            if constexpr (VEC) __builtin_nontemporal_store(pack<D>(f), reinterpret_cast<u32x4*>(dy + p[k] * H + h));
-            else dy[p[k] * H + h] = from_f32<D>(f[0]);
+            for (int i = 0; i < V; i++) f[i] = wk * g[i];
+            if constexpr (VEC) __builtin_nontemporal_store(pack<D>(f), reinterpret_cast<u32x4*>(dy + row_of(k) * H + h));
+            else dy[row_of(k) * H + h] = from_f32<D>(f[0]);
           }
       }
-#pragma unroll 1
-      for (int k = 0; k < 8; k++) {
-        if (own[k] != 2) continue;
-        const int64_t me = t * K + k0 + k;
+      while (shared) {
+        const int k = __builtin_ctz(shared);
+        shared &= shared - 1;
+        const int64_t p = row_of(k), me = t * K + k0 + k;
         bool earlier = false;
         for (int64_t i0 = 0; i0 < me && !earlier; i0 += 64)
-          earlier = __any(i0 + lane < me && pos[i0 + lane < me ? i0 + lane : 0] == p[k]);
+          earlier = __any(i0 + lane < me && pos[i0 + lane < me ? i0 + lane : 0] == p);
         if (earlier) continue;
         for (int64_t h = (int64_t)l * V; h < H; h += TPT * V) {
           float f[V];
 #pragma unroll
           for (int i = 0; i < V; i++) f[i] = 0.0f;
-          for (int64_t i = me; i < T * K; i++) {
-            if (pos[i] != p[k]) continue;
-            const int64_t ti = i / K;
-            float g[V];
-            if constexpr (VEC) unpack<D>(*reinterpret_cast<const u32x4*>(dout + ti * ldd + h), g);
-            else g[0] = to_f32<D>(dout[ti * ldd + h]);
+          // the loop over h leaves the wave's last lanes behind: positions by those at work
+          const uint64_t at_work = __ballot(true);
+          const int width = __popcll(at_work);   // lanes 0 .. width - 1
+          for (int64_t i0 = me; i0 < T * K; i0 += width) {
+            uint64_t hit = __ballot(i0 + lane < T * K && pos[i0 + lane < T * K ? i0 + lane : 0] == p);
+            while (hit) {
+              const int64_t i = i0 + __builtin_ctzll(hit);
+              hit &= hit - 1;
+              const int64_t ti = i / K;
+              float g[V];
+              if constexpr (VEC) unpack<D>(*reinterpret_cast<const u32x4*>(dout + ti * ldd + h), g);
+              else g[0] = to_f32<D>(dout[ti * ldd + h]);
 #pragma unroll
-            for (int j = 0; j < V; j++) f[j] = fmaf(w[i], g[j], f[j]);
+              for (int j = 0; j < V; j++) f[j] = fmaf(w[i], g[j], f[j]);
+            }
           }
-          if constexpr (VEC) *reinterpret_cast<u32x4*>(dy + p[k] * H + h) = pack<D>(f);
-          else dy[p[k] * H + h] = from_f32<D>(f[0]);
+          if constexpr (VEC) *reinterpret_cast<u32x4*>(dy + p * H + h) = pack<D>(f);
+          else dy[p * H + h] = from_f32<D>(f[0]);
         }
       }
       if (dw) {
+        float mine = 0.0f;   // lane k: slot k's sum over the wave
 #pragma unroll
-        for (int k = 0; k < 8; k++) acc[k] = lanes_reduce<64>(acc[k], OpAdd{});
+        for (int k = 0; k < 8; k++)
+          if ((named >> k) & 1) {
+            const float sum = lanes_reduce<64>(acc[k], OpAdd{});
+            mine = lane == k ? sum : mine;
+          }
         if (TPT == 64) {
-#pragma unroll
-          for (int k = 0; k < 8; k++)
-            if (lane == 0 && k0 + k < K) dw[t * K + k0 + k] = acc[k];
+          if (lane < 8 && in) dw[slot] = mine;
         } else {
-          if (lane == 0) {
-#pragma unroll
-            for (int k = 0; k < 8; k++) part[threadIdx.x >> 6][k] = acc[k];
-          }
+          if (lane < 8) part[threadIdx.x >> 6][lane] = mine;
           __syncthreads();
-          if (threadIdx.x < 8 && k0 + (int)threadIdx.x < K) {
-            const int k = threadIdx.x;
-            dw[t * K + k0 + k] = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
-          }
+          if (threadIdx.x < 8 && in) dw[slot] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
           __syncthreads();
         }
       }
@@ -1299,8 +1327,9 @@ static hipError_t combine_back_t(const void* y, int64_t rows, int64_t ldy, const
   const auto* yy = static_cast<const typename D::T*>(y);
   const auto* g = static_cast<const typename D::T*>(dout);
   auto* o = static_cast<typename D::T*>(dy);
-  if (dy && rows <= kOneCount && T * K <= kOneCount) {
-    hipLaunchKernelGGL(moe_count_rows_kernel, dim3(1), dim3(1024), 0, stream, pos, (int)(T * K), (int)rows, count);
+  if (dy && rows <= 2 * kOneCount && T * K <= kOneCount) {
+    hipLaunchKernelGGL(moe_count_rows_kernel, dim3((unsigned)((rows + kCountRange - 1) / kCountRange)), dim3(1024), 0, stream,
+                       pos, (int)(T * K), (int)rows, count);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   } else if (dy) {

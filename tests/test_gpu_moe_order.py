@@ -103,3 +103,54 @@ def test_dispatch_of_any_number_of_slots(n, E):
     log("dispatch n=%d E=%d" % (n, E))
     for g, want in zip(moe.dispatch(torch.from_numpy(ids).cuda(), E), ref.dispatch(ids, E)):
         assert np.array_equal(to_host(g).view(np.int32), want)
+
+
+# rows and slots around the ranges that a workgroup counts, and past the sizes that one launch does
+@pytest.mark.parametrize("T,K,rows", [(1024, 2, 2047), (1024, 2, 2048), (683, 3, 2049), (1, 1, 5000), (3000, 1, 1), (8191, 8, 65528),
+                                      (32768, 8, 262144), (32769, 8, 100), (100, 1, 524289)])
+@pytest.mark.parametrize("kind", ["distinct", "dropped"])
+def test_combine_gradient_of_any_number_of_rows(T, K, rows, kind):
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe
+
+    H = 8
+    log("combine gradient T=%d K=%d rows=%d %s" % (T, K, rows, kind))
+    rng = np.random.default_rng(T + rows)
+    n = T * K
+    position = np.full(n, -1, np.int32)
+    named = min(n, rows) if kind == "distinct" else min(n, rows) // 2
+    position[rng.permutation(n)[:named]] = rng.permutation(rows)[:named]
+    position = position.reshape(T, K)
+    y = rng.integers(-4, 5, (rows, H)).astype(np.float32)
+    w = rng.integers(-4, 5, (T, K)).astype(np.float32)
+    g = rng.integers(-4, 5, (T, H)).astype(np.float32)      # every product and sum is exact
+    ty, tw = (torch.from_numpy(a).cuda().requires_grad_() for a in (y, w))
+    out = moe.combine(ty, torch.from_numpy(position).cuda(), tw)
+    dy, dw = (t.cpu().numpy() for t in torch.autograd.grad(out, (ty, tw), torch.from_numpy(g).cuda()))
+    t, k = np.nonzero(position >= 0)
+    want_dy, want_dw = np.zeros_like(y), np.zeros_like(w)
+    want_dy[position[t, k]] = w[t, k][:, None] * g[t]
+    want_dw[t, k] = (y[position[t, k]] * g[t]).sum(1)
+    assert np.array_equal(dy, want_dy) and np.array_equal(dw, want_dw)
+
+
+# rows that several slots name, at sizes where a slot-by-slot search would take seconds
+@pytest.mark.parametrize("T,K,rows,H", [(20000, 4, 40000, 8), (20000, 4, 300, 40), (5000, 8, 3, 264), (3000, 5, 7500, 2056)])
+def test_combine_gradient_of_many_shared_rows(T, K, rows, H):
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe
+
+    log("combine gradient, shared rows T=%d K=%d rows=%d H=%d" % (T, K, rows, H))
+    rng = np.random.default_rng(T + rows)
+    position = (rng.permutation(T * K) % rows).reshape(T, K).astype(np.int32)
+    y = rng.integers(-4, 5, (rows, H)).astype(np.float32)
+    w = rng.integers(-4, 5, (T, K)).astype(np.float32)
+    g = rng.integers(-4, 5, (T, H)).astype(np.float32)      # sums of whole numbers below 2^24: exact in any order
+    ty, tw = (torch.from_numpy(a).cuda().requires_grad_() for a in (y, w))
+    out = moe.combine(ty, torch.from_numpy(position).cuda(), tw)
+    dy, dw = (t.cpu().numpy() for t in torch.autograd.grad(out, (ty, tw), torch.from_numpy(g).cuda()))
+    want_dy = np.zeros_like(y)
+    for k in range(K):
+        np.add.at(want_dy, position[:, k], w[:, k:k + 1] * g)
+    want_dw = np.stack([(y[position[:, k]] * g).sum(1) for k in range(K)], 1)
+    assert np.array_equal(dy, want_dy) and np.array_equal(dw, want_dw)
