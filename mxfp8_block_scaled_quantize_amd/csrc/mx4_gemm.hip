@@ -142,6 +142,14 @@ static hipError_t launch_rows(const Mx4Gemm& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Whether workgroups take 16 columns instead of 32: where they are still at most
+// one a compute unit, and K is so long that a wave's part of it is in flight at
+// once with 16 columns (8 slices) and not with 32 (4).  5 x 256 x 7168: 5.3 us, with
+// 32 columns 6.9; 29 x 1024 x 6144: 6.6 and 8.4; K = 4096 and less: 7 % slower.
+static bool narrow_rows(const Mx4Gemm& g, int64_t bm) {
+  return !g.offsets && g.epilogue != EPI_SWIGLU && g.K > 4096 && g.N / 16 * row_blocks(g, bm) <= 256;
+}
+
 // ---- choice of the kernel by estimated time.  Every variant was timed, as
 // launches in a graph, on 1500 products: 1 .. 16384 rows, 256 .. 16384 columns,
 // K 256 .. 8192, dense and in 2 .. 64 ragged groups, with and without SwiGLU.  The
@@ -201,7 +209,7 @@ static Choice choose(const Mx4Gemm& g) {
     if (row_blocks(g, bm) > 65535) continue;   // the grid's second dimension
     const auto& f = few[i];
     const double fill = rows < bm ? rows / bm : 1;
-    const double us = f.start + k * (f.k + fill * f.fill) +
+    const double us = (f.start + k * (f.k + fill * f.fill)) * (narrow_rows(g, bm) ? 0.62 : 1) +
                       (rounds(blocks(bm, 32, true), f.part) - 1) * (f.start + k * (f.more_k + fill * f.more_fill));
     offer(Mx4Tile::kRows, 1 << i, f.call + longer(us, b_mb / f.tb_s));
   }
@@ -237,6 +245,9 @@ static hipError_t launch_rows_e(const Mx4Gemm& g, hipStream_t stream) {
 }
 template <int MB>
 static hipError_t launch_rows_w(const Mx4Gemm& g, hipStream_t stream) {
+  if (narrow_rows(g, 16 * MB))
+    return g.epilogue == EPI_ACC ? launch_rows<MB, 1, 8, false, EPI_ACC>(g, stream)
+                                 : launch_rows<MB, 1, 8, false, EPI_NONE>(g, stream);
   // eight waves where K is long enough to be split and workgroups are few (one
   // row x 2048 columns, K = 8192: 6.3 us, with four waves 6.8; K = 1024, 256 x
   // 4096: 10.4 and 9.8; 32 experts of 2048 x 4096: 23 and 20)

@@ -403,3 +403,10 @@ def test_gemm_of_other_tiles(M, N, K, mode):
 @pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
 def test_grouped_gemm_of_other_tiles(counts, N, K, mode):
     test_grouped_gemm(counts, N, K, mode)
+
+
+# few rows, workgroups of 16 columns (long K) and the sizes next to it
+@pytest.mark.parametrize("M,N,K", [(1, 32, 4224), (5, 288, 7168), (33, 1056, 6272), (29, 1024, 8192), (16, 4096, 4224), (17, 4128, 4224)])
+@pytest.mark.parametrize("mode", ["plain", "accumulate", "swiglu"])
+def test_gemm_of_few_rows_and_long_k(M, N, K, mode):
+    test_gemm(M, N, K, mode)
