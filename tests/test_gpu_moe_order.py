@@ -154,3 +154,35 @@ def test_combine_gradient_of_many_shared_rows(T, K, rows, H):
         np.add.at(want_dy, position[:, k], w[:, k:k + 1] * g)
     want_dw = np.stack([(y[position[:, k]] * g).sum(1) for k in range(K)], 1)
     assert np.array_equal(dy, want_dy) and np.array_equal(dw, want_dw)
+
+
+def test_outputs_of_one_call_are_independent_tensors():
+    """They lie in one allocation, but alias nothing and stand on their own."""
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import moe, mxfp4
+
+    x = torch.randn((33, 256), device="cuda").bfloat16()
+    logits = torch.randn((33, 24), device="cuda")
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            w, ids = moe.route(logits, 3)
+            plan = moe.dispatch(ids, 24)
+            q = mxfp4.quantize(x, packed=True)
+            groups = [(w, ids), tuple(plan), tuple(q.values())]
+        for group in groups:
+            spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in group)
+            assert all(a[1] <= b[0] for a, b in zip(spans, spans[1:]))
+            before = [t.clone() for t in group]
+            for t in group:
+                assert t.is_contiguous() and t.data_ptr() % 256 == 0 and not t._is_view()
+                assert t.is_inference() == (mode is torch.inference_mode)
+            with mode():
+                for i, t in enumerate(group):
+                    t.zero_()
+                    assert all(torch.equal(a, b) for a, b in list(zip(group, before))[i + 1:])
+    w, ids = moe.route(logits, 3)
+    leaf = w.requires_grad_()
+    (leaf * 2).sum().backward()
+    assert torch.equal(leaf.grad, torch.full_like(w, 2.0))
+    del w, leaf
+    assert int(ids.min()) >= 0        # outlives the others of its call
