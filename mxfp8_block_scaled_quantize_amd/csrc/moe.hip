@@ -1091,6 +1091,10 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* _
 // rows of its range in LDS and goes through all positions for that (a few
 // hundred KB of L2 reads): one launch, and no atomics on memory.  65528 slots and
 // rows: 6.7 us, with a clear and a launch of atomics 9.6; 262144: 22.9 and 16.0.
+// Up to kNoCount slots nothing is counted ahead: the gradients' waves look through
+// the positions themselves (256 x 4 x 1024, all gradients: 4.8 us, with a launch of
+// counts 6.7; 1024 x 4: 12.7 and 8.5) and the host has a launch less.
+constexpr int64_t kNoCount = 1024;
 constexpr int64_t kOneCount = 1 << 17;
 constexpr int kCountRange = 2048;
 __global__ __launch_bounds__(1024) void moe_count_rows_kernel(const int32_t* __restrict__ pos, int n, int rows,
@@ -1143,10 +1147,23 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
   constexpr int V = VEC ? D::V : 1;
   constexpr int PER = 256 / TPT;
   __shared__ float part[4][8];
+  __shared__ int32_t has_slot[256];
   const int lane = threadIdx.x & 63;
   if ((int64_t)blockIdx.x >= token_blocks) {   // rows without a slot; launched with dy alone
-    const int64_t r0 = ((int64_t)blockIdx.x - token_blocks) * 256 + (threadIdx.x & ~63);
-    uint64_t none = __ballot(r0 + lane < rows && count[r0 + lane < rows ? r0 + lane : 0] == 0);
+    const int64_t rb = ((int64_t)blockIdx.x - token_blocks) * 256, r0 = rb + (threadIdx.x & ~63);
+    const bool in = r0 + lane < rows;
+    if (count) {
+      has_slot[threadIdx.x] = in ? count[r0 + lane] : 1;
+    } else {
+      has_slot[threadIdx.x] = !in;
+      __syncthreads();
+      for (int64_t i = threadIdx.x; i < T * K; i += 256) {
+        const int64_t at = (int64_t)pos[i] - rb;
+        if (at >= 0 && at < 256) has_slot[at] = 1;
+      }
+      __syncthreads();
+    }
+    uint64_t none = __ballot(has_slot[threadIdx.x] == 0);
     while (none) {
       const int64_t r = r0 + __builtin_ctzll(none);
       none &= none - 1;
@@ -1167,7 +1184,24 @@ __global__ __launch_bounds__(256) void moe_combine_backward_kernel(
       int pv = in ? pos[slot] : -1;
       const float wv = in ? w[slot] : 0.0f;
       if (pv >= rows) pv = -1;
-      const int cv = dy && pv >= 0 ? count[pv] : 0;
+      int cv = dy && count && pv >= 0 ? count[pv] : 0;
+      if (dy && !count) {   // the wave counts its rows among all positions itself
+        int n[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int64_t i0 = 0; i0 < T * K; i0 += 256) {
+          int q[4];
+#pragma unroll
+          for (int u = 0; u < 4; u++) q[u] = i0 + 64 * u + lane < T * K ? pos[i0 + 64 * u + lane] : -1;
+#pragma unroll
+          for (int k = 0; k < 8; k++) {
+            if (k0 + k >= K) break;
+            const int p = __builtin_amdgcn_readlane(pv, k);
+#pragma unroll
+            for (int u = 0; u < 4; u++) n[k] += __popcll(__ballot(q[u] == p));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) cv = pv >= 0 && (lane & 7) == k ? n[k] : cv;
+      }
       const uint32_t named = (uint32_t)__ballot(pv >= 0) & 0xFFu;   // slots with a row,
       const uint32_t alone = (uint32_t)__ballot(cv == 1) & 0xFFu;   // that nobody else names,
       uint32_t shared = (uint32_t)__ballot(cv > 1) & 0xFFu;         // that others name too
@@ -1327,7 +1361,9 @@ static hipError_t combine_back_t(const void* y, int64_t rows, int64_t ldy, const
   const auto* yy = static_cast<const typename D::T*>(y);
   const auto* g = static_cast<const typename D::T*>(dout);
   auto* o = static_cast<typename D::T*>(dy);
-  if (dy && rows <= 2 * kOneCount && T * K <= kOneCount) {
+  if (T * K <= kNoCount) {
+    count = nullptr;
+  } else if (dy && rows <= 2 * kOneCount && T * K <= kOneCount) {
     hipLaunchKernelGGL(moe_count_rows_kernel, dim3((unsigned)((rows + kCountRange - 1) / kCountRange)), dim3(1024), 0, stream,
                        pos, (int)(T * K), (int)rows, count);
     const hipError_t e = hipGetLastError();

@@ -186,3 +186,9 @@ def test_outputs_of_one_call_are_independent_tensors():
     assert torch.equal(leaf.grad, torch.full_like(w, 2.0))
     del w, leaf
     assert int(ids.min()) >= 0        # outlives the others of its call
+
+
+# the number of slots up to which the gradients' waves count for themselves, and one past it
+@pytest.mark.parametrize("T,K,rows,H", [(1024, 1, 1024, 40), (1025, 1, 1025, 40), (113, 9, 1500, 264), (60, 17, 700, 2056), (1024, 1, 7, 8), (3, 64, 100, 33)])
+def test_combine_gradient_of_few_slots(T, K, rows, H):
+    test_combine_gradient_of_many_shared_rows(T, K, rows, H)
