@@ -12,7 +12,9 @@
 // Measured and not kept: deeper rings (64 x 64 with six slots 8.6 us where three
 // took 8.3; 128 x 128 with four, one workgroup a compute unit, 60 us where two
 // took 45), fragments read one step ahead into a second set of registers (7.1 us
-// where 6.3), 128 x 256 tiles (51 us where 128 x 128 takes 45).
+// where 6.3), 128 x 256 tiles (51 us where 128 x 128 takes 45); over 600 products:
+// two slots for the two smaller tiles (5 % slower), a second barrier a step that
+// frees its slot for one more step of loads (1 to 3 % slower).
 #include "launch.h"
 #include "mx4_gemm.h"
 
