@@ -45,7 +45,7 @@ extern "C" {
  * scores in 64 bits, not of their 32-bit roundings; without a bias it is the
  * logits' own.  The sums, weights and gradients are 32-bit.
  * A logit of -inf has score 0 (a row of nothing else has scores and weights
- * of 0).  NaN or +inf under softmax make the row's weights NaN, under sigmoid a
+ * of 0), and a score below fp32's normal range (2^-126) may be given as 0.  NaN or +inf under softmax make the row's weights NaN, under sigmoid a
  * NaN has a NaN score.  A choice of NaN is ordered below every other one, so
  * ids are always top_k different experts.
  *

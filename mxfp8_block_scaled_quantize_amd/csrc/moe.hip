@@ -146,14 +146,16 @@ __device__ __forceinline__ void wave_lds_fence() {
 }
 
 // -------------------------------------------------------------------- scores
-// exp in 32 bits with the product x log2(e) kept in two parts, so that the
-// result is within about 2 ulp (the plain exp2(x log2 e) loses |x| / 2 ulp).
+// exp in 32 bits with the product x log2(e) kept in two parts, so that a result
+// in fp32's normal range is within about 2 ulp (the plain exp2(x log2 e) loses
+// |x| / 2 ulp).  Past the range it is +inf or 0, for NaN it is NaN.
 __device__ __forceinline__ float exp_of(float x) {
   const float h = x * 1.44269504088896341f;
   const float l = fmaf(x, 1.92596299e-08f, fmaf(x, 1.44269504088896341f, -h));
   const float e = __builtin_amdgcn_exp2f(h);
-  // h of +-inf (or beyond the range) leaves l undefined: the result is e itself
-  return fabsf(h) < 150.0f ? fmaf(e * l, 0.69314718055994531f, e) : e;
+  // from h = 128 on e is +inf, which no correction may touch (inf - inf); below
+  // -128 there is nothing left to correct, and of +-inf and NaN l is undefined
+  return fabsf(h) < 128.0f ? fmaf(e * l, 0.69314718055994531f, e) : e;
 }
 __device__ __forceinline__ float rcp_of(float x) { return __builtin_amdgcn_rcpf(x); }
 
@@ -277,7 +279,8 @@ struct RouteLds {
 // order is the logits' own.  Else the choice is made in 32 bits, and nothing is
 // written for a row in which two values that matter are closer than what they
 // can be off by (returned for all its lanes):
-//   u = 2^-24.  exp_of is within 4 u of its value, rcp_of within 2 u.
+//   u = 2^-24.  exp_of is within 4 u of its value, rcp_of within 2 u (or both
+//   are 0 or +inf for a score below 2^-126, far less than any of these bounds).
 //   softmax  a score s is within (18 + VPL) u s: 4 u of its own exp, 4 u of the
 //            sum's terms, (VPL + 6) u of adding them up, 3 u of 1 / sum and the
 //            product, and the rounding of x - max, |d| e^-|d| u <= 0.4 u.  The
