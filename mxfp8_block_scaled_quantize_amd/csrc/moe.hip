@@ -321,6 +321,12 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
     const float off = a.sigmoid ? 8 * U : (9 + VPL / 2) * U * fminf(1.0f, 4.0f * largest);   // of one group
     auto value = [&](const Top2& t) { return two ? t.m1 + t.m2 : t.m1; };
     auto error = [&](const Top2& t) { return off + 2 * U * (fabsf(t.m1) + (two ? fabsf(t.m2) : 0.0f)); };
+    // biases next to the type's largest or lowest value: a sum that 32 bits do
+    // not hold says nothing about its place among the others of its kind
+    auto overflow = [&](const Top2& t) {
+      return two && fabsf(t.m1) < INFINITY && fabsf(t.m2) < INFINITY && fabsf(t.m1 + t.m2) == INFINITY;
+    };
+    bool past = false;
     float low = INFINITY, high = -INFINITY;   // smallest an open group may be, largest a closed one
     if (l < 4 && a.groups + l < kMaxGroups) gval[a.groups + l] = -INFINITY;
     if (a.group_lanes) {   // in registers
@@ -333,6 +339,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
       if (a.group_lanes > 8) t.merge_dpp<0x140>();
       const int g = l / a.group_lanes;
       const float mine = value(t);
+      past = overflow(t);
       if (g < a.groups && (l & (a.group_lanes - 1)) == 0) gval[g] = mine;
       wave_lds_fence();
       const bool open = rank_of(gval, a.groups, g, mine) < a.top_groups;
@@ -362,6 +369,7 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
         if (g < a.groups && (l & (lg - 1)) == 0) {
           gval[g] = value(t);
           keep[g] = __float_as_uint(error(t));
+          past = past || overflow(t);
         }
       }
       wave_lds_fence();
@@ -385,10 +393,10 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
         if (!open && e0 + j < a.E) key[j] = 1;
       }
     }
-    if (!SURE) {   // an infinite value leaves NaN, which says nothing: infinities are equal in 64 bits too
+    if (!SURE) {   // an infinite choice leaves NaN, which says nothing: infinities are equal in 64 bits too
       low = lanes_reduce<LPR>(fminf(low, INFINITY), OpMin{});
       high = lanes_reduce<LPR>(fmaxf(high, -INFINITY), OpMax{});
-      doubt = low < high;
+      doubt = past || low < high;
     }
     wave_lds_fence();
   }
