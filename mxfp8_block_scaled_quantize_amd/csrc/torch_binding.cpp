@@ -244,7 +244,14 @@ Tensor output(const Tensor* out, int64_t rows, int64_t cols, c10::Device dev, co
   if (out->scalar_type() != at::kBFloat16 || out->sizes() != at::IntArrayRef{rows, cols} || out->stride(1) != 1 ||
       out->device() != dev)
     refuse(text);
+  if (out->requires_grad() && at::GradMode::is_enabled())
+    refuse("out requires a gradient, which this operator does not have: pass it with gradients disabled");
   return *out;
+}
+// The kernel has written a caller's tensor behind autograd's back: what was saved
+// of it for a backward pass is stale.
+void written(const Tensor* out) {
+  if (out && !out->is_inference()) torch::autograd::impl::bump_version(*out);
 }
 
 // dequantize(q, scales, out)
@@ -267,6 +274,7 @@ PyObject* dequantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(mxfp4_dequantize(q.const_data_ptr<uint8_t>(), s.const_data_ptr(), R, K, o.data_ptr(), ld(o),
                            packed ? MXFP4_PACKED_SCALES : 0, stream_of(dev)),
           "mxfp4_dequantize");
+    written(out);
     return wrap(o);
   });
 }
@@ -316,6 +324,7 @@ PyObject* product(PyObject*, PyObject* const* v, Py_ssize_t n) {
             "mxfp4_grouped_gemm");
     else
       check(mxfp4_gemm(pa, sa, pb, sb, c.data_ptr(), ld(c), M, N, K, flags, stream_of(dev)), "mxfp4_gemm");
+    written(out);
     return wrap(c);
   });
 }

@@ -5,7 +5,9 @@ the block-scaled products, dense and grouped.
 ``dequantize``, ``gemm`` and ``grouped_gemm`` check their tensors, allocate the
 outputs and call it (in the extension module ``_mx_torch``).  Codes are uint8, two to a byte (lower index in the low nibble);
 packed scale words are int32 [K / 128, rows], as for MXFP8.  Every step runs in
-the HIP kernels of ``libmxfp8.so``; there is no fallback.
+the HIP kernels of ``libmxfp8.so``; there is no fallback.  A tensor passed as
+``out`` counts as modified in place; one that requires a gradient is refused
+while gradients are enabled.
 """
 
 from __future__ import annotations
