@@ -280,6 +280,14 @@ def quantize(x, rowwise=True, colwise=False, dbias=False, amax=False, packed=Fal
     return out
 
 
+def _written(out):
+    """A kernel has written the caller's tensor `out` behind autograd's back:
+    move its version, so that a value saved of it for backward is not used."""
+    import torch
+    if out is not None:
+        torch.autograd.graph.increment_version(out)
+
+
 def _require(t, name, dtype, shape=None, device=None):
     """Host-side checks of a tensor handed to the C ABI as a dense array."""
     import torch
@@ -360,6 +368,7 @@ def gemm(a, a_packed, b, b_packed, out=None, accumulate=False, sqrelu=False, gel
             mxfp8_gemm_bias(a, a_packed, b, b_packed, bias, c, c.stride(0), M, N, K, flags, stream)
         else:
             mxfp8_gemm_ex(a, a_packed, b, b_packed, c, c.stride(0), M, N, K, flags, stream)
+    _written(out)
     return c
 
 
@@ -418,4 +427,5 @@ def grouped_gemm(a, a_packed, b, b_packed, offsets, out=None, accumulate=False, 
                                     stream)
         else:
             mxfp8_grouped_gemm_ex(a, a_packed, b, b_packed, offsets, G, c, c.stride(0), M, N, K, flags, stream)
+    _written(out)
     return c
