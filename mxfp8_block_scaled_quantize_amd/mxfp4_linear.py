@@ -5,9 +5,14 @@
     wgrad   dW = dy^T x   A = dy columnwise copy [N][M],  B = x columnwise copy [K][M]
 
 As in the MXFP8 layer, columnwise copies are stored transposed, one pass makes
-both copies, only the copies a product reads are made, and the weight's copies
-are kept until the parameter changes.  Values are rounded to nearest, gradients
-included.  x [.., K] and W [N, K] BF16 with tokens, K and N multiples of 128.
+both copies, and only the copies a product reads are made.  Values are rounded
+to nearest, gradients included.  x [.., K] and W [N, K] BF16 with tokens, K and N
+multiples of 128.
+
+The weight is quantized in every forward pass, from its value of that moment on
+the stream of that pass: a copy kept from an earlier call could be stale (a write
+through ``.data`` leaves no trace) or not yet written on this stream.  A program
+whose weight stays says so with ``freeze_weight``.
 """
 
 import torch
@@ -33,6 +38,10 @@ def _matrix(x, weight):
         raise ValueError("MXFP4 linear needs tokens, in- and out-features to be multiples of 128 "
                          "(got M=%d, K=%d, N=%d)" % (M, K, N))
     return x2
+
+
+def _alike(old, new):
+    return old is not None and new is not None and old.shape == new.shape and old.device == new.device
 
 
 class MXFP4LinearFunction(torch.autograd.Function):
@@ -65,6 +74,9 @@ class MXFP4LinearFunction(torch.autograd.Function):
         return dx, dw, None
 
 
+_NO_COPIES = (None, None, None, None)
+
+
 class MXFP4Linear(torch.nn.Module):
     """y = x W^T with MXFP4 fprop, dgrad and wgrad.  Without a gradient to come
     any number of tokens is allowed (no copy is reduced over them)."""
@@ -77,24 +89,65 @@ class MXFP4Linear(torch.nn.Module):
         w = torch.empty((out_features, in_features), dtype=torch.bfloat16, device=device)
         torch.nn.init.normal_(w, std=in_features ** -0.5)
         self.weight = torch.nn.Parameter(w)
-        self._wq_key = None
-        self._wq = None
+        self._wq, self._wq_of = _NO_COPIES, ()   # frozen copies and (in a tuple) the parameter they are of
+
+    def freeze_weight(self, colwise=False):
+        """Quantize the weight now, for all later calls that need no gradient of
+        it (colwise=True: the transposed copy too, which the input's gradient
+        reads).  Until the next freeze_weight or thaw_weight the layer does not
+        look at the parameter; loading a state dict, moving the module and
+        replacing the parameter end it too.  Copies of the same shape are written in
+        place, so a graph captured with them follows.  Waits for the device before
+        and after, so that they can be used on any stream; not during a capture."""
+        w = self.weight.detach()
+        if w.is_cuda and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("freeze_weight cannot run while a graph is captured")
+        # usable in a later backward pass even if this is called in inference mode
+        with torch.inference_mode(False), torch.no_grad():
+            old = self._wq if self._is_frozen() else _NO_COPIES
+            fresh = _copies(w.contiguous(), True, colwise or old[2] is not None)
+            self._wait(w)
+            self._wq = tuple(o.copy_(t) if _alike(o, t) else t for o, t in zip(old, fresh))
+            self._wq_of = (self.weight,)
+            self._wait(w)
+        return self
+
+    def thaw_weight(self):
+        """Give up the copies of freeze_weight, once the device is done with them."""
+        if self._wq[0] is not None:
+            self._wait(self._wq[0])
+        self._wq, self._wq_of = _NO_COPIES, ()
+        return self
+
+    @staticmethod
+    def _wait(t):
+        if t.is_cuda:
+            torch.cuda.synchronize(t.device)
+
+    def _is_frozen(self):
+        return bool(self._wq_of) and self._wq_of[0] is self.weight
+
+    def _apply(self, *args, **kwargs):
+        self.thaw_weight()
+        return super()._apply(*args, **kwargs)
+
+    def _load_from_state_dict(self, *args, **kwargs):
+        self.thaw_weight()
+        return super()._load_from_state_dict(*args, **kwargs)
 
     def quantized_weight(self, colwise=True):
-        """The weight's copies, made again only when the parameter's storage,
-        shape or version counter has changed (or the transposed one is wanted
-        for the first time)."""
-        w = self.weight
-        key = (w.data_ptr(), w.device, tuple(w.shape), w._version)
-        if self._wq is None or self._wq_key != key or (colwise and self._wq[2] is None):
-            with torch.no_grad():
-                self._wq = _copies(w.detach().contiguous(), True, colwise)
-            self._wq_key = key
-        return self._wq
+        """(q_row, p_row, q_colT, p_colT): the frozen copies, or those of the
+        parameter's present value (the transposed one None without colwise)."""
+        if self._is_frozen() and not (colwise and self._wq[2] is None):
+            return self._wq
+        with torch.no_grad():
+            return _copies(self.weight.detach().contiguous(), True, colwise)
 
     def forward(self, x):
         if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):
-            return MXFP4LinearFunction.apply(x, self.weight, self.quantized_weight())
+            # a weight in training is quantized there, a frozen one may be kept
+            frozen = self.quantized_weight(x.requires_grad) if not self.weight.requires_grad else None
+            return MXFP4LinearFunction.apply(x, self.weight, frozen)
         if x.dtype != torch.bfloat16 or x.shape[-1] != self.in_features:
             raise ValueError("input must be BF16 with %d features" % self.in_features)
         q = quantize(x.reshape(-1, x.shape[-1]).contiguous(), packed=True)
