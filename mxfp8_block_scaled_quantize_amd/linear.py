@@ -19,9 +19,13 @@ Shapes: x [M, K], W [N, K] BF16 with M, N and K multiples of 128 (each of the
 three GEMMs reduces over one of them).
 
 ``MXFP8Linear`` keeps the weight's quantization (both copies) between calls
-and quantizes the weight again only when the parameter changes: its storage,
-shape or version counter (every in-place update, an optimizer step included,
-bumps the counter).  Micro-batches between two weight updates reuse one
+and quantizes the weight again only when the parameter changes: another
+parameter or storage, shape or version counter (every in-place update, an
+optimizer step included, bumps the counter; a write through ``.data`` or a raw
+pointer does not: call ``forget_quantized_weight`` after one).  The copies are
+used on any stream, after the stream that makes them; a graph capture makes its
+own, so that a replay follows the weight.
+Micro-batches between two weight updates reuse one
 quantization.  Only the copies a GEMM will read are made: without any
 gradient (grad mode off, or no input that requires one) the module's forward
 quantizes the input rowwise only; x's columnwise copy is made only when the
@@ -150,23 +154,61 @@ class MXFP8Linear(torch.nn.Module):
                      if bias else None)
         if fuse_wgrad_accumulation:
             self.weight.main_grad = torch.zeros_like(w)
-        self._wq_key = None
+        self.forget_quantized_weight()
+
+    def forget_quantized_weight(self):
+        """Quantize the weight again in the next call."""
         self._wq = None
+        # the parameter, an alias that keeps its storage from being handed out
+        # again, its version; the stream of the copies and the event behind them
+        self._wq_key = self._wq_stream = self._wq_ready = None
+
+    def _apply(self, *args, **kwargs):
+        self.forget_quantized_weight()
+        return super()._apply(*args, **kwargs)
+
+    def __getstate__(self):   # events belong to this process
+        return {**self.__dict__, "_wq": None, "_wq_key": None, "_wq_stream": None, "_wq_ready": None}
+
+    def _is_current(self, w):
+        if self._wq is None:
+            return False
+        parameter, alias, version = self._wq_key
+        return (parameter is w and alias.data_ptr() == w.data_ptr() and alias.device == w.device
+                and alias.shape == w.shape and version == w._version)
+
+    def _keeps_copies(self):
+        # the copies of a capture hold nothing until its replay; inference tensors have no version
+        w = self.weight
+        return not (w.is_inference() or (w.is_cuda and torch.cuda.is_current_stream_capturing()))
+
+    def _quantize_weight(self):
+        # not inference tensors, which no later backward pass could use
+        with torch.inference_mode(False), torch.no_grad():
+            return _quantize_both(self.weight.detach().contiguous())
 
     def quantized_weight(self):
         """Both MXFP8 copies of the weight, quantized again only when the
-        parameter's storage, shape or version counter has changed."""
+        parameter, its storage, shape or version counter has changed."""
         w = self.weight
-        key = (w.data_ptr(), w.device, tuple(w.shape), w._version)
-        if self._wq is None or self._wq_key != key:
-            with torch.no_grad():
-                self._wq = _quantize_both(w.detach().contiguous())
-            self._wq_key = key
+        if not self._keeps_copies():
+            return self._quantize_weight()
+        stream = torch.cuda.current_stream(w.device) if w.is_cuda else None
+        if not self._is_current(w):
+            self._wq = self._quantize_weight()
+            self._wq_key = (w, w.detach(), w._version)
+            self._wq_stream = stream
+            self._wq_ready = stream.record_event() if stream is not None else None
+        elif stream != self._wq_stream:
+            stream.wait_event(self._wq_ready)
+            for t in self._wq:
+                t.record_stream(stream)
         return self._wq
 
     def forward(self, x):
         params = [self.weight] + ([self.bias] if self.bias is not None else [])
         if not (torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in params))):
-            return mxfp8_linear_inference(x, self.weight, self.quantized_weight(), self.bias)
+            return mxfp8_linear_inference(x, self.weight, self.quantized_weight() if self._keeps_copies() else None,
+                                          self.bias)
         return MXFP8LinearFunction.apply(x, self.weight, self.fuse_wgrad_accumulation, self.quantized_weight(),
                                          self.bias)
