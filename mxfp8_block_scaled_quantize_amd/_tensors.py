@@ -6,6 +6,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd import forward_ad
 
 from . import MXFP8Error, lib
 
@@ -43,3 +44,13 @@ def on_stream(stream, tensors, call):
         if t is not None:
             t.record_stream(stream)
     return result
+
+
+def no_tangent(where, *tensors):
+    """Refuse dual tensors: the layers have no forward-mode derivative, and a
+    tangent must not get lost on a path without autograd."""
+    if forward_ad._current_level < 0:
+        return
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            raise NotImplementedError("%s does not propagate forward-mode tangents" % where)

@@ -12,6 +12,7 @@
 #include <array>
 
 #include <ATen/hip/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -124,6 +125,14 @@ void need(const Tensor& t, const char* name, at::ScalarType type, at::IntArrayRe
   if (t.sizes() != shape) refuse(std::string(name) + " must have shape " + shape_text(shape) + ", got " + shape_text(t.sizes()));
   if (t.device() != device) refuse(std::string(name) + " is on " + t.device().str() + ", expected " + device.str());
   if (!t.is_contiguous()) refuse(std::string(name) + " must be contiguous");
+}
+
+// The operators have no forward-mode derivative: a dual tensor's tangent must not
+// get lost (inside a custom function's forward it is the function's affair).
+void no_tangent(const Tensor* t, const char* name) {
+  if (t && c10::AutogradState::get_tls_state().get_fw_grad_mode() && t->_fw_grad(0).defined())
+    refuse(std::string(name) + " carries a forward-mode tangent, which this operator does not propagate",
+           PyExc_NotImplementedError);
 }
 
 // ------------------------------------------------------------------- the call
@@ -246,6 +255,7 @@ Tensor output(const Tensor* out, int64_t rows, int64_t cols, c10::Device dev, co
     refuse(text);
   if (out->requires_grad() && at::GradMode::is_enabled())
     refuse("out requires a gradient, which this operator does not have: pass it with gradients disabled");
+  no_tangent(out, "out");
   return *out;
 }
 // The kernel has written a caller's tensor behind autograd's back: what was saved
@@ -416,6 +426,8 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (p.top_k < 1) refuse("top_k must be at least 1");
     const Tensor* bias = tensor_or_none(a[3], "bias");
     if (bias) need(*bias, "bias", at::kFloat, {logits.size(1)}, logits.device());
+    no_tangent(&logits, "logits");
+    no_tangent(bias, "bias");
     if (logits.requires_grad() && at::GradMode::is_enabled()) {
       auto r = Route::apply(logits, bias ? std::optional<Tensor>(*bias) : std::nullopt, p.top_k, p.groups, p.top_groups,
                             p.group_top, (int64_t)p.flags);
@@ -519,6 +531,8 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor &position = THPVariable_Unpack(a[1]), &w = tensor(a[2], "weights");
     need(position, "position", at::kInt, position.sizes(), y.device());
     need(w, "weights", at::kFloat, position.sizes(), y.device());
+    no_tangent(&y, "y");
+    no_tangent(&w, "weights");
     if (at::GradMode::is_enabled() && (y.requires_grad() || w.requires_grad())) return wrap(Combine::apply(y, position, w));
     return wrap(combine_forward(y, position, w));
   });

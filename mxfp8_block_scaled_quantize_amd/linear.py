@@ -36,6 +36,7 @@ copy only for wgrad.
 import torch
 
 from . import gemm, quantize
+from ._tensors import no_tangent
 
 
 def _quantize_both(t, dbias=False):
@@ -207,6 +208,7 @@ class MXFP8Linear(torch.nn.Module):
 
     def forward(self, x):
         params = [self.weight] + ([self.bias] if self.bias is not None else [])
+        no_tangent("MXFP8Linear", x, *params)
         if not (torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in params))):
             return mxfp8_linear_inference(x, self.weight, self.quantized_weight() if self._keeps_copies() else None,
                                           self.bias)

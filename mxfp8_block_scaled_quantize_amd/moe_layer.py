@@ -14,6 +14,7 @@ can be captured in a graph.
 import torch
 
 from . import moe, mxfp4
+from ._tensors import no_tangent
 
 
 class MXFP4MoE(torch.nn.Module):
@@ -55,6 +56,7 @@ class MXFP4MoE(torch.nn.Module):
         """x BF16 [.., hidden] -> BF16 of the same shape."""
         if x.dtype != torch.bfloat16 or x.shape[-1] != self.hidden:
             raise ValueError("input must be BF16 with %d features" % self.hidden)
+        no_tangent("MXFP4MoE", x)
         t = x.reshape(-1, self.hidden).contiguous()
         weights, ids = moe.route(t @ self.router.t(), self.top_k, bias=self.bias, **self.plan)
         plan = moe.dispatch(ids, self.experts)

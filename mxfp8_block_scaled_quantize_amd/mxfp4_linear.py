@@ -17,6 +17,7 @@ whose weight stays says so with ``freeze_weight``.
 
 import torch
 
+from ._tensors import no_tangent
 from .mxfp4 import gemm, quantize
 
 
@@ -144,6 +145,7 @@ class MXFP4Linear(torch.nn.Module):
             return _copies(self.weight.detach().contiguous(), True, colwise)
 
     def forward(self, x):
+        no_tangent("MXFP4Linear", x, self.weight)
         if torch.is_grad_enabled() and (x.requires_grad or self.weight.requires_grad):
             # a weight in training is quantized there, a frozen one may be kept
             frozen = self.quantized_weight(x.requires_grad) if not self.weight.requires_grad else None
