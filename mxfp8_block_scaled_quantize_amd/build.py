@@ -31,19 +31,50 @@ DEVICE_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
                 "-Wall", "-Wno-unused-function", "-Wno-unknown-warning-option"]
 
 
-def _torch_dir() -> str:
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+def _torch_dir():
+    spec = importlib.util.find_spec("torch")
+    return None if spec is None else os.path.dirname(spec.origin)
 
 
-def _host_compile(obj: str) -> list:
+def _host_compile(obj: str, torch_dir: str) -> list:
     """Compile command of the extension module (HIP's headers want the platform named)."""
-    inc = os.path.join(_torch_dir(), "include")
+    inc = os.path.join(torch_dir, "include")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-isystem", inc,
             "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/opt/rocm/include",
             "-I" + sysconfig.get_path("include"), "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
 
 
+def _start(cmd):
+    """A running compiler, or why there is none."""
+    try:
+        return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        return e
+
+
+def _succeeded(cmd, p, verbose) -> bool:
+    if isinstance(p, OSError):
+        sys.stderr.write("FAILED: %s\n%s\n" % (" ".join(cmd), p))
+        return False
+    out, _ = p.communicate()
+    text = "\n".join(line for line in out.decode(errors="replace").splitlines()
+                     if "packed-fp32-ops" not in line)
+    if p.returncode != 0:
+        sys.stderr.write("FAILED: %s\n%s\n" % (" ".join(cmd), text))
+    elif verbose and text.strip():
+        sys.stderr.write(text + "\n")
+    return p.returncode == 0
+
+
+def _link(cmd, path) -> None:
+    tmp = path + ".tmp%d" % os.getpid()
+    subprocess.check_call([*cmd, "-o", tmp])
+    os.replace(tmp, path)
+
+
 def build(verbose: bool = False) -> str:
+    """Compile and link everything; raises if any part fails.  libmxfp8.so needs
+    neither g++ nor PyTorch's headers and is linked without them too."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     procs = []
     objs = []
@@ -51,32 +82,25 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
         objs.append(obj)
         cmd = [HIPCC, *DEVICE_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
-        procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+        procs.append((cmd, _start(cmd)))
     binding = os.path.join(BUILD_DIR, TORCH_SOURCE.replace(".cpp", ".o"))
-    cmd = _host_compile(binding)
-    procs.append((cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    failed = False
-    for cmd, p in procs:
-        out, _ = p.communicate()
-        text = "\n".join(line for line in out.decode(errors="replace").splitlines()
-                         if "packed-fp32-ops" not in line)
-        if p.returncode != 0:
-            failed = True
-            sys.stderr.write("FAILED: %s\n%s\n" % (" ".join(cmd), text))
-        elif verbose and text.strip():
-            sys.stderr.write(text + "\n")
-    if failed:
+    torch_dir = _torch_dir()
+    host = None
+    if torch_dir is not None:
+        cmd = _host_compile(binding, torch_dir)
+        host = (cmd, _start(cmd))
+    done = [_succeeded(cmd, p, verbose) for cmd, p in procs]
+    host_done = host is not None and _succeeded(*host, verbose)
+    if not all(done):
         raise RuntimeError("hipcc compilation failed")
     n = len(SOURCES)
     for path, parts in ((LIB_PATH, objs[:n]), (CALIB_PATH, objs[n:])):
-        tmp = path + ".tmp%d" % os.getpid()
-        subprocess.check_call([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *parts, "-o", tmp])
-        os.replace(tmp, path)
-    tmp = TORCH_PATH + ".tmp%d" % os.getpid()
-    subprocess.check_call(["g++", "-shared", binding, "-o", tmp, "-L" + HERE, "-lmxfp8", "-L" + os.path.join(_torch_dir(), "lib"),
-                           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip",
-                           "-ltorch_hip", "-Wl,-rpath,$ORIGIN"])
-    os.replace(tmp, TORCH_PATH)
+        _link([HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *parts], path)
+    if not host_done:
+        raise RuntimeError("libmxfp8.so is built, _mx_torch.so is not: " +
+                           ("PyTorch was not found" if host is None else "its compilation failed"))
+    _link(["g++", "-shared", binding, "-L" + HERE, "-lmxfp8", "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python",
+           "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_hip", "-ltorch_hip", "-Wl,-rpath,$ORIGIN"], TORCH_PATH)
     return LIB_PATH
 
 
