@@ -8,7 +8,7 @@ import ctypes
 import torch
 from torch.autograd import forward_ad
 
-from . import MXFP8Error, lib
+from . import lib
 
 
 def declare(name, argtypes, restype=ctypes.c_int):
@@ -17,11 +17,6 @@ def declare(name, argtypes, restype=ctypes.c_int):
     f.restype = restype
     f.argtypes = argtypes
     return f
-
-
-def check(status, where):
-    if status != 0:
-        raise MXFP8Error(status, where)
 
 
 def extension():

@@ -16,7 +16,8 @@ from typing import NamedTuple
 
 import torch
 
-from ._tensors import check, declare, extension, on_stream
+from . import _check, _p, _s
+from ._tensors import declare, extension, on_stream
 
 MOE_FP32, MOE_BF16, MOE_FP16 = 0, 1, 2
 MOE_ROUTE_SIGMOID = 1
@@ -44,29 +45,17 @@ def _functions():
     return _fn
 
 
-def _address(t):
-    return None if t is None else t if isinstance(t, int) else t.data_ptr()
-
-
-def _stream(stream):
-    if isinstance(stream, int):
-        return stream
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-
 # ------------------------------------------------------------ C ABI mirror
 
 def moe_route(logits, dtype, tokens, experts, ld, bias, top_k, groups, top_groups, group_top, flags, weights, ids,
               stream=None):
-    p = _address
-    check(_functions()["moe_route"](p(logits), dtype, tokens, experts, ld, p(bias), top_k, groups, top_groups, group_top,
-                                    flags, p(weights), p(ids), _stream(stream)), "moe_route")
+    _check(_functions()["moe_route"](_p(logits), dtype, tokens, experts, ld, _p(bias), top_k, groups, top_groups, group_top,
+                                     flags, _p(weights), _p(ids), _s(stream)), "moe_route")
 
 
 def moe_route_backward(logits, dtype, tokens, experts, ld, ids, dweights, top_k, flags, dlogits, stream=None):
-    p = _address
-    check(_functions()["moe_route_backward"](p(logits), dtype, tokens, experts, ld, p(ids), p(dweights), top_k, flags,
-                                             p(dlogits), _stream(stream)), "moe_route_backward")
+    _check(_functions()["moe_route_backward"](_p(logits), dtype, tokens, experts, ld, _p(ids), _p(dweights), top_k, flags,
+                                              _p(dlogits), _s(stream)), "moe_route_backward")
 
 
 def moe_dispatch_workspace_bytes(tokens, experts, top_k):
@@ -74,23 +63,20 @@ def moe_dispatch_workspace_bytes(tokens, experts, top_k):
 
 
 def moe_dispatch(ids, tokens, experts, top_k, offsets, token, position, workspace=None, workspace_bytes=0, stream=None):
-    p = _address
-    check(_functions()["moe_dispatch"](p(ids), tokens, experts, top_k, p(offsets), p(token), p(position), p(workspace),
-                                       workspace_bytes, _stream(stream)), "moe_dispatch")
+    _check(_functions()["moe_dispatch"](_p(ids), tokens, experts, top_k, _p(offsets), _p(token), _p(position), _p(workspace),
+                                        workspace_bytes, _s(stream)), "moe_dispatch")
 
 
 def moe_combine(y, dtype, rows, ld_y, position, weights, tokens, top_k, hidden, out, stream=None):
-    p = _address
-    check(_functions()["moe_combine"](p(y), dtype, rows, ld_y, p(position), p(weights), tokens, top_k, hidden, p(out),
-                                      _stream(stream)), "moe_combine")
+    _check(_functions()["moe_combine"](_p(y), dtype, rows, ld_y, _p(position), _p(weights), tokens, top_k, hidden, _p(out),
+                                       _s(stream)), "moe_combine")
 
 
 def moe_combine_backward(y, dtype, rows, ld_y, position, weights, tokens, top_k, hidden, dout, ld_dout, dy, dweights,
                          workspace=None, workspace_bytes=0, stream=None):
-    p = _address
-    check(_functions()["moe_combine_backward"](p(y), dtype, rows, ld_y, p(position), p(weights), tokens, top_k, hidden,
-                                               p(dout), ld_dout, p(dy), p(dweights), p(workspace), workspace_bytes,
-                                               _stream(stream)), "moe_combine_backward")
+    _check(_functions()["moe_combine_backward"](_p(y), dtype, rows, ld_y, _p(position), _p(weights), tokens, top_k, hidden,
+                                                _p(dout), ld_dout, _p(dy), _p(dweights), _p(workspace), workspace_bytes,
+                                                _s(stream)), "moe_combine_backward")
 
 
 # ------------------------------------------------------------------ operators

@@ -14,9 +14,8 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
-from ._tensors import check, declare, extension, on_stream
+from . import _check, _p, _s
+from ._tensors import declare, extension, on_stream
 
 MXFP4_ROWWISE = 1
 MXFP4_COLWISE = 2
@@ -41,41 +40,27 @@ def _functions():
     return _fn
 
 
-def _address(t):
-    return None if t is None else t if isinstance(t, int) else t.data_ptr()
-
-
-def _stream(stream):
-    if isinstance(stream, int):
-        return stream
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
-
-
 # ------------------------------------------------------------ C ABI mirror
 
 def mxfp4_quantize(x, x_rows, rows, cols, ld_x, index, flags, q_row=None, s_row=None, q_colT=None, s_colT=None,
                    stream=None):
-    p = _address
-    check(_functions()["mxfp4_quantize"](p(x), x_rows, rows, cols, ld_x, p(index), flags, p(q_row), p(s_row), p(q_colT),
-                                         p(s_colT), _stream(stream)), "mxfp4_quantize")
+    _check(_functions()["mxfp4_quantize"](_p(x), x_rows, rows, cols, ld_x, _p(index), flags, _p(q_row), _p(s_row), _p(q_colT),
+                                          _p(s_colT), _s(stream)), "mxfp4_quantize")
 
 
 def mxfp4_dequantize(q, s, rows, cols, out, ld_out, flags, stream=None):
-    p = _address
-    check(_functions()["mxfp4_dequantize"](p(q), p(s), rows, cols, p(out), ld_out, flags, _stream(stream)),
-          "mxfp4_dequantize")
+    _check(_functions()["mxfp4_dequantize"](_p(q), _p(s), rows, cols, _p(out), ld_out, flags, _s(stream)),
+           "mxfp4_dequantize")
 
 
 def mxfp4_gemm(a, a_packed, b, b_packed, c, ldc, M, N, K, flags, stream=None):
-    p = _address
-    check(_functions()["mxfp4_gemm"](p(a), p(a_packed), p(b), p(b_packed), p(c), ldc, M, N, K, flags, _stream(stream)),
-          "mxfp4_gemm")
+    _check(_functions()["mxfp4_gemm"](_p(a), _p(a_packed), _p(b), _p(b_packed), _p(c), ldc, M, N, K, flags, _s(stream)),
+           "mxfp4_gemm")
 
 
 def mxfp4_grouped_gemm(a, a_packed, b, b_packed, offsets, G, c, ldc, M_total, N, K, flags, stream=None):
-    p = _address
-    check(_functions()["mxfp4_grouped_gemm"](p(a), p(a_packed), p(b), p(b_packed), p(offsets), G, p(c), ldc, M_total, N,
-                                             K, flags, _stream(stream)), "mxfp4_grouped_gemm")
+    _check(_functions()["mxfp4_grouped_gemm"](_p(a), _p(a_packed), _p(b), _p(b_packed), _p(offsets), G, _p(c), ldc, M_total, N,
+                                              K, flags, _s(stream)), "mxfp4_grouped_gemm")
 
 
 # ------------------------------------------------------ allocating helpers
