@@ -29,10 +29,14 @@ def extension():
 
 
 def on_stream(stream, tensors, call):
-    """Run `call` with `stream` current: its outputs belong to that stream, and
-    its inputs' memory is not handed out again before the stream is done."""
+    """Run `call` with `stream` (a torch stream or a raw handle, of the tensors'
+    device) current: its outputs belong to that stream, and its inputs' memory is
+    not handed out again before the stream is done."""
+    device = next((t.device for t in tensors if getattr(t, "is_cuda", False)), None)
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    elif device is not None and stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
     with torch.cuda.stream(stream):
         result = call()
     for t in tensors:
