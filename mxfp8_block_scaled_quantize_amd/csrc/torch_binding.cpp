@@ -108,7 +108,11 @@ int32_t small_integer(PyObject* o, const char* name) {
   if (v < INT32_MIN || v > INT32_MAX) refuse(std::string(name) + " is out of range");
   return (int32_t)v;
 }
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();   // the object's own error is set
+  return v == 1;
+}
 
 std::string shape_text(at::IntArrayRef s) {
   std::string t = "(";
