@@ -19,19 +19,28 @@ from ._tensors import no_tangent
 
 class MXFP4MoE(torch.nn.Module):
     """experts of [gate_up: 2 * ffn x hidden, down: hidden x ffn] in MXFP4 (one
-    buffer each, quantized by ``load``), a router in BF16.  hidden and ffn are
-    multiples of 128.  scores, groups, top_groups, group_top and renormalize as
-    for ``moe.route``; balance=True adds a per-expert choice bias (a buffer)."""
+    buffer each, quantized by ``load``).  hidden and ffn are multiples of 128.
+    scores, groups, top_groups, group_top and renormalize as for ``moe.route``;
+    balance=True adds a per-expert choice bias (a buffer).
+
+    router_dtype is the type of the router's weights and of its logits.  BF16, the
+    default, rounds a logit by up to 2^-8 of its value, as models trained with a
+    BF16 router expect, and experts that lie closer than that may change places.
+    torch.float32 multiplies in 32 bits, and ``moe.route`` then orders by the
+    logits as they come.  The product is PyTorch's (this library has products of
+    block-scaled operands alone), experts / (3 top_k ffn) of the experts' work."""
 
     def __init__(self, hidden, ffn, experts, top_k, scores="softmax", groups=1, top_groups=1, group_top=2, renormalize=True,
-                 balance=False, device=None):
+                 balance=False, device=None, router_dtype=torch.bfloat16):
         super().__init__()
         if hidden % 128 or ffn % 128:
             raise ValueError("hidden and ffn must be multiples of 128")
+        if router_dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("router_dtype must be torch.bfloat16 or torch.float32")
         self.hidden, self.ffn, self.experts, self.top_k = hidden, ffn, experts, top_k
         self.plan = dict(scores=scores, groups=groups, top_groups=top_groups, group_top=group_top, renormalize=renormalize)
         u8, i32 = torch.uint8, torch.int32
-        self.register_buffer("router", torch.zeros((experts, hidden), dtype=torch.bfloat16, device=device))
+        self.register_buffer("router", torch.zeros((experts, hidden), dtype=router_dtype, device=device))
         self.register_buffer("bias", torch.zeros(experts, dtype=torch.float32, device=device) if balance else None)
         self.register_buffer("gate_up", torch.zeros((experts, 2 * ffn, hidden // 2), dtype=u8, device=device))
         self.register_buffer("gate_up_scales", torch.zeros((hidden // 128, experts * 2 * ffn), dtype=i32, device=device))
@@ -40,8 +49,8 @@ class MXFP4MoE(torch.nn.Module):
 
     @torch.no_grad()
     def load(self, router, gate_up, down, bias=None):
-        """Take BF16 weights: router [experts, hidden], gate_up [experts, 2 * ffn,
-        hidden] (gate rows, then up rows), down [experts, hidden, ffn]."""
+        """Take a router [experts, hidden] and BF16 weights: gate_up [experts,
+        2 * ffn, hidden] (gate rows, then up rows), down [experts, hidden, ffn]."""
         self.router.copy_(router)
         if bias is not None:
             self.bias.copy_(bias)
@@ -58,7 +67,7 @@ class MXFP4MoE(torch.nn.Module):
             raise ValueError("input must be BF16 with %d features" % self.hidden)
         no_tangent("MXFP4MoE", x)
         t = x.reshape(-1, self.hidden).contiguous()
-        weights, ids = moe.route(t @ self.router.t(), self.top_k, bias=self.bias, **self.plan)
+        weights, ids = moe.route(t.to(self.router.dtype) @ self.router.t(), self.top_k, bias=self.bias, **self.plan)
         plan = moe.dispatch(ids, self.experts)
         a = mxfp4.quantize(t, packed=True, index=plan.token)
         h = mxfp4.grouped_gemm(a["q_row"], a["p_row"], self.gate_up, self.gate_up_scales, plan.offsets, swiglu=True)
