@@ -171,46 +171,45 @@ class MXFP8Linear(torch.nn.Module):
     def __getstate__(self):   # events belong to this process
         return {**self.__dict__, "_wq": None, "_wq_key": None, "_wq_stream": None, "_wq_ready": None}
 
-    def _is_current(self, w):
-        if self._wq is None:
-            return False
-        parameter, alias, version = self._wq_key
-        return (parameter is w and alias.data_ptr() == w.data_ptr() and alias.device == w.device
-                and alias.shape == w.shape and version == w._version)
-
-    def _keeps_copies(self):
-        # the copies of a capture hold nothing until its replay; inference tensors have no version
-        w = self.weight
-        return not (w.is_inference() or (w.is_cuda and torch.cuda.is_current_stream_capturing()))
-
     def _quantize_weight(self):
         # not inference tensors, which no later backward pass could use
         with torch.inference_mode(False), torch.no_grad():
             return _quantize_both(self.weight.detach().contiguous())
 
+    def _kept_copies(self):
+        """The kept copies, made anew where the weight has changed, ready for the
+        current stream; None where none may be kept: those of a capture hold
+        nothing until its replay, and inference tensors have no version."""
+        w = self.weight
+        cuda = w.is_cuda
+        if w.is_inference() or (cuda and torch.cuda.is_current_stream_capturing()):
+            return None
+        # the raw handle costs 0.1 us, torch.cuda.current_stream 2
+        stream = torch._C._cuda_getCurrentRawStream(w.get_device()) if cuda else None
+        if self._wq is not None:
+            parameter, alias, version = self._wq_key
+            if (parameter is w and version == w._version and alias.data_ptr() == w.data_ptr() and alias.shape == w.shape):
+                if stream != self._wq_stream:
+                    here = torch.cuda.current_stream(w.device)
+                    here.wait_event(self._wq_ready)
+                    for t in self._wq:
+                        t.record_stream(here)
+                return self._wq
+        self._wq = self._quantize_weight()
+        self._wq_key = (w, w.detach(), w._version)
+        self._wq_stream = stream
+        self._wq_ready = torch.cuda.current_stream(w.device).record_event() if cuda else None
+        return self._wq
+
     def quantized_weight(self):
         """Both MXFP8 copies of the weight, quantized again only when the
         parameter, its storage, shape or version counter has changed."""
-        w = self.weight
-        if not self._keeps_copies():
-            return self._quantize_weight()
-        stream = torch.cuda.current_stream(w.device) if w.is_cuda else None
-        if not self._is_current(w):
-            self._wq = self._quantize_weight()
-            self._wq_key = (w, w.detach(), w._version)
-            self._wq_stream = stream
-            self._wq_ready = stream.record_event() if stream is not None else None
-        elif stream != self._wq_stream:
-            stream.wait_event(self._wq_ready)
-            for t in self._wq:
-                t.record_stream(stream)
-        return self._wq
+        return self._kept_copies() or self._quantize_weight()
 
     def forward(self, x):
         params = [self.weight] + ([self.bias] if self.bias is not None else [])
         no_tangent("MXFP8Linear", x, *params)
         if not (torch.is_grad_enabled() and (x.requires_grad or any(p.requires_grad for p in params))):
-            return mxfp8_linear_inference(x, self.weight, self.quantized_weight() if self._keeps_copies() else None,
-                                          self.bias)
+            return mxfp8_linear_inference(x, self.weight, self._kept_copies(), self.bias)
         return MXFP8LinearFunction.apply(x, self.weight, self.fuse_wgrad_accumulation, self.quantized_weight(),
                                          self.bias)

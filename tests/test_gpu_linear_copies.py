@@ -46,7 +46,7 @@ def test_streams():
             for s in sides:              # the first one quantizes, the others wait for its copies
                 with torch.cuda.stream(s):
                     got.append(layer(x))
-            assert layer._wq_stream == sides[0]
+            assert layer._wq_stream == sides[0].cuda_stream
             for s in sides:
                 torch.cuda.current_stream().wait_stream(s)
             want = _want(torch, layer, x)
