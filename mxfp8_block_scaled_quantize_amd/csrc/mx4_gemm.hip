@@ -232,9 +232,14 @@ static Choice choose(const Mx4Gemm& g) {
   return best;
 }
 
+// Whether the chosen kernel's grid can be launched (where no variant's can, the
+// choice is the largest tile).
 bool mx4_gemm_grid_fits(const Mx4Gemm& g) {
+  const Choice c = choose(g);
+  if (c.tile == Mx4Tile::k256x256) return mx4_gemm_tile_fits(g);
+  if (c.tile != Mx4Tile::kRows) return true;   // offered where it fits
   // a grid's dimensions are limited one by one: 2^32 - 1 work-items, 65535 workgroups of the second
-  return choose(g).tile != Mx4Tile::kRows || (grid_fits(g.N / 16, 1, 512) && row_blocks(g, 16) <= 65535);
+  return grid_fits(g.N / 16, 1, 512) && row_blocks(g, 16 * c.mb) <= 65535;
 }
 
 template <int MB, int W, bool GROUPED>
