@@ -173,6 +173,9 @@ void* stream_of(c10::Device d) { return c10::hip::getCurrentHIPStream(d.index())
 // Stride between the rows of a matrix with unit column stride; of one row it
 // says nothing.  Rows that overlap (expanded ones) are refused by the C ABI.
 int64_t ld(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+// Whether the columns of a matrix follow each other (of one column the stride
+// says nothing).
+bool unit_columns(const Tensor& t) { return t.size(1) <= 1 || t.stride(1) == 1; }
 PyObject* wrap(Tensor t) { return THPVariable_Wrap(std::move(t)); }
 PyObject* pair(Tensor a, Tensor b) {
   PyObject* r = PyTuple_New(2);
@@ -424,7 +427,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n) {
       refuse("logits must be a [tokens, experts] tensor of float32, bfloat16 or float16");
     const Tensor& logits = THPVariable_Unpack(a[0]);
     on_gpu(logits, "logits");
-    if (logits.stride(1) != 1) refuse("logits must have unit stride along the experts");
+    if (!unit_columns(logits)) refuse("logits must have unit stride along the experts");
     const RoutePlan p{small_integer(a[1], "top_k"), small_integer(a[4], "groups"), small_integer(a[5], "top_groups"),
                       small_integer(a[6], "group_top"), (uint32_t)integer(a[2], "flags")};
     if (p.top_k < 1) refuse("top_k must be at least 1");
@@ -528,7 +531,7 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const char* text = "y must be a [rows, hidden] tensor of float32, bfloat16 or float16 with unit column stride";
     if (!THPVariable_Check(a[0])) refuse(text);
     const Tensor& y = THPVariable_Unpack(a[0]);
-    if (moe_dtype(y) < 0 || y.dim() != 2 || y.stride(1) != 1) refuse(text);
+    if (moe_dtype(y) < 0 || y.dim() != 2 || !unit_columns(y)) refuse(text);
     on_gpu(y, "y");
     if (!THPVariable_Check(a[1]) || THPVariable_Unpack(a[1]).dim() != 2)
       refuse("position must be an int32 [tokens, top_k] tensor");
