@@ -43,7 +43,8 @@ extern "C" {
  *   weights[t] = their scores, renormalized if asked for.
  * Ties go to the lowest index (of group or expert).  The order is that of the
  * scores in 64 bits, not of their 32-bit roundings; without a bias it is the
- * logits' own.  The sums, weights and gradients are 32-bit.
+ * logits' own.  The sums, weights and gradients are 32-bit; a weight is
+ * within 16 ulp (2e-6) of its exact value, 7e-8 of it on average.
  * A logit of -inf has score 0 (a row of nothing else has scores and weights
  * of 0), and a score below fp32's normal range (2^-126) may be given as 0.  NaN or +inf under softmax make the row's weights NaN, under sigmoid a
  * NaN has a NaN score.  A choice of NaN is ordered below every other one, so

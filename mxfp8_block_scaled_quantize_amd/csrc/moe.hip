@@ -578,9 +578,10 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, const typename D
 // A wave holds 64 / LPR rows.  The choice is made in 32 bits; a row in which
 // the order of two values is within the rounding (one in a few thousand with a
 // bias) is chosen again in 64, which the kernel then waits 2.5 us for.  Bound by
-// the rounds' latency for few rows (16 tokens, 256 experts, top 8: 3.1 us, 4.5
+// the rounds' latency for few rows (16 tokens, 256 experts, top 8: 3.1 us, 4.6
 // with a bias and 8 groups) and by their instructions for many (16384 tokens, 128
-// experts, top 8: 6.0 us for 5 MB, 8.1 with a bias; 0.35 a round).
+// experts, top 8: softmax 6.1 us for 5 MB, 9.1 with a bias, sigmoid 5.8 and 7.1;
+// 0.35 a round).
 template <typename D, int LPR, int VPL, bool SURE>
 __global__ __launch_bounds__(256) void moe_route_kernel(const typename D::T* __restrict__ logits, int64_t T, int64_t ld,
                                                         RouteArgs a, float* __restrict__ weights,
@@ -1101,7 +1102,8 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const typename D::T* _
 // How often a row of y is named.  Up to kOneCount slots a workgroup counts the
 // rows of its range in LDS and goes through all positions for that (a few
 // hundred KB of L2 reads): one launch, and no atomics on memory.  65528 slots and
-// rows: 6.7 us, with a clear and a launch of atomics 9.6; 262144: 22.9 and 16.0.
+// rows: 6.7 us (between the launches of a graph; 8.1 by itself), with a clear and a
+// launch of atomics 9.6; 262144: 22.9 and 16.0.
 // Up to kNoCount slots nothing is counted ahead: the gradients' waves look through
 // the positions themselves (256 x 4 x 1024, all gradients: 4.8 us, with a launch of
 // counts 6.7; 1024 x 4: 12.7 and 8.5) and the host has a launch less.
@@ -1147,8 +1149,8 @@ __global__ __launch_bounds__(256) void moe_named_kernel(const int32_t* __restric
 // w * dout; one that several name is summed by the lowest of its slots (which
 // finds the others by going through the positions: right, and slow, for what
 // no dispatch produces).  The workgroups behind the tokens' own zero the rows
-// that nobody names.  8191 tokens x 8 x 4096: 219 us for 1.14 GB, 5.2 TB/s, and
-// 6.7 us to count who names whom; 8071 x 2 x 304: 7 us (18 with each slot's
+// that nobody names.  8191 tokens x 8 x 4096: 217 us for 1.14 GB, 5.3 TB/s, and
+// 8 us to count who names whom; 8071 x 2 x 304: 7 us (18 with each slot's
 // position, weight and count read by itself).
 template <typename D, bool VEC, int TPT>
 __global__ __launch_bounds__(256) void moe_combine_backward_kernel(

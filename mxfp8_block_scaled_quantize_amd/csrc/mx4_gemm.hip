@@ -19,9 +19,10 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // of B (SwiGLU: 16 gate rows and their 16 up rows) and 16 MB rows of A of one
 // group, each wave a part of K.  Both operands go from global memory straight
 // to registers in the matrix instructions' layout (16 rows x 64 bytes a load),
-// several K slices in flight; the waves' sums meet in LDS.  One row x 14336 columns, K = 4096: 7.4 us
-// for 31 MB, of which 2 are the launch; 148 rows of 32 experts through 2048 x 4096
-// weights (SwiGLU): 22.8 us for the 142 MB of all experts, 6.2 TB/s.
+// several K slices in flight; the waves' sums meet in LDS.  One row x 14336 columns, K = 4096: 7.3 us
+// for 31 MB, of which 2 are the launch; 148 rows of 32 experts, 27 with rows, through
+// 2048 x 4096 weights (SwiGLU): 23.4 us for the 130 MB that the counters see, 5.5 TB/s
+// (row sums of 4 GB read 6.4).
 enum { EPI_NONE = 0, EPI_ACC = 1, EPI_SWIGLU = 2 };
 
 template <int MB, int NB, int W, bool GROUPED, int EPI>

@@ -6,7 +6,7 @@
 // 2 x 2 waves of (BM / 2) x (BN / 2), and a ring of NS slots, unrolled so that
 // every slot is a constant.  A step waits for its own slot's loads, reads all its
 // fragments, asks for the step NS - 1 further on and multiplies.  Few tiles: the
-// time is the steps' own latency (barrier, LDS reads, MFMA chain: 0.27 us a step
+// time is the steps' own latency (barrier, LDS reads, MFMA chain: 0.24 us a step
 // of 64 x 64), and two workgroups of a compute unit fill each other's gaps.
 // K = 4096: 512 x 4096 10.0 us with 64 x 64, 1024 x 4096 15.3 with 128 x 128.
 // Measured and not kept: deeper rings (64 x 64 with six slots 8.6 us where three

@@ -1,5 +1,6 @@
 // The MXFP4 GEMM's 256 x 256 tile, for products with enough tiles to fill the
-// chip: bound by the matrix cores.
+// chip: bound by the matrix cores' rate at the clock that the chip's power leaves
+// them, and by each tile's start and output.
 //
 // Operand layout of V_MFMA_SCALE_F32_32X32X64_F8F6F4 with E2M1 on both sides:
 // lane l holds row l % 32, K = 32 (l / 32) + [0, 32) in its 16 bytes, i.e. one
@@ -24,12 +25,15 @@
 // Rows past the end of an operand read as zero (buffer range check), results
 // past the end are not stored.
 //
-// 8192 x 14336 x 4096 takes 231 us, 4.2 PFLOP/s; MFMAs on operands that never
+// 8192 x 14336 x 4096 takes 229 us, 4.2 PFLOP/s; MFMAs on operands that never
 // leave the registers reach 5.8 PFLOP/s on this grid (166 us), and codes that
-// toggle more bits slow both down (uniformly random ones: 256 us), so it is the
-// chip's power that bounds it.  K = 16384: 4.9 PFLOP/s; a tile's start and output
-// cost about 6 us, a step 1.6 us under full load and 1.1 on an otherwise idle
-// chip.  Measured and not kept: a workgroup that stays and loads the next tile's
+// toggle more bits slow both down (uniformly random ones: 256 us).  A tile's start
+// and output cost about 6 us in which nothing is multiplied (40 of the 229: seven
+// rounds of tiles), a step 1.6 us under full load and 1.1 on an otherwise idle
+// chip.  Counters on this grid, matrix cores busy and clock: K = 1024 25 % of the
+// cycles at 2.25 GHz, K = 4096 49 % at 1.85; 8192 x 8192 x 16384 64 % at 1.63 (4.6
+// PFLOP/s under the profiler, 4.9 without): the busier they are, the lower the
+// clock.  Measured and not kept: a workgroup that stays and loads the next tile's
 // first steps during its last ones, its output through a staging area of its own
 // (254 us: more scalar registers than there are, and output rows in 128-byte
 // instead of 512-byte pieces); cached instead of non-temporal stores (247 us);
