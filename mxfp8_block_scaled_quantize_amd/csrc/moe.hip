@@ -5,6 +5,7 @@
 
 #include "mx_device.h"
 #include "launch.h"
+#include "wave_scan.h"
 
 namespace mx {
 

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "mx_device.h"
+#include "wave_scan.h"
 
 namespace mx {
 namespace mx4 {
