@@ -37,18 +37,21 @@ extern "C" {
  *   choice_e = score_e + bias[e] (bias NULL: score_e);
  *   groups > 1: the experts are `groups` runs of experts / groups; a run's
  *     value is the sum of its group_top largest choices (fewer where it has
- *     fewer experts; NaN counts as -inf), and only the experts of the
- *     top_groups runs of the largest values can be chosen;
+ *     fewer experts; a choice or a sum of NaN counts as -inf), and only the
+ *     experts of the top_groups runs of the largest values can be chosen;
  *   ids[t]     = the top_k experts of the largest choices, largest first;
  *   weights[t] = their scores, renormalized if asked for.
  * Ties go to the lowest index (of group or expert).  The order is that of the
  * scores in 64 bits, not of their 32-bit roundings; without a bias it is the
- * logits' own.  The sums, weights and gradients are 32-bit; a weight is
- * within 16 ulp (2e-6) of its exact value, 7e-8 of it on average.
+ * logits' own, that of the runs too where group_top is 1.  The sums, weights and
+ * gradients are 32-bit; a weight is within 16 ulp (2e-6) of its exact value (7e-8
+ * of it on average), and under softmax |logit - largest| 2^-23 of it more (the
+ * rounding of that difference).
  * A logit of -inf has score 0 (a row of nothing else has scores and weights
- * of 0), and a score below fp32's normal range (2^-126) may be given as 0.  NaN or +inf under softmax make the row's weights NaN, under sigmoid a
- * NaN has a NaN score.  A choice of NaN is ordered below every other one, so
- * ids are always top_k different experts.
+ * of 0), and a score below fp32's normal range (2^-126) may be given as 0.  NaN
+ * or +inf under softmax make the row's weights NaN, under sigmoid a NaN has a
+ * NaN score.  A choice of NaN is ordered below every other one, so ids are
+ * always top_k different experts.
  *
  * dtype      of the logits: MOE_FP32, MOE_BF16 or MOE_FP16 (aligned to it).
  * experts    1 .. MOE_MAX_EXPERTS; ld >= experts.

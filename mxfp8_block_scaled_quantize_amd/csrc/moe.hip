@@ -320,7 +320,10 @@ __device__ __forceinline__ bool route_row(const RouteArgs& a, const float* x, co
     // bias the largest logit says the same
     const bool two = a.group_top == 2 && a.per > 1;
     const float off = a.sigmoid ? 8 * U : (9 + VPL / 2) * U * fminf(1.0f, 4.0f * largest);   // of one group
-    auto value = [&](const Top2& t) { return two ? t.m1 + t.m2 : t.m1; };
+    auto value = [&](const Top2& t) {
+      const float v = two ? t.m1 + t.m2 : t.m1;
+      return v == v ? v : -INFINITY;   // inf - inf
+    };
     auto error = [&](const Top2& t) { return off + 2 * U * (fabsf(t.m1) + (two ? fabsf(t.m2) : 0.0f)); };
     // biases next to the type's largest or lowest value: a sum that 32 bits do
     // not hold says nothing about its place among the others of its kind
@@ -525,7 +528,10 @@ __device__ __forceinline__ void route_exact(const RouteArgs& a, const typename D
     if (lg > 2) add(dppx<double, 0x4E>(m1), dppx<double, 0x4E>(m2));
     if (lg > 4) add(dppx<double, 0x141>(m1), dppx<double, 0x141>(m2));
     if (lg > 8) add(dppx<double, 0x140>(m1), dppx<double, 0x140>(m2));
-    if (mine < a.groups && (lane & (lg - 1)) == 0) gval[mine] = a.group_top == 2 && a.per > 1 ? m1 + m2 : m1;
+    if (mine < a.groups && (lane & (lg - 1)) == 0) {
+      const double v = a.group_top == 2 && a.per > 1 ? m1 + m2 : m1;
+      gval[mine] = v == v ? v : -INFINITY;   // inf - inf
+    }
     wave_lds_fence();
     if (lane < a.groups) {
       const double v = gval[lane];
