@@ -1,0 +1,183 @@
+// Device code shared by the two attention kernels over the paged MXFP4 cache.
+//
+// Rows.  The queries of a sequence and the heads that share a key-value head are
+// rows of one product: row = query * group + head of the group.  A tile is some
+// rows of one sequence and key-value head; its keys are cut into parts, each for a
+// workgroup, whose sums meet in the workspace (`sums`) and are joined by
+// kv_join_kernel.
+//
+// Scores.  S^T = K Q^T on the scaled matrix instructions: the keys' codes go from
+// the cache into the FP4 operand as they are, 32 codes and a scale byte a lane.  The
+// other operand takes FP8, so a query is split: its row is divided by 2^(E - 7)
+// (E: the exponent of its largest value, which lands in [128, 256)), `hi` is the
+// E4M3 rounding (4 of the 8 significant bits) and `lo` that of 16 times the rest,
+// which has 4 bits too: together they are the query's bits down to half of E4M3's
+// smallest step of lo, 2^-14, i.e. 2^-21 of the row's largest value.  Two products
+// of half the cost of a BF16 one, and no conversion of the keys.
+//
+// Values.  O^T = V^T P^T on the BF16 matrix instructions, as a token's values have
+// scales of their own: codes and scale become BF16 (exactly).
+#pragma once
+
+#include "kv.h"
+#include "launch.h"
+#include "mx_device.h"
+#include "wave_scan.h"
+
+namespace mx {
+namespace kv {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// What the kernels take, of KvAttention.
+struct Args {
+  const uint16_t* __restrict__ q;
+  int64_t q_token, q_head;
+  const uint8_t* __restrict__ cache;
+  int64_t record;
+  const int32_t* __restrict__ table;
+  int64_t ld_table;
+  const int32_t* __restrict__ lengths;
+  const int32_t* __restrict__ offsets;
+  uint16_t* __restrict__ out;
+  float* __restrict__ lse;
+  float* __restrict__ sums;   // O [parts][rows][D], then (m, l) [parts][rows][2]; null: one part
+  int32_t tokens, heads, kv_heads, group, sequences, pages, page_shift, keys_most, window, parts;
+  float scale2;               // scale * log2(e)
+};
+
+struct Tile {
+  int sequence, first_token, row0, rows;   // rows: of the sequence behind row0
+  int queries, length;
+};
+
+// Tile `t` among the sequences' tiles of TM rows.  False: past the last one.
+template <int TM>
+__device__ __forceinline__ bool find_tile(const Args& a, int t, Tile* tile) {
+  if (!a.offsets) {
+    const int per = (a.group + TM - 1) / TM;
+    const int b = t / per;
+    if (b >= a.sequences) return false;
+    tile->sequence = b;
+    tile->first_token = b;
+    tile->row0 = (t - b * per) * TM;
+    tile->queries = 1;
+  } else {
+    const int lane = threadIdx.x & 63;
+    int carry = 0;
+    for (int g0 = 0;; g0 += 64) {
+      if (g0 >= a.sequences) return false;
+      const int g = g0 + lane;
+      int lo = 0, hi = 0;
+      if (g < a.sequences) {
+        const int l = a.offsets[g], h = a.offsets[g + 1];
+        lo = l < 0 ? 0 : (l > a.tokens ? a.tokens : l);
+        hi = h < 0 ? 0 : (h > a.tokens ? a.tokens : h);
+      }
+      lo = lo > carry ? lo : carry;
+      lo = scan64(lo, [](int x, int y) { return x > y ? x : y; });
+      hi = hi > lo ? hi : lo;
+      carry = __builtin_amdgcn_readlane(hi, 63);
+      const int nt = (int)(((unsigned)(hi - lo) * (unsigned)a.group + TM - 1) / TM);
+      const int incl = scan64(nt, [](int x, int y) { return x + y; });
+      const int total = __builtin_amdgcn_readlane(incl, 63);
+      if (t < total) {
+        const int fl = __builtin_ctzll(__ballot(incl > t));
+        tile->sequence = g0 + fl;
+        tile->row0 = (t - __builtin_amdgcn_readlane(incl - nt, fl)) * TM;
+        tile->first_token = __builtin_amdgcn_readlane(lo, fl);
+        tile->queries = __builtin_amdgcn_readlane(hi, fl) - tile->first_token;
+        break;
+      }
+      t -= total;
+    }
+  }
+  tile->rows = tile->queries * a.group - tile->row0;
+  int length = __builtin_amdgcn_readfirstlane(a.lengths[tile->sequence]);
+  length = length < 0 ? 0 : length > a.keys_most ? a.keys_most : length;
+  tile->length = length;
+  return true;
+}
+
+// Keys [lo, hi) that query x of a tile's sequence sees (lo < hi, or both 0).
+__device__ __forceinline__ void seen(const Args& a, const Tile& t, int x, int* lo, int* hi) {
+  const int at = t.length - t.queries + x;
+  *hi = at < 0 ? 0 : at + 1;
+  *lo = a.window > 0 && *hi > a.window ? *hi - a.window : 0;
+}
+
+// A page's record of a head, or null for a number that is no page.
+__device__ __forceinline__ const uint8_t* record_of(const Args& a, const Tile& t, int head, int key) {
+  const int page = a.table[t.sequence * a.ld_table + (key >> a.page_shift)];
+  return (unsigned)page < (unsigned)a.pages ? a.cache + ((int64_t)page * a.kv_heads + head) * a.record : nullptr;
+}
+
+// Eight BF16 query values as E4M3 parts (two words each) on the scale 2^(e - 127).
+// `lo` is 16 times what `hi` leaves.
+__device__ __forceinline__ void split8(uint4 v, int e, uint32_t* hi, uint32_t* lo) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    int h = 0, l = 0;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      const uint32_t d = w[2 * i + j];
+      const float x = ldexpf(bf_lo(d), 127 - e), y = ldexpf(bf_hi(d), 127 - e);
+      h = j ? __builtin_amdgcn_cvt_pk_fp8_f32(x, y, h, true) : __builtin_amdgcn_cvt_pk_fp8_f32(x, y, h, false);
+      const f32x2 r = j ? __builtin_amdgcn_cvt_pk_f32_fp8(h, true) : __builtin_amdgcn_cvt_pk_f32_fp8(h, false);
+      const float rx = (x - r.x) * 16.0f, ry = (y - r.y) * 16.0f;
+      l = j ? __builtin_amdgcn_cvt_pk_fp8_f32(rx, ry, l, true) : __builtin_amdgcn_cvt_pk_fp8_f32(rx, ry, l, false);
+    }
+    hi[i] = (uint32_t)h;
+    lo[i] = (uint32_t)l;
+  }
+}
+__device__ __forceinline__ uint32_t amax8(uint4 v) {
+  const uint32_t m = pk_max_u16(pk_max_u16(abs_bits2(v.x), abs_bits2(v.y)), pk_max_u16(abs_bits2(v.z), abs_bits2(v.w)));
+  return max(m & 0xFFFFu, m >> 16);
+}
+// Scale byte of `hi` (that of `lo` is 4 less) for a row's amax pattern.
+__device__ __forceinline__ int query_scale(uint32_t amax_bits) {
+  const int e = (int)(amax_bits >> 7);
+  return (e < 20 ? 20 : e > 254 ? 254 : e) - 7;
+}
+
+// A token's eight codes as four words of BF16 pairs.
+__device__ __forceinline__ void bf16_of(uint32_t codes, float scale, uint32_t* w) {
+  w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
+  w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
+  w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
+  w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
+}
+__device__ __forceinline__ float scale_of(uint32_t word, int byte) { return __uint_as_float(((word >> (8 * byte)) & 0xFFu) << 23); }
+
+// BF16 pair (t0, t1) of the low or high halves of two words.
+__device__ __forceinline__ uint32_t lows(uint32_t t0, uint32_t t1) { return __builtin_amdgcn_perm(t1, t0, 0x05040100u); }
+__device__ __forceinline__ uint32_t highs(uint32_t t0, uint32_t t1) { return __builtin_amdgcn_perm(t1, t0, 0x07060302u); }
+
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  const bf16x2 h = {(__bf16)x, (__bf16)y};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+}  // namespace kv
+
+// Tiles of TM rows that any offsets can give.
+inline int64_t kv_tiles(const KvAttention& a, int64_t tm) {
+  const int64_t group = a.heads / a.cache.heads;
+  if (!a.offsets) return a.sequences * ((group + tm - 1) / tm);
+  const int64_t with = a.sequences < a.tokens ? a.sequences : a.tokens;
+  return (a.tokens * group + with * (tm - 1)) / tm;
+}
+kv::Args kv_args(const KvAttention& a, int64_t parts);
+hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t parts, hipStream_t stream);
+
+}  // namespace mx

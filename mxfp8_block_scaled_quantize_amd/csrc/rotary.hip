@@ -1,0 +1,162 @@
+// Rotary positions: the pairs of a head's first 2 F dimensions turned by angles
+// that grow with the position.
+//
+// A thread takes one token's V neighbouring pairs (or V pairs of dimensions that
+// stay), makes their sines and cosines once and turns those of several heads of q
+// and k.  The angle in turns is position * turns[f], reduced to [-1/2, 1/2] in 64
+// bits (the product is exact to 2^-53 of itself: 4e-8 turns for a position of 2^31
+// at 1/(2 pi) turns each), so that far positions cost no accuracy; the rest is fp32.
+// Bound by HBM: every element is read and written once.
+
+#include "kv.h"
+#include "launch.h"
+#include "mx_device.h"
+
+namespace mx {
+
+namespace {
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32(_Float16 v) { return (float)v; }
+template <>
+__device__ __forceinline__ float to_f32(__bf16 v) { return (float)v; }
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Run {
+  T v[V];
+};
+
+struct Rotary {
+  RotaryRows q, k;
+  int64_t tokens;
+  int32_t head_dim, pairs, heads, heads_each, parts, turning;   // parts of a token: `turning` of them turn
+  const int32_t* positions;
+  const double* turns;
+  float magnitude;
+};
+
+template <typename T, int V, bool INTERLEAVED, bool INVERSE>
+__global__ __launch_bounds__(256) void rotary_kernel(Rotary r) {
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const uint32_t part = (uint32_t)(x % r.parts);
+  const int64_t y = x / r.parts;
+  const int groups = (r.heads + r.heads_each - 1) / r.heads_each;
+  const int64_t token = y / groups;
+  if (token >= r.tokens) return;
+  const int h0 = (int)(y % groups) * r.heads_each, h1 = h0 + r.heads_each < r.heads ? h0 + r.heads_each : r.heads;
+  const bool turn = part < (uint32_t)r.turning;
+  // the two runs of V dimensions that this thread takes (of those that stay: the
+  // second may be behind the end)
+  int64_t a, b;
+  float c[V], s[V];
+  if (turn) {
+    const int f = (int)part * V;
+    a = INTERLEAVED ? 2 * f : f;
+    b = INTERLEAVED ? 2 * f + V : f + r.pairs;
+    const double position = (double)r.positions[token];
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const double t = position * r.turns[f + i];
+      float sn, cs;
+      sincospif(2.0f * (float)(t - rint(t)), &sn, &cs);
+      c[i] = cs * r.magnitude;
+      s[i] = INVERSE ? -(sn * r.magnitude) : sn * r.magnitude;
+    }
+  } else {
+    a = 2 * (int64_t)r.pairs + (int64_t)(part - r.turning) * 2 * V;
+    b = a + V;
+  }
+  const bool second = b < r.head_dim;
+  for (int h = h0; h < h1; h++) {
+    const bool is_q = h < r.q.heads;
+    const RotaryRows& rows = is_q ? r.q : r.k;
+    const int64_t head = is_q ? h : h - r.q.heads;
+    const T* in = static_cast<const T*>(rows.in) + token * rows.token + head * rows.head;
+    T* out = static_cast<T*>(rows.out) + (token * rows.heads + head) * r.head_dim;
+    Run<T, V> u = *reinterpret_cast<const Run<T, V>*>(in + a), w = u;
+    if (second) w = *reinterpret_cast<const Run<T, V>*>(in + b);
+    if (turn) {
+      if (INTERLEAVED) {
+        T all[2 * V];
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          all[i] = u.v[i];
+          all[V + i] = w.v[i];
+        }
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          const float p = to_f32(all[2 * i]), q = to_f32(all[2 * i + 1]);
+          all[2 * i] = (T)(p * c[i] - q * s[i]);
+          all[2 * i + 1] = (T)(p * s[i] + q * c[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          u.v[i] = all[i];
+          w.v[i] = all[V + i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          const float p = to_f32(u.v[i]), q = to_f32(w.v[i]);
+          u.v[i] = (T)(p * c[i] - q * s[i]);
+          w.v[i] = (T)(p * s[i] + q * c[i]);
+        }
+      }
+    }
+    *reinterpret_cast<Run<T, V>*>(out + a) = u;
+    if (second) *reinterpret_cast<Run<T, V>*>(out + b) = w;
+  }
+}
+
+// Runs of V elements start on multiples of V everywhere: 16-byte accesses.
+bool wide(const RotaryRows& x, int64_t v, int64_t size) {
+  return x.heads == 0 || ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) % 16 == 0 &&
+                          x.token % v == 0 && x.head % v == 0 && v * size == 16);
+}
+
+template <typename T, int V>
+hipError_t launch(Rotary r, bool interleaved, bool inverse, hipStream_t stream) {
+  r.turning = r.pairs / V;
+  const int64_t rest = r.head_dim - 2 * (int64_t)r.pairs;
+  r.parts = (int)(r.turning + (rest + 2 * V - 1) / (2 * V));
+  // heads of a thread: up to 8, fewer where that would leave less than 8 waves a
+  // compute unit
+  r.heads_each = 8;
+  while (r.heads_each > 1 && r.tokens * r.parts * ((r.heads + r.heads_each - 1) / r.heads_each) < 256 * 8 * 64) r.heads_each >>= 1;
+  const int64_t groups = (r.heads + r.heads_each - 1) / r.heads_each;
+  const dim3 grid((unsigned)((r.tokens * r.parts * groups + 255) / 256));
+#define MX_ROT(IL, INV) hipLaunchKernelGGL((rotary_kernel<T, V, IL, INV>), grid, dim3(256), 0, stream, r)
+  if (interleaved) { if (inverse) MX_ROT(true, true); else MX_ROT(true, false); }
+  else { if (inverse) MX_ROT(false, true); else MX_ROT(false, false); }
+#undef MX_ROT
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_type(const Rotary& r, bool interleaved, bool inverse, hipStream_t stream) {
+  constexpr int V = 16 / sizeof(T);
+  const bool w = r.pairs % V == 0 && r.head_dim % V == 0 && wide(r.q, V, sizeof(T)) && wide(r.k, V, sizeof(T));
+  return w ? launch<T, V>(r, interleaved, inverse, stream) : launch<T, 1>(r, interleaved, inverse, stream);
+}
+
+}  // namespace
+
+bool rotary_grid_fits(int64_t tokens, int64_t heads, int64_t head_dim) {
+  return heads <= kMaxWorkItems && head_dim <= kMaxWorkItems && grid_fits(tokens, heads * head_dim, 1) &&
+         tokens * heads * head_dim <= kMaxWorkItems - 255;
+}
+
+hipError_t launch_rotary(RotaryRows q, RotaryRows k, int dtype, int64_t tokens, int64_t head_dim, int64_t pairs,
+                         const int32_t* positions, const double* turns, float magnitude, bool interleaved, bool inverse,
+                         hipStream_t stream) {
+  const Rotary r{q, k, tokens, (int32_t)head_dim, (int32_t)pairs, (int32_t)(q.heads + k.heads), 1, 0, 0, positions, turns, magnitude};
+  if (dtype == 0) return launch_type<float>(r, interleaved, inverse, stream);
+  if (dtype == 1) return launch_type<__bf16>(r, interleaved, inverse, stream);
+  return launch_type<_Float16>(r, interleaved, inverse, stream);
+}
+
+}  // namespace mx

@@ -1,5 +1,5 @@
-// Tensor-level entry points of the MXFP4 and mixture-of-experts operators: the
-// extension module _mx_torch.  Each function checks its tensors, allocates the
+// Tensor-level entry points of the MXFP4, mixture-of-experts, key-value cache and
+// rotary operators: the extension module _mx_torch.  Each function checks its tensors, allocates the
 // outputs and makes one call of the C ABI on the current stream of the
 // tensors' device.  It is C++ because the smallest calls take less time on the
 // GPU than argument handling and allocations take in Python (one decoding step's
@@ -20,8 +20,10 @@
 #include <torch/csrc/autograd/functions/basic_ops.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "../../include/kvcache.h"
 #include "../../include/moe.h"
 #include "../../include/mxfp4.h"
+#include "../../include/rotary.h"
 
 namespace {
 
@@ -360,7 +362,7 @@ int32_t moe_dtype(const Tensor& t) {
 variable_list once_only(variable_list grads) {
   if (!at::GradMode::is_enabled()) return grads;
   auto node = std::make_shared<torch::autograd::DelayedError>(
-      "the mixture-of-experts operators are differentiable once", (int)grads.size());
+      "this operator is differentiable once", (int)grads.size());
   variable_list in;
   for (auto& g : grads) in.push_back(g.defined() ? g.detach().requires_grad_(true) : g);
   return (*node)(std::move(in));
@@ -545,6 +547,332 @@ PyObject* combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------------ key-value cache
+// The caller's cache: its sizes follow from its shape and the head size.
+struct CacheShape {
+  int64_t pages, kv_heads;
+  int32_t page_size, head_dim;
+};
+CacheShape cache_shape(const Tensor& c, int64_t head_dim) {
+  if (c.scalar_type() != at::kByte || c.dim() != 3) refuse("cache must be a uint8 [pages, kv_heads, bytes] tensor");
+  need(c, "cache", at::kByte, c.sizes(), c.device());
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) refuse("head_dim must be 64, 128 or 256, got " + std::to_string(head_dim));
+  const int64_t token = head_dim + head_dim / 16;
+  const int64_t page = c.size(2) / token;
+  if (c.size(2) % token || page < 16 || page > 256 || (page & (page - 1)))
+    refuse("a cache of heads of " + std::to_string(head_dim) + " has 16, 32, 64, 128 or 256 times " + std::to_string(token) +
+           " bytes to a page and head, got " + std::to_string(c.size(2)));
+  if (c.size(0) < 1 || c.size(1) < 1) refuse("cache has no page or no head");
+  if (c.size(1) > INT32_MAX) refuse("too many heads");
+  return {c.size(0), c.size(1), (int32_t)page, (int32_t)head_dim};
+}
+// A BF16 [tokens, heads, head_dim] tensor with unit stride along the head.
+const Tensor& rows3(PyObject* o, const char* name) {
+  const std::string text = std::string(name) + " must be a BF16 [tokens, heads, head_dim] tensor with unit stride along the head";
+  if (!THPVariable_Check(o)) refuse(text, PyExc_TypeError);
+  const Tensor& t = THPVariable_Unpack(o);
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || (t.size(2) > 1 && t.stride(2) != 1)) refuse(text);
+  on_gpu(t, name);
+  return t;
+}
+// Strides of a dimension of size 1 say nothing.
+int64_t stride_of(const Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+void no_gradient(const Tensor& t, const char* name) {
+  if (t.requires_grad() && at::GradMode::is_enabled())
+    refuse(std::string(name) + " requires a gradient, which this operator does not have: call it with gradients disabled");
+  no_tangent(&t, name);
+}
+// The caller's block table [rows, width].
+const Tensor& block_table(PyObject* o, int64_t rows, c10::Device dev) {
+  const Tensor& t = tensor(o, "table");
+  if (t.dim() != 2) refuse("table must be an int32 [requests, pages] tensor");
+  on_gpu(t, "table");
+  if (t.scalar_type() != at::kInt || !unit_columns(t)) refuse("table must be int32 with unit stride along a request's pages");
+  if (t.size(0) != rows) refuse("table has " + std::to_string(t.size(0)) + " requests, lengths " + std::to_string(rows));
+  if (t.device() != dev) refuse("table is on " + t.device().str() + ", expected " + dev.str());
+  return t;
+}
+int64_t length_of(PyObject* o, const char* name) {
+  const Tensor& t = tensor(o, name);
+  if (t.dim() != 1) refuse(std::string(name) + " must have one dimension");
+  return t.size(0);
+}
+
+// extend(table, lengths, counts, free, free_count, tokens, page_size)
+PyObject* kv_extend_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 7);
+    const int64_t B = length_of(a[1], "lengths"), pages = length_of(a[3], "free"), T = integer(a[5], "tokens");
+    const Tensor &lengths = tensor(a[1], "lengths"), &counts = tensor(a[2], "counts"), &free = tensor(a[3], "free"),
+                 &free_count = tensor(a[4], "free_count");
+    const c10::Device dev = lengths.device();
+    need(lengths, "lengths", at::kInt, {B}, dev);
+    need(counts, "counts", at::kInt, {B}, dev);
+    need(free, "free", at::kInt, {pages}, dev);
+    need(free_count, "free_count", at::kInt, {1}, dev);
+    const Tensor& table = block_table(a[0], B, dev);
+    const int32_t page = small_integer(a[6], "page_size");
+    if (T < 0 || T >= INT32_MAX) refuse("tokens is out of range");
+    c10::DeviceGuard guard(dev);
+    at::AutoDispatchBelowADInplaceOrView below;
+    Block all(dev);
+    const std::array<int64_t, 5> size{B + 1, B, T, T, 1};
+    std::array<size_t, 5> at_;
+    for (int i = 0; i < 5; i++) at_[i] = all.add({size[i]}, at::kInt);
+    all.make();
+    std::array<Tensor, 5> o;
+    for (int i = 0; i < 5; i++) o[i] = all.get(at_[i], {size[i]}, at::kInt);
+    check(kv_extend(table.data_ptr<int32_t>(), ld(table), table.size(1), lengths.const_data_ptr<int32_t>(),
+                    counts.const_data_ptr<int32_t>(), B, free.const_data_ptr<int32_t>(), free_count.const_data_ptr<int32_t>(),
+                    pages, page, T, o[0].data_ptr<int32_t>(), o[1].data_ptr<int32_t>(), o[2].data_ptr<int32_t>(),
+                    o[3].data_ptr<int32_t>(), o[4].data_ptr<int32_t>(), stream_of(dev)),
+          "kv_extend");
+    written(&table);
+    PyObject* r = PyTuple_New(5);
+    if (r)
+      for (int i = 0; i < 5; i++) PyTuple_SET_ITEM(r, i, wrap(o[i]));
+    return r;
+  });
+}
+
+// release(table, lengths, finished, free, free_count, page_size)
+PyObject* kv_release_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 6);
+    const int64_t B = length_of(a[1], "lengths"), pages = length_of(a[3], "free");
+    const Tensor &lengths = tensor(a[1], "lengths"), &finished = tensor(a[2], "finished"), &free = tensor(a[3], "free"),
+                 &free_count = tensor(a[4], "free_count");
+    const c10::Device dev = lengths.device();
+    need(lengths, "lengths", at::kInt, {B}, dev);
+    need(finished, "finished", at::kBool, {B}, dev);
+    need(free, "free", at::kInt, {pages}, dev);
+    need(free_count, "free_count", at::kInt, {1}, dev);
+    const Tensor& table = block_table(a[0], B, dev);
+    const int32_t page = small_integer(a[5], "page_size");
+    c10::DeviceGuard guard(dev);
+    at::AutoDispatchBelowADInplaceOrView below;
+    Block all(dev);
+    const size_t at_l = all.add({B}, at::kInt), at_c = all.add({1}, at::kInt);
+    all.make();
+    Tensor l = all.get(at_l, {B}, at::kInt), c = all.get(at_c, {1}, at::kInt);
+    check(kv_release(table.data_ptr<int32_t>(), ld(table), table.size(1), lengths.const_data_ptr<int32_t>(),
+                     static_cast<const uint8_t*>(finished.const_data_ptr()), B, free.data_ptr<int32_t>(),
+                     free_count.const_data_ptr<int32_t>(), pages, page, l.data_ptr<int32_t>(), c.data_ptr<int32_t>(),
+                     stream_of(dev)),
+          "kv_release");
+    written(&table);
+    written(&free);
+    return pair(l, c);
+  });
+}
+
+// append(cache, k, v, slots)
+PyObject* kv_append_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 4);
+    const Tensor &cache = tensor(a[0], "cache"), &k = rows3(a[1], "k"), &v = rows3(a[2], "v"), &slots = tensor(a[3], "slots");
+    const CacheShape s = cache_shape(cache, k.size(2));
+    const c10::Device dev = cache.device();
+    const int64_t T = k.size(0);
+    if (k.size(1) != s.kv_heads) refuse("k has " + std::to_string(k.size(1)) + " heads, the cache " + std::to_string(s.kv_heads));
+    if (v.sizes() != k.sizes()) refuse("v must have k's shape " + shape_text(k.sizes()) + ", got " + shape_text(v.sizes()));
+    for (const Tensor* t : {&k, &v})
+      if (t->device() != dev) refuse("k and v are on " + t->device().str() + ", expected " + dev.str());
+    need(slots, "slots", at::kInt, {T}, dev);
+    no_gradient(k, "k");
+    no_gradient(v, "v");
+    c10::DeviceGuard guard(dev);
+    at::AutoDispatchBelowADInplaceOrView below;
+    check(kv_append(cache.data_ptr<uint8_t>(), s.pages, s.page_size, (int32_t)s.kv_heads, s.head_dim, k.const_data_ptr(),
+                    stride_of(k, 0), stride_of(k, 1), v.const_data_ptr(), stride_of(v, 0), stride_of(v, 1),
+                    slots.const_data_ptr<int32_t>(), T, stream_of(dev)),
+          "kv_append");
+    written(&cache);
+    Py_RETURN_NONE;
+  });
+}
+
+// read(cache, slots, head_dim)
+PyObject* kv_read_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 3);
+    const Tensor &cache = tensor(a[0], "cache"), &slots = tensor(a[1], "slots");
+    const CacheShape s = cache_shape(cache, integer(a[2], "head_dim"));
+    const c10::Device dev = cache.device();
+    const int64_t T = length_of(a[1], "slots");
+    need(slots, "slots", at::kInt, {T}, dev);
+    c10::DeviceGuard guard(dev);
+    at::AutoDispatchBelowADInplaceOrView below;
+    const std::array<int64_t, 3> shape{T, s.kv_heads, s.head_dim};
+    Block both(dev);
+    const size_t at_k = both.add(shape, at::kBFloat16), at_v = both.add(shape, at::kBFloat16);
+    both.make();
+    Tensor k = both.get(at_k, shape, at::kBFloat16), v = both.get(at_v, shape, at::kBFloat16);
+    check(kv_read(cache.const_data_ptr<uint8_t>(), s.pages, s.page_size, (int32_t)s.kv_heads, s.head_dim,
+                  slots.const_data_ptr<int32_t>(), T, k.data_ptr(), v.data_ptr(), stream_of(dev)),
+          "kv_read");
+    return pair(k, v);
+  });
+}
+
+// attention(q, cache, table, lengths, offsets, scale, window, max_queries, lse, out)
+PyObject* kv_attention_(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 10);
+    const Tensor &q = rows3(a[0], "q"), &cache = tensor(a[1], "cache"), &lengths = tensor(a[3], "lengths");
+    const CacheShape s = cache_shape(cache, q.size(2));
+    const c10::Device dev = q.device();
+    if (cache.device() != dev) refuse("cache is on " + cache.device().str() + ", expected " + dev.str());
+    const int64_t T = q.size(0), H = q.size(1), B = length_of(a[3], "lengths");
+    if (H < 1 || H % s.kv_heads || H > INT32_MAX)
+      refuse("q has " + std::to_string(H) + " heads, the cache " + std::to_string(s.kv_heads) + ", which must divide them");
+    need(lengths, "lengths", at::kInt, {B}, dev);
+    const Tensor& table = block_table(a[2], B, dev);
+    const Tensor* offsets = tensor_or_none(a[4], "offsets");
+    if (offsets) need(*offsets, "offsets", at::kInt, {B + 1}, dev);
+    else if (T != B) refuse("without offsets every sequence has one query: q has " + std::to_string(T) + ", lengths " + std::to_string(B));
+    double scale = 1.0 / std::sqrt((double)s.head_dim);
+    if (a[5] != Py_None) {
+      scale = PyFloat_AsDouble(a[5]);
+      if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    }
+    if (!((float)scale > 0.0f) || !std::isfinite((float)scale)) refuse("scale must be a positive finite number");
+    const int64_t window = integer(a[6], "window");
+    if (window < 0) refuse("window must not be negative (0: none)");
+    int64_t most = T > 1 ? T : 1;
+    if (a[7] != Py_None) {
+      most = integer(a[7], "max_queries");
+      if (most < 1) refuse("max_queries must be at least 1");
+    }
+    const bool with_lse = truth(a[8]);
+    const Tensor* out = tensor_or_none(a[9], "out");
+    no_gradient(q, "q");
+    const std::array<int64_t, 3> shape{T, H, s.head_dim};
+    if (out) {
+      need(*out, "out", at::kBFloat16, shape, dev);
+      no_gradient(*out, "out");
+    }
+    c10::DeviceGuard guard(dev);
+    at::AutoDispatchBelowADInplaceOrView below;
+    const size_t bytes = kv_attention_workspace_bytes(T, (int32_t)H, (int32_t)s.kv_heads, s.head_dim, B, table.size(1), s.page_size,
+                                                      offsets != nullptr, most, window);
+    Tensor work, o = out ? *out : fresh(shape, at::kBFloat16, dev), lse;
+    if (bytes) work = fresh({(int64_t)bytes}, at::kByte, dev);
+    if (with_lse) lse = fresh({T, H}, at::kFloat, dev);
+    check(kv_attention(q.const_data_ptr(), stride_of(q, 0), stride_of(q, 1), T, (int32_t)H, cache.const_data_ptr<uint8_t>(), s.pages,
+                       s.page_size, (int32_t)s.kv_heads, s.head_dim, table.const_data_ptr<int32_t>(), ld(table), table.size(1),
+                       lengths.const_data_ptr<int32_t>(), offsets ? offsets->const_data_ptr<int32_t>() : nullptr, B, most,
+                       (float)scale, window, o.data_ptr(), with_lse ? lse.data_ptr<float>() : nullptr,
+                       bytes ? work.data_ptr() : nullptr, bytes, stream_of(dev)),
+          "kv_attention");
+    written(out);
+    return with_lse ? pair(o, lse) : wrap(o);
+  });
+}
+
+// --------------------------------------------------------------------- rotary
+int32_t rotary_dtype(const Tensor& t) {
+  switch (t.scalar_type()) {
+    case at::kFloat: return ROTARY_FP32;
+    case at::kBFloat16: return ROTARY_BF16;
+    case at::kHalf: return ROTARY_FP16;
+    default: return -1;
+  }
+}
+struct Turn {
+  Tensor positions, turns;
+  double magnitude;
+  uint32_t flags;
+};
+// q and k (which may be undefined) turned: fresh tensors.
+std::pair<Tensor, Tensor> rotate_both(const Tensor& q, const Tensor& k, const Turn& t) {
+  const Tensor& some = q.defined() ? q : k;
+  c10::DeviceGuard guard(some.device());
+  at::AutoDispatchBelowADInplaceOrView below;
+  Block both(some.device());
+  const size_t at_q = q.defined() ? both.add(q.sizes(), q.scalar_type()) : 0;
+  const size_t at_k = k.defined() ? both.add(k.sizes(), k.scalar_type()) : 0;
+  both.make();
+  Tensor qo, ko;
+  if (q.defined()) qo = both.get(at_q, q.sizes(), q.scalar_type());
+  if (k.defined()) ko = both.get(at_k, k.sizes(), k.scalar_type());
+  check(rotary_rotate(q.defined() ? q.const_data_ptr() : nullptr, q.defined() ? stride_of(q, 0) : 0, q.defined() ? stride_of(q, 1) : 0,
+                      q.defined() ? q.size(1) : 0, k.defined() ? k.const_data_ptr() : nullptr, k.defined() ? stride_of(k, 0) : 0,
+                      k.defined() ? stride_of(k, 1) : 0, k.defined() ? k.size(1) : 0, rotary_dtype(some), some.size(0), some.size(2),
+                      t.turns.numel(), t.positions.const_data_ptr<int32_t>(), t.turns.const_data_ptr<double>(), (float)t.magnitude,
+                      t.flags, qo.defined() ? qo.data_ptr() : nullptr, ko.defined() ? ko.data_ptr() : nullptr,
+                      stream_of(some.device())),
+        "rotary_rotate");
+  return {qo, ko};
+}
+
+struct Rotate : torch::autograd::Function<Rotate> {
+  static variable_list forward(AutogradContext* ctx, const Variable& q, const std::optional<Tensor>& k, const Tensor& positions,
+                               const Tensor& turns, double magnitude, int64_t flags) {
+    ctx->save_for_backward({positions, turns});
+    ctx->saved_data["magnitude"] = magnitude;
+    ctx->saved_data["flags"] = flags;
+    ctx->set_materialize_grads(false);
+    auto [qo, ko] = rotate_both(q, k ? *k : Tensor(), {positions, turns, magnitude, (uint32_t)flags});
+    if (!k) return {qo};
+    return {qo, ko};
+  }
+  static variable_list backward(AutogradContext* ctx, variable_list grads) {
+    const auto saved = ctx->get_saved_variables();
+    variable_list out(6);
+    auto usable = [&](size_t i) {
+      if (i >= grads.size() || !grads[i].defined() || !ctx->needs_input_grad(i)) return Tensor();
+      at::AutoDispatchBelowADInplaceOrView below;
+      return grads[i].size(2) > 1 && grads[i].stride(2) != 1 ? grads[i].contiguous() : grads[i].detach();
+    };
+    const Tensor dq = usable(0), dk = usable(1);
+    if (dq.defined() || dk.defined()) {
+      auto [q, k] = rotate_both(dq, dk, {saved[0], saved[1], ctx->saved_data["magnitude"].toDouble(),
+                                         (uint32_t)(ctx->saved_data["flags"].toInt() ^ ROTARY_INVERSE)});
+      out[0] = q;
+      out[1] = k;
+    }
+    return once_only(std::move(out));
+  }
+};
+
+// rotate(q, k, positions, turns, interleaved, magnitude)
+PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 6);
+    const char* text = "q must be a [tokens, heads, head_dim] tensor of float32, bfloat16 or float16 with unit stride along the head";
+    if (!THPVariable_Check(a[0])) refuse(text, PyExc_TypeError);
+    const Tensor& q = THPVariable_Unpack(a[0]);
+    const Tensor* k = tensor_or_none(a[1], "k");
+    if (rotary_dtype(q) < 0 || q.dim() != 3 || (q.size(2) > 1 && q.stride(2) != 1)) refuse(text);
+    on_gpu(q, "q");
+    const c10::Device dev = q.device();
+    if (k) {
+      if (k->scalar_type() != q.scalar_type() || k->dim() != 3 || k->size(0) != q.size(0) || k->size(2) != q.size(2) ||
+          (k->size(2) > 1 && k->stride(2) != 1))
+        refuse("k must be [tokens, heads, head_dim] with q's type, tokens and head_dim and unit stride along the head");
+      if (k->device() != dev) refuse("k is on " + k->device().str() + ", expected " + dev.str());
+    }
+    const Tensor &positions = tensor(a[2], "positions"), &turns = tensor(a[3], "turns");
+    need(positions, "positions", at::kInt, {q.size(0)}, dev);
+    need(turns, "turns", at::kDouble, {length_of(a[3], "turns")}, dev);
+    if (2 * turns.numel() > q.size(2)) refuse("turns has more pairs than a head has dimensions");
+    const bool interleaved = truth(a[4]);
+    const double magnitude = PyFloat_AsDouble(a[5]);
+    if (magnitude == -1.0 && PyErr_Occurred()) throw python_error();
+    no_tangent(&q, "q");
+    no_tangent(k, "k");
+    no_gradient(turns, "turns");
+    const int64_t flags = interleaved ? ROTARY_INTERLEAVED : 0;
+    if (at::GradMode::is_enabled() && (q.requires_grad() || (k && k->requires_grad()))) {
+      auto r = Rotate::apply(q, k ? std::optional<Tensor>(*k) : std::nullopt, positions, turns, magnitude, flags);
+      return k ? pair(r[0], r[1]) : wrap(r[0]);
+    }
+    auto [qo, ko] = rotate_both(q, k ? *k : Tensor(), {positions, turns, magnitude, (uint32_t)flags});
+    return k ? pair(qo, ko) : wrap(qo);
+  });
+}
+
 #define MX_FN(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f))
 PyMethodDef methods[] = {{"quantize", MX_FN(quantize), METH_FASTCALL, nullptr},
                          {"dequantize", MX_FN(dequantize), METH_FASTCALL, nullptr},
@@ -553,6 +881,12 @@ PyMethodDef methods[] = {{"quantize", MX_FN(quantize), METH_FASTCALL, nullptr},
                          {"route", MX_FN(route), METH_FASTCALL, nullptr},
                          {"dispatch", MX_FN(dispatch), METH_FASTCALL, nullptr},
                          {"combine", MX_FN(combine), METH_FASTCALL, nullptr},
+                         {"extend", MX_FN(kv_extend_), METH_FASTCALL, nullptr},
+                         {"release", MX_FN(kv_release_), METH_FASTCALL, nullptr},
+                         {"append", MX_FN(kv_append_), METH_FASTCALL, nullptr},
+                         {"read", MX_FN(kv_read_), METH_FASTCALL, nullptr},
+                         {"attention", MX_FN(kv_attention_), METH_FASTCALL, nullptr},
+                         {"rotate", MX_FN(rotate), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_mx_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
