@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(HERE, "libmxfp8.so")
 CALIB_PATH = os.path.join(HERE, "libmxfp8_calib.so")
 SOURCES = ["api.hip", "quantize.hip", "pack_scales.hip", "gemm.hip", "api_mx4.hip", "mx4_quantize.hip", "mx4_gemm.hip",
            "mx4_gemm_mid.hip", "mx4_gemm_tile.hip", "moe.hip", "api_kv.hip", "kv_pages.hip", "kv_copy.hip", "kv_attention.hip",
-           "rotary.hip"]
+           "kv_attention_tile.hip", "rotary.hip"]
 CALIB_SOURCES = ["calib.hip"]
 TORCH_PATH = os.path.join(HERE, "_mx_torch.so")
 TORCH_SOURCE = "torch_binding.cpp"

@@ -347,31 +347,37 @@ __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
 
 int64_t group_of(const KvAttention& a) { return a.heads / a.cache.heads; }
 
-// Rows of a tile.
+// Rows of a tile: 16 or 32 for a run of queries that fits, else 128 (the kernel for
+// many queries).
 int64_t rows_of(const KvAttention& a) {
   const int64_t rows = a.max_queries < 65536 ? a.max_queries * group_of(a) : 65536;
-  return rows <= 16 ? 16 : 32;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
 // Parts that the keys of a tile are cut into.
 int64_t parts_of(const KvAttention& a) {
-  const int64_t blocks = kv_tiles(a, rows_of(a)) * a.cache.heads;
+  const int64_t tm = rows_of(a), blocks = kv_tiles(a, tm) * a.cache.heads;
   int64_t keys = a.table_width * a.cache.page_size;
   if (a.window > 0 && a.window + a.max_queries < keys) keys = a.window + a.max_queries;
-  int64_t parts = 1024 / (blocks > 0 ? blocks : 1);
-  const int64_t most = keys / 256;
+  int64_t parts = (tm == 128 ? 512 : 1024) / (blocks > 0 ? blocks : 1);
+  const int64_t most = keys / (tm == 128 ? 512 : 256);
   parts = parts < most ? parts : most;
   return parts < 1 ? 1 : parts > 64 ? 64 : parts;
 }
 
 template <int D>
-hipError_t launch_rows(const KvAttention& a, int64_t parts, hipStream_t stream) {
+hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
   const Args g = kv_args(a, parts);
   const int64_t tm = rows_of(a);
   const dim3 grid((unsigned)(kv_tiles(a, tm) * parts * a.cache.heads));
-  if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
-  else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);
-  hipError_t e = hipGetLastError();
+  hipError_t e = hipSuccess;
+  if (tm == 128) {
+    e = launch_kv_attention_tile(a, parts, stream);
+  } else {
+    if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
+    else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);
+    e = hipGetLastError();
+  }
   if (e == hipSuccess && parts > 1) {
     hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)(a.tokens * a.heads)), dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
@@ -420,9 +426,9 @@ bool kv_attention_grid_fits(const KvAttention& a) {
 
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream) {
   const int64_t parts = parts_of(a);
-  if (a.cache.head_dim == 64) return launch_rows<64>(a, parts, stream);
-  if (a.cache.head_dim == 128) return launch_rows<128>(a, parts, stream);
-  return launch_rows<256>(a, parts, stream);
+  if (a.cache.head_dim == 64) return launch_all<64>(a, parts, stream);
+  if (a.cache.head_dim == 128) return launch_all<128>(a, parts, stream);
+  return launch_all<256>(a, parts, stream);
 }
 
 }  // namespace mx

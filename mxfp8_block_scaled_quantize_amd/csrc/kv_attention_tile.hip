@@ -1,0 +1,333 @@
+// Attention of many queries (prompts, pieces of prompts) over the paged MXFP4 cache:
+// bound by the matrix cores and, beside them, by the softmax's exponentials.
+//
+// A workgroup of 4 waves has 128 rows of one sequence and key-value head, 32 a wave,
+// and goes through its keys 64 at a time.  S^T = K Q^T by 32x32x64 scaled MFMAs whose
+// FP4 operand is 16 bytes of a key's codes a lane, loaded straight from the cache a
+// step ahead.  Lane (c, h) = (l % 32, l / 32) gets the scores of row c and keys 8 (i /
+// 4) + 4 h + i % 4 of each 32: its eight registers of every 16 keys are the second
+// product's operand as they are, with that product's keys in the order (4 h + 0..3, 8 +
+// 4 h + 0..3) for lane half h.  The values are turned to BF16 once for the workgroup,
+// a step ahead: a lane takes 4 keys x 8 values, swaps them pairwise and writes, for each
+// value, the 4 keys to an LDS row of 64 keys in that order (two buffers, 16-byte chunks
+// XOR-swizzled by the row so that neither writes nor reads collide).  O^T = V^T P^T by
+// 32x32x16 MFMAs.  One barrier a step.
+#include "kv_attention.h"
+
+namespace mx {
+
+using namespace kv;
+
+namespace {
+
+constexpr int KEYS = 64;
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+
+// The step's four runs of 16 keys: where their records are (null: no page, or no key).
+typedef uint64_t u64x4 __attribute__((ext_vector_type(4)));
+struct Runs {
+  u64x4 r;   // a vector, so that one chosen by a lane is selected in registers
+  __device__ __forceinline__ void find(const Args& a, const Tile& t, int head, int key, int end) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = key + 16 * i < end ? reinterpret_cast<uint64_t>(record_of(a, t, head, key + 16 * i)) : 0;
+  }
+  __device__ __forceinline__ bool all() const { return r[0] && r[1] && r[2] && r[3]; }
+  __device__ __forceinline__ const uint8_t* of(int run) const {
+    const uint64_t x = run == 0 ? r[0] : run == 1 ? r[1] : run == 2 ? r[2] : r[3];
+    return reinterpret_cast<const uint8_t*>(x);
+  }
+};
+
+// What a lane loads of a step's keys: 32 codes (16 bytes) and a scale for every MFMA.
+template <int D>
+struct KeyPart {
+  static constexpr int KS = D / 64;   // MFMA steps along a key
+  u32x4 k[2][KS];
+  uint32_t s[2][(KS + 1) / 2];
+  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int key) {
+    const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    const int page_size = 1 << a.page_shift;
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const uint8_t* r = c < 16 ? runs.of(2 * i) : runs.of(2 * i + 1);
+      if (!r) r = a.cache;   // any record: what comes is not used
+      const int at = (key + 32 * i + c) & (page_size - 1);
+#pragma unroll
+      for (int f = 0; f < KS; f++) k[i][f] = *reinterpret_cast<const u32x4*>(r + at * (D / 2) + 16 * (2 * f + h));
+      const uint8_t* b = r + page_size * D + at * (D / 32);
+      if (D == 64) s[i][0] = *reinterpret_cast<const uint16_t*>(b);
+      else {
+#pragma unroll
+        for (int f = 0; f < KS / 2; f++) s[i][f] = reinterpret_cast<const uint32_t*>(b)[f];
+      }
+    }
+  }
+};
+
+// What a lane loads of a step's values: units of 4 keys x 8 values.
+template <int D>
+struct ValuePart {
+  static constexpr int UNITS = D == 256 ? 2 : 1;
+  u32x4 v[UNITS];
+  uint32_t s[UNITS];
+  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int key) {
+    const int page_size = 1 << a.page_shift;
+#pragma unroll
+    for (int u = 0; u < UNITS; u++) {
+      const int x = threadIdx.x + 256 * u, group = x / (D / 8), d = x % (D / 8), run = group >> 2;
+      if (D == 64 && x >= 128) break;   // whole waves
+      const uint8_t* r = runs.of(D == 64 ? run : __builtin_amdgcn_readfirstlane(run));
+      if (!r) r = a.cache;
+      const int at = (key + 16 * run) & (page_size - 1);
+      v[u] = *reinterpret_cast<const u32x4*>(r + page_size * (D / 2) + ((at >> 2) + (group & 3)) * (2 * D) + 16 * d);
+      s[u] = *reinterpret_cast<const uint32_t*>(r + page_size * D + page_size * (D / 32) + (d >> 2) * page_size + at + 4 * (group & 3));
+    }
+  }
+  // As BF16 to the LDS rows.  Of places that no query sees, zeros.
+  __device__ __forceinline__ void store(const Runs& runs, int key, int end, lds_u8* to) {
+#pragma unroll
+    for (int u = 0; u < UNITS; u++) {
+      const int x = threadIdx.x + 256 * u, group = x / (D / 8), d = x % (D / 8);
+      if (D == 64 && x >= 128) break;
+      const int run = group >> 2, quad = group & 3;
+      if (key + KEYS > end || !runs.all()) {
+        const bool there = runs.of(run) != nullptr;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+          if (!there || key + 4 * group + j >= end) {
+            v[u][j] = 0;
+            s[u] &= ~(0xFFu << (8 * j));
+          }
+      }
+      uint32_t w[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; j++) bf16_of(v[u][j], scale_of(s[u], j), w[j]);
+      const int chunk = 2 * run + (quad & 1);
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        u32x2 word;
+        word.x = (i & 1) ? highs(w[0][i >> 1], w[1][i >> 1]) : lows(w[0][i >> 1], w[1][i >> 1]);
+        word.y = (i & 1) ? highs(w[2][i >> 1], w[3][i >> 1]) : lows(w[2][i >> 1], w[3][i >> 1]);
+        *reinterpret_cast<lds_u32x2*>(to + (8 * d + i) * 128 + ((chunk ^ i ^ d) & 7) * 16 + (quad >> 1) * 8) = word;
+      }
+    }
+  }
+};
+
+template <int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
+  constexpr int KS = KeyPart<D>::KS;
+  __shared__ __attribute__((aligned(16))) uint8_t values[2][D * 128];
+  lds_u8* const lds = (lds_u8*)&values[0][0];
+  const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int head = (int)(blockIdx.x % (unsigned)a.kv_heads);
+  const int rest = (int)(blockIdx.x / (unsigned)a.kv_heads);
+  const int part = rest % a.parts;
+  Tile t;
+  // the last tiles of a sequence, which see the most keys, first
+  if (!find_tile<128>(a, tiles - 1 - rest / a.parts, &t)) return;   // the whole workgroup
+  const int rows = t.rows < 128 ? t.rows : 128;
+  const int64_t all_rows = (int64_t)a.tokens * a.heads;
+
+  int first_lo, first_hi, last_lo, last_hi;
+  seen(a, t, t.row0 / a.group, &first_lo, &first_hi);
+  seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
+  const int begin = first_lo & ~(KEYS - 1), end = last_hi;
+  const int steps = (end - begin + KEYS - 1) / KEYS;
+  const int each = (steps + a.parts - 1) / a.parts;
+  const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
+
+  // this lane's row, and the keys of the wave's rows
+  const int row = 32 * w + c;
+  const bool valid = row < rows;
+  const int x = (t.row0 + (valid ? row : 0)) / a.group;
+  const int64_t token = t.first_token + x;
+  const int q_head = head * a.group + (t.row0 + (valid ? row : 0)) - x * a.group;
+  int lo, hi;
+  seen(a, t, x, &lo, &hi);
+  if (!valid) lo = hi = 0;
+  const bool has_rows = 32 * w < rows;   // wave-uniform
+  int wave_lo = 0, wave_hi = 0, all_lo = 0, all_hi = 0;   // keys that some row of the wave, that all of them see
+  if (has_rows) {
+    const int last = 32 * w + 31 < rows ? 32 * w + 31 : rows - 1;
+    seen(a, t, (t.row0 + 32 * w) / a.group, &wave_lo, &all_hi);
+    seen(a, t, (t.row0 + last) / a.group, &all_lo, &wave_hi);
+  }
+  v8i qh[KS], ql[KS];
+  int scale;
+  {
+    const uint16_t* q = a.q + token * a.q_token + q_head * a.q_head;
+    uint4 v[KS][4];
+    uint32_t m = 0;
+#pragma unroll
+    for (int s = 0; s < KS; s++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {   // bytes 0 .. 15: dimensions 16 h + .., 16 .. 31: 32 + 16 h + ..
+        v[s][i] = valid ? *reinterpret_cast<const uint4*>(q + 64 * s + 32 * (i >> 1) + 16 * h + 8 * (i & 1)) : make_uint4(0u, 0u, 0u, 0u);
+        m = max(m, amax8(v[s][i]));
+      }
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+    scale = query_scale(m);
+#pragma unroll
+    for (int s = 0; s < KS; s++)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        uint32_t x2[2], y2[2];
+        split8(v[s][i], scale, x2, y2);
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+          qh[s][2 * i + j] = (int)x2[j];
+          ql[s][2 * i + j] = (int)y2[j];
+        }
+      }
+  }
+
+  v16f o[D / 32];
+#pragma unroll
+  for (int d = 0; d < D / 32; d++)
+#pragma unroll
+    for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
+
+  Runs runs, ahead;   // of this step and the next
+  KeyPart<D> keys;
+  ValuePart<D> vals;
+  if (s0 < s1) {
+    runs.find(a, t, head, begin + KEYS * s0, end);
+    keys.load(a, runs, begin + KEYS * s0);
+    vals.load(a, runs, begin + KEYS * s0);
+    ahead.find(a, t, head, begin + KEYS * (s0 + 1), end);
+    vals.store(runs, begin + KEYS * s0, end, lds + (s0 & 1) * D * 128);
+  }
+  __syncthreads();
+  for (int s = s0; s < s1; s++) {
+    const int key = begin + KEYS * s;
+    const bool more = s + 1 < s1;
+    if (more) vals.load(a, ahead, key + KEYS);
+    const bool work = key < wave_hi && key + KEYS > wave_lo;   // wave-uniform
+    auto stage = [&]() {
+      if (more) vals.store(ahead, key + KEYS, end, lds + ((s + 1) & 1) * D * 128);
+    };
+    if (!work) {
+      if (more) keys.load(a, ahead, key + KEYS);
+      stage();
+    } else {
+      v16f y[2];
+#pragma unroll
+      for (int i = 0; i < 2; i++) {
+#pragma unroll
+        for (int j = 0; j < 16; j++) y[i][j] = 0.0f;
+#pragma unroll
+        for (int f = 0; f < KS; f++) {
+          v8i k{};
+          k.lo = __builtin_bit_cast(v4i, keys.k[i][f]);
+          const int ks = (int)(keys.s[i][f >> 1] >> (8 * h));   // byte 0, or 2 for an odd f
+          if (f & 1) {
+            y[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, ql[f], y[i], 4, 0, 2, ks, 0, scale - 4);
+            y[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, qh[f], y[i], 4, 0, 2, ks, 0, scale);
+          } else {
+            y[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, ql[f], y[i], 4, 0, 0, ks, 0, scale - 4);
+            y[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(k, qh[f], y[i], 4, 0, 0, ks, 0, scale);
+          }
+        }
+      }
+      if (more) keys.load(a, ahead, key + KEYS);   // in the registers that the products are done with
+      float mx = -INFINITY;
+      if (key >= all_lo && key + KEYS <= all_hi && runs.all()) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int j = 0; j < 16; j++) mx = fmaxf(mx, y[i][j]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int j = 0; j < 16; j++) {
+            const int at = key + 32 * i + 8 * (j >> 2) + 4 * h + (j & 3);
+            if (!(at >= lo && at < hi && runs.of(2 * i + (j >> 3)))) y[i][j] = -INFINITY;
+            mx = fmaxf(mx, y[i][j]);
+          }
+      }
+      mx *= a.scale2;
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      if (__any(mx > top + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
+        const float higher = fmaxf(mx, top);
+        const float shrink = higher > -INFINITY ? __builtin_amdgcn_exp2f(top - higher) : 1.0f;
+        top = higher;
+        sum *= shrink;
+#pragma unroll
+        for (int d = 0; d < D / 32; d++) o[d] *= shrink;
+      }
+      const float base = top > -INFINITY ? top : 0.0f;
+      u32x4 p[4];   // of 16 keys each
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+          const float e0 = __builtin_amdgcn_exp2f(fmaf(y[i][2 * j], a.scale2, -base));
+          const float e1 = __builtin_amdgcn_exp2f(fmaf(y[i][2 * j + 1], a.scale2, -base));
+          sum += e0 + e1;
+          p[2 * i + (j >> 2)][j & 3] = bf16_pair(e0, e1);
+        }
+      stage();
+      const lds_u8* v = lds + (s & 1) * D * 128 + c * 128;
+#pragma unroll
+      for (int f = 0; f < 4; f++) {
+#pragma unroll
+        for (int d = 0; d < D / 32; d++) {
+          const u32x4 vw = *reinterpret_cast<const lds_u32x4*>(v + d * 4096 + (((2 * f + h) ^ c ^ (4 * d + (c >> 3))) & 7) * 16);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vw), __builtin_bit_cast(bf16x8, p[f]), o[d], 0, 0, 0);
+        }
+      }
+    }
+    runs = ahead;
+    if (more) ahead.find(a, t, head, key + 2 * KEYS, end);
+    __syncthreads();
+  }
+
+  sum += __shfl_xor(sum, 32, 64);
+  if (!valid) return;
+  const int64_t at = token * a.heads + q_head;
+  const bool some = sum > 0.0f || sum != sum;
+  if (a.sums) {
+    if (h == 0) {
+      float* ml = a.sums + a.parts * all_rows * D + (part * all_rows + at) * 2;
+      ml[0] = top;
+      ml[1] = sum;
+    }
+    if (s0 >= s1) return;
+    float* to = a.sums + (part * all_rows + at) * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<v4f*>(to + 32 * d + 8 * i + 4 * h) = v4f{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+  } else {
+    const float factor = some ? 1.0f / sum : 0.0f;
+    if (a.lse && h == 0) a.lse[at] = some ? (top + __builtin_amdgcn_logf(sum)) * kLn2 : -INFINITY;
+    uint16_t* to = a.out + at * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; d++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<u32x2*>(to + 32 * d + 8 * i + 4 * h) =
+            u32x2{bf16_pair(o[d][4 * i] * factor, o[d][4 * i + 1] * factor), bf16_pair(o[d][4 * i + 2] * factor, o[d][4 * i + 3] * factor)};
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t parts, hipStream_t stream) {
+  const kv::Args g = kv_args(a, parts);
+  const int64_t tiles = kv_tiles(a, 128);
+  const dim3 grid((unsigned)(tiles * parts * a.cache.heads));
+  if (a.cache.head_dim == 64) hipLaunchKernelGGL(kv_attention_tile_kernel<64>, grid, dim3(256), 0, stream, g, (int)tiles);
+  else if (a.cache.head_dim == 128) hipLaunchKernelGGL(kv_attention_tile_kernel<128>, grid, dim3(256), 0, stream, g, (int)tiles);
+  else hipLaunchKernelGGL(kv_attention_tile_kernel<256>, grid, dim3(256), 0, stream, g, (int)tiles);
+  return hipGetLastError();
+}
+
+}  // namespace mx
