@@ -51,6 +51,7 @@ struct Args {
   float* __restrict__ lse;
   float* __restrict__ sums;   // O [parts][rows][D], then (m, l) [parts][rows][2]; null: one part
   int32_t tokens, heads, kv_heads, group, sequences, pages, page_shift, keys_most, window, parts;
+  int32_t least;              // steps of 32 keys of a part, at least
   float scale2;               // scale * log2(e)
 };
 
@@ -150,12 +151,18 @@ __device__ __forceinline__ int query_scale(uint32_t amax_bits) {
   return (e < 20 ? 20 : e > 254 ? 254 : e) - 7;
 }
 
+// Codes 2 x and 2 x + 1 of a word as a BF16 pair.
+__device__ __forceinline__ uint32_t bf16_pair_of(uint32_t codes, float scale, int x) {
+  const bf16x2 v = x == 0   ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0)
+                   : x == 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1)
+                   : x == 2 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2)
+                            : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+  return __builtin_bit_cast(uint32_t, v);
+}
 // A token's eight codes as four words of BF16 pairs.
 __device__ __forceinline__ void bf16_of(uint32_t codes, float scale, uint32_t* w) {
-  w[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0));
-  w[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1));
-  w[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2));
-  w[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3));
+#pragma unroll
+  for (int x = 0; x < 4; x++) w[x] = bf16_pair_of(codes, scale, x);
 }
 __device__ __forceinline__ float scale_of(uint32_t word, int byte) { return __uint_as_float(((word >> (8 * byte)) & 0xFFu) << 23); }
 

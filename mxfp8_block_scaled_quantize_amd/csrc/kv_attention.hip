@@ -19,16 +19,37 @@ using namespace kv;
 namespace {
 
 constexpr int WAVES = 4;
+// Codes are read once: non-temporal loads (64 sequences of up to 8192 tokens: 70 us, 77 without).
+constexpr int NT = 2;
 
-// Sum, or maximum, over the four lane groups (lanes 16 apart).
+// Maximum, or sum, over the four lane groups (lanes 16 apart): swapping rows of 16
+// (of 32) between two copies leaves each lane with its own and its partner's value.
 __device__ __forceinline__ float group_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
+  const uint32_t x = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  const uint32_t y = __float_as_uint(fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1])));
+  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 __device__ __forceinline__ float group_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  const uint32_t x = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  const uint32_t y = __float_as_uint(__uint_as_float(a[0]) + __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
+
+// Page numbers of a step's two runs of 16 keys.
+struct Pages {
+  int p[2];
+  __device__ __forceinline__ void find(const Args& a, const Tile& t, int key, int end) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int at = key + 16 * i < end ? key + 16 * i : end - 1;
+      p[i] = a.table[t.sequence * a.ld_table + (at >> a.page_shift)];
+    }
+  }
+};
 
 // 32 keys of one head as a lane loads them.
 template <int D>
@@ -38,40 +59,44 @@ struct Keys {
   uint32_t ks[2][KB], vs[2][KB];
   bool there[2];   // wave-uniform: the page is one
 
-  __device__ __forceinline__ void load(const Args& a, const Tile& t, int head, int key, int end) {
-    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
-    const int page_size = 1 << a.page_shift;
+  // No branch, so that the compiler can wait for one step's loads among those of the
+  // next ones: what is not there (no page, or `wanted` false) is an empty buffer,
+  // which reads as zeros.
+  __device__ __forceinline__ void load(const Args& a, const Pages& pages, int head, int key, bool wanted) {
+    const uint32_t lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const uint32_t page_size = 1u << a.page_shift;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const int at = key + 16 * i;
-      const uint8_t* r = at < end ? record_of(a, t, head, at) : nullptr;
-      there[i] = r != nullptr;
-      if (!r) r = a.cache;   // any record: what comes is not used
-      const int o = at & (page_size - 1);
-      const uint8_t* v0 = r + page_size * (D / 2);
-      const uint8_t* ks0 = r + page_size * D;
-      const uint8_t* vs0 = ks0 + page_size * (D / 32);
+      there[i] = (unsigned)pages.p[i] < (unsigned)a.pages;
+      const int page = there[i] ? pages.p[i] : 0;
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(a.cache) + ((int64_t)page * a.kv_heads + head) * a.record, 0, there[i] && wanted ? (int)a.record : 0,
+          0x00020000);
+      const int o = (key + 16 * i) & (int)(page_size - 1);
+      const int k0 = o * (D / 2), v0 = page_size * (D / 2) + (o >> 2) * (2 * D);
+      const int ks0 = page_size * D + o * (D / 32), vs0 = page_size * (D + D / 32) + o;
 #pragma unroll
       for (int b = 0; b < KB; b++) {
-        const int kb = D == 64 ? (g & 1) : g + 4 * b;              // block of 32 of the key
-        const int vd = D == 64 ? (c & 7) : c + 16 * b;             // eight values
-        k[i][b] = *reinterpret_cast<const u32x4*>(r + (o + c) * (D / 2) + 16 * kb);
-        ks[i][b] = ks0[(o + c) * (D / 32) + kb];
-        v[i][b] = *reinterpret_cast<const u32x4*>(v0 + ((o >> 2) + g) * (2 * D) + 16 * vd);
-        vs[i][b] = *reinterpret_cast<const uint32_t*>(vs0 + (vd >> 2) * page_size + o + 4 * g);
+        const uint32_t kb = D == 64 ? (g & 1) : g + 4 * b;              // block of 32 of the key
+        const uint32_t vd = D == 64 ? (c & 7) : c + 16 * b;             // eight values
+        k[i][b] = __builtin_amdgcn_raw_buffer_load_b128(r, c * (D / 2) + 16 * kb, k0, NT);
+        ks[i][b] = __builtin_amdgcn_raw_buffer_load_b8(r, c * (D / 32) + kb, ks0, 0);
+        v[i][b] = __builtin_amdgcn_raw_buffer_load_b128(r, g * (2 * D) + 16 * vd, v0, NT);
+        vs[i][b] = __builtin_amdgcn_raw_buffer_load_b32(r, (vd >> 2) * page_size + 4 * g, vs0, 0);
       }
     }
   }
 };
 
-template <int D, int NB>
-__global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
+template <int D, int NB, int DEPTH>
+__global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 64 ? 3 : 2) void kv_attention_rows_kernel(Args a) {
   constexpr int TM = 16 * NB;
   constexpr int KB = Keys<D>::KB;
   constexpr int DT = D / 16;         // 16-row blocks of O^T
   constexpr int TERMS = D == 64 ? 1 : 2;
-  __shared__ float meet[WAVES][4][64][4];
-  __shared__ float stats[WAVES][NB][16][2];
+  constexpr int CH = DT < 8 ? DT : 8;   // blocks that meet at a time
+  __shared__ __attribute__((aligned(16))) float meet[WAVES][CH][64][4];
+  __shared__ float stats[WAVES][16][2];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int head = (int)(blockIdx.x % (unsigned)a.kv_heads);
@@ -89,14 +114,14 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
   const int begin = first_lo & ~31, end = last_hi;
   const int steps = (end - begin + 31) / 32;
   int each = (steps + a.parts - 1) / a.parts;
+  each = each < a.least ? a.least : each;
   each = (each + WAVES - 1) / WAVES * WAVES;
   const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
 
   // the lane's rows: column c of each block
   int64_t token[NB];
   int q_head[NB], lo[NB], hi[NB];
-  v8i qh[NB][KB], ql[NB][KB];
-  int qs[NB];
+  uint4 qv[NB][2 * KB][2];
 #pragma unroll
   for (int n = 0; n < NB; n++) {
     const int row = 16 * n + c;
@@ -109,14 +134,38 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
     const uint16_t* q = a.q + token[n] * a.q_token + q_head[n] * a.q_head;
     // bytes 0 .. 15 of the FP8 operand are dimensions 16 g + (0 .. 15), the others 64 + 16 g + ..;
     // for 64 dimensions the second half is `lo` of the same ones
-    uint4 v[2 * KB][2];
+#pragma unroll
+    for (int b = 0; b < (D == 64 ? 1 : 2 * KB); b++)
+#pragma unroll
+      for (int i = 0; i < 2; i++) qv[n][b][i] = *reinterpret_cast<const uint4*>(q + 64 * b + 16 * g + 8 * i);
+  }
+
+  // DEPTH steps of the wave are on their way, and the page numbers of one more
+  Keys<D> ring[DEPTH];
+  Pages pages;
+  const int stride = 32 * WAVES, first = begin + 32 * (s0 + w), last = s0 < s1 ? begin + 32 * s1 : 0;
+  if (end > 0) {
+    pages.find(a, t, first, end);
+#pragma unroll
+    for (int u = 0; u < DEPTH; u++) {
+      ring[u].load(a, pages, head, first + u * stride, first + u * stride < last);
+      pages.find(a, t, first + (u + 1) * stride, end);
+      __builtin_amdgcn_sched_barrier(0);   // the steps' loads in the order of the loop
+    }
+  }
+
+  v8i qh[NB][KB], ql[NB][KB];
+  int qs[NB];
+#pragma unroll
+  for (int n = 0; n < NB; n++) {
+    const bool valid = 16 * n + c < rows;
     uint32_t m = 0;
 #pragma unroll
     for (int b = 0; b < (D == 64 ? 1 : 2 * KB); b++)
 #pragma unroll
       for (int i = 0; i < 2; i++) {
-        v[b][i] = valid ? *reinterpret_cast<const uint4*>(q + 64 * b + 16 * g + 8 * i) : make_uint4(0u, 0u, 0u, 0u);
-        m = max(m, amax8(v[b][i]));
+        if (!valid) qv[n][b][i] = make_uint4(0u, 0u, 0u, 0u);
+        m = max(m, amax8(qv[n][b][i]));
       }
     m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
@@ -128,7 +177,7 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
 #pragma unroll
         for (int i = 0; i < 2; i++) {
           uint32_t x2[2], y2[2];
-          split8(v[2 * b + h][i], qs[n], x2, y2);
+          split8(qv[n][2 * b + h][i], qs[n], x2, y2);
 #pragma unroll
           for (int j = 0; j < 2; j++) {
             qh[n][b][4 * h + 2 * i + j] = (int)x2[j];
@@ -149,20 +198,18 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
     for (int d = 0; d < DT; d++) o[n][d] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  Keys<D> now, next;
-  if (s0 + w < s1) now.load(a, t, head, begin + 32 * (s0 + w), end);
-  for (int s = s0 + w; s < s1; s += WAVES) {
-    const int key = begin + 32 * s;
-    if (s + WAVES < s1) next.load(a, t, head, key + 32 * WAVES, end);
+  // what every query of the tile sees
+  const int full_lo = last_lo, full_hi = first_hi;
+  auto step = [&](Keys<D>& now, const int key) {
     // values of places that no query sees are taken as zeros, whatever they hold
-    if (key + 32 > end || !now.there[0] || !now.there[1]) {
+    if (key + 32 > end) {
 #pragma unroll
       for (int i = 0; i < 2; i++)
 #pragma unroll
         for (int b = 0; b < KB; b++)
 #pragma unroll
           for (int j = 0; j < 4; j++)
-            if (!now.there[i] || key + 16 * i + 4 * g + j >= end) {
+            if (key + 16 * i + 4 * g + j >= end) {
               now.v[i][b][j] = 0;
               now.vs[i][b] &= ~(0xFFu << (8 * j));
             }
@@ -184,16 +231,21 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
         }
       }
       float mx = -INFINITY;
+      if (!(key >= full_lo && key + 32 <= full_hi && now.there[0] && now.there[1])) {
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+#pragma unroll
+          for (int j = 0; j < 4; j++) {
+            const int at = key + 16 * i + 4 * g + j;
+            if (!(now.there[i] && at >= lo[n] && at < hi[n])) x[i][j] = -INFINITY;
+          }
+      }
 #pragma unroll
       for (int i = 0; i < 2; i++)
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-          const int at = key + 16 * i + 4 * g + j;
-          x[i][j] = now.there[i] && at >= lo[n] && at < hi[n] ? x[i][j] * a.scale2 : -INFINITY;
-          mx = fmaxf(mx, x[i][j]);
-        }
-      mx = group_max(mx);
-      if (__any(mx > top[n])) {
+        for (int j = 0; j < 4; j++) mx = fmaxf(mx, x[i][j]);
+      mx = group_max(mx * a.scale2);
+      if (__any(mx > top[n] + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
         const float higher = fmaxf(mx, top[n]);
         const float shrink = higher > -INFINITY ? __builtin_amdgcn_exp2f(top[n] - higher) : 1.0f;
         top[n] = higher;
@@ -205,94 +257,103 @@ __global__ __launch_bounds__(64 * WAVES) void kv_attention_rows_kernel(Args a) {
       float e[8];
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        e[j] = __builtin_amdgcn_exp2f(x[j >> 2][j & 3] - base);
+        e[j] = __builtin_amdgcn_exp2f(fmaf(x[j >> 2][j & 3], a.scale2, -base));
         sum[n] += e[j];
         p[n][j] = (__bf16)e[j];
       }
     }
 #pragma unroll
     for (int b = 0; b < KB; b++) {
-      uint32_t val[2][4][4];   // BF16 pairs of each key
 #pragma unroll
-      for (int i = 0; i < 2; i++)
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-          // for 64 values lanes c and c + 8 take the halves of a word
-          const uint32_t codes = D == 64 ? now.v[i][b][j] >> (c & 8 ? 16 : 0) : now.v[i][b][j];
-          bf16_of(codes, scale_of(now.vs[i][b], j), val[i][j]);
-        }
-#pragma unroll
-      for (int d = 0; d < (D == 64 ? 4 : 8); d++) {
-        u32x4 word;
+      for (int x = 0; x < (D == 64 ? 2 : 4); x++) {   // two of the eight (four) values at a time
+        uint32_t val[2][4];
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
-          for (int j = 0; j < 2; j++)
-            word[2 * i + j] = (d & 1) ? highs(val[i][2 * j][d >> 1], val[i][2 * j + 1][d >> 1])
-                                      : lows(val[i][2 * j][d >> 1], val[i][2 * j + 1][d >> 1]);
+          for (int j = 0; j < 4; j++) {
+            // for 64 values lanes c and c + 8 take the halves of a word
+            const uint32_t codes = D == 64 ? now.v[i][b][j] >> (c & 8 ? 16 : 0) : now.v[i][b][j];
+            val[i][j] = bf16_pair_of(codes, scale_of(now.vs[i][b], j), x);
+          }
+        const u32x4 even = {lows(val[0][0], val[0][1]), lows(val[0][2], val[0][3]), lows(val[1][0], val[1][1]), lows(val[1][2], val[1][3])};
+        const u32x4 odd = {highs(val[0][0], val[0][1]), highs(val[0][2], val[0][3]), highs(val[1][0], val[1][1]), highs(val[1][2], val[1][3])};
 #pragma unroll
-        for (int n = 0; n < NB; n++)
-          o[n][8 * b + d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, word), p[n], o[n][8 * b + d], 0, 0, 0);
+        for (int n = 0; n < NB; n++) {
+          v4f &o0 = o[n][8 * b + 2 * x], &o1 = o[n][8 * b + 2 * x + 1];
+          o0 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), p[n], o0, 0, 0, 0);
+          o1 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), p[n], o1, 0, 0, 0);
+        }
       }
     }
-    now = next;
+  };
+
+  for (int key = first; key < last; key += DEPTH * stride) {
+#pragma unroll
+    for (int u = 0; u < DEPTH; u++) {
+      const int at = key + u * stride, to = at + DEPTH * stride;
+      if (at < last) step(ring[u], at);
+      ring[u].load(a, pages, head, to, to < last);
+      pages.find(a, t, to + stride, end);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   }
 
-  // the waves' sums meet
+  // the waves' sums meet: lane (c, g) of wave j adds up registers j of row c's blocks of
+  // O^T, four at a time, which are neighbouring dimensions
 #pragma unroll
   for (int n = 0; n < NB; n++) {
     sum[n] = group_sum(sum[n]);
+    if (n) __syncthreads();
     if (g == 0) {
-      stats[w][n][c][0] = top[n];
-      stats[w][n][c][1] = sum[n];
+      stats[w][c][0] = top[n];
+      stats[w][c][1] = sum[n];
     }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < NB; n++) {
-    float all = -INFINITY, total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < WAVES; i++) all = fmaxf(all, stats[i][n][c][0]);
-    const float base = all > -INFINITY ? all : 0.0f;
-#pragma unroll
-    for (int i = 0; i < WAVES; i++) total += stats[i][n][c][1] * __builtin_amdgcn_exp2f(stats[i][n][c][0] - base);
-    const float mine = __builtin_amdgcn_exp2f(top[n] - base);
     const bool valid = 16 * n + c < rows;
     const int64_t row = token[n] * a.heads + q_head[n];
-    const float factor = a.sums ? 1.0f : (total > 0.0f || total != total ? 1.0f / total : 0.0f);
-    if (valid && w == 0 && g == 0) {
-      if (a.sums) {
-        float* ml = a.sums + a.parts * all_rows * D + (part * all_rows + row) * 2;
-        ml[0] = all;
-        ml[1] = total;
-      } else if (a.lse) {
-        a.lse[row] = total > 0.0f || total != total ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
-      }
-    }
-    if (a.sums && s0 >= s1) continue;   // the whole workgroup: nothing but the statistics
-    // four blocks of O^T at a time: lane (c, g) of wave j then adds up registers j of
-    // row c's blocks, four neighbouring dimensions
+    float part_of[WAVES], factor = 1.0f;
 #pragma unroll
-    for (int q = 0; q < DT / 4; q++) {
+    for (int d0 = 0; d0 < DT; d0 += CH) {
+      if (d0) __syncthreads();
+#pragma unroll
+      for (int d = 0; d < CH; d++) *reinterpret_cast<v4f*>(meet[w][d][lane]) = o[n][d0 + d];
       __syncthreads();
+      if (d0 == 0) {
+        float all = -INFINITY, total = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) *reinterpret_cast<v4f*>(meet[w][i][lane]) = o[n][4 * q + i] * mine;
-      __syncthreads();
-      float r[4];
+        for (int u = 0; u < WAVES; u++) all = fmaxf(all, stats[u][c][0]);
+        const float base = all > -INFINITY ? all : 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        r[i] = 0.0f;
-#pragma unroll
-        for (int u = 0; u < WAVES; u++) r[i] += meet[u][i][lane][w];
-        r[i] *= factor;
+        for (int u = 0; u < WAVES; u++) {
+          part_of[u] = __builtin_amdgcn_exp2f(stats[u][c][0] - base);
+          total += stats[u][c][1] * part_of[u];
+        }
+        const bool some = total > 0.0f || total != total;
+        if (!a.sums) factor = some ? 1.0f / total : 0.0f;
+        if (valid && w == 0 && g == 0) {
+          if (a.sums) {
+            float* ml = a.sums + a.parts * all_rows * D + (part * all_rows + row) * 2;
+            ml[0] = all;
+            ml[1] = total;
+          } else if (a.lse) {
+            a.lse[row] = some ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+          }
+        }
       }
-      const int m = 4 * g + w;   // row of the blocks: (eight values, or half of them)
-      const int d0 = D == 64 ? 8 * (m & 7) + 4 * (m >> 3) : 128 * (q >> 1) + 8 * m + 4 * (q & 1);
-      if (valid) {
-        if (a.sums) {
-          *reinterpret_cast<v4f*>(a.sums + (part * all_rows + row) * D + d0) = v4f{r[0], r[1], r[2], r[3]};
-        } else {
-          *reinterpret_cast<u32x2*>(a.out + row * D + d0) = u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
+      if (valid && !(a.sums && s0 >= s1)) {   // an empty part has nothing but its statistics
+#pragma unroll
+        for (int q = 0; q < CH / 4; q++) {
+          float r[4];
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            r[i] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < WAVES; u++) r[i] += meet[u][4 * q + i][lane][w] * part_of[u];
+            r[i] *= factor;
+          }
+          const int m = 4 * g + w;   // row of the blocks: (eight values, or half of them)
+          const int to = D == 64 ? 8 * (m & 7) + 4 * (m >> 3) : 16 * d0 + 8 * m + 4 * q;
+          if (a.sums) *reinterpret_cast<v4f*>(a.sums + (part * all_rows + row) * D + to) = v4f{r[0], r[1], r[2], r[3]};
+          else *reinterpret_cast<u32x2*>(a.out + row * D + to) = u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
         }
       }
     }
@@ -354,15 +415,28 @@ int64_t rows_of(const KvAttention& a) {
   return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
 }
 
-// Parts that the keys of a tile are cut into.
+// Parts that the keys of a tile are cut into: as many as give every compute unit a
+// workgroup (two for the kernel for many queries), of at least 512 keys.  A second
+// launch joins them, 3 to 4 us, in which a workgroup goes through 1000 keys: one token of
+// a sequence of 131071 keys, 8 heads: 34.5 us with 32 parts, 38.9 with 64, 48 with 16; 64
+// sequences: 69 us with 1 part, 70 with 2, 72 with 4.  Where there are tiles enough, parts
+// bound what one very long sequence among them takes: 16384 keys are 70 us.
+constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;
 int64_t parts_of(const KvAttention& a) {
-  const int64_t tm = rows_of(a), blocks = kv_tiles(a, tm) * a.cache.heads;
+  const int64_t tm = rows_of(a);
+  int64_t tiles = kv_tiles(a, tm);
+  if (a.offsets && a.max_queries < 65536) {   // as many as runs of max_queries have, if that is less
+    const int64_t likely = a.sequences * ((a.max_queries * group_of(a) + tm - 1) / tm);
+    tiles = tiles < likely ? tiles : likely;
+  }
+  const int64_t blocks = tiles * a.cache.heads;
   int64_t keys = a.table_width * a.cache.page_size;
   if (a.window > 0 && a.window + a.max_queries < keys) keys = a.window + a.max_queries;
-  int64_t parts = (tm == 128 ? 512 : 1024) / (blocks > 0 ? blocks : 1);
-  const int64_t most = keys / (tm == 128 ? 512 : 256);
+  const int64_t fill = (tm == 128 ? 512 : 256) / (blocks > 0 ? blocks : 1), bound = (keys + MOST_KEYS - 1) / MOST_KEYS;
+  int64_t parts = fill > bound ? fill : bound;
+  const int64_t most = keys / LEAST_KEYS;
   parts = parts < most ? parts : most;
-  return parts < 1 ? 1 : parts > 64 ? 64 : parts;
+  return parts < 1 ? 1 : parts > MOST_PARTS ? MOST_PARTS : parts;
 }
 
 template <int D>
@@ -374,8 +448,9 @@ hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
   if (tm == 128) {
     e = launch_kv_attention_tile(a, parts, stream);
   } else {
-    if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
-    else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);
+    constexpr int DEPTH = 2;
+    if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1, DEPTH>), grid, dim3(64 * WAVES), 0, stream, g);
+    else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2, 2>), grid, dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
   }
   if (e == hipSuccess && parts > 1) {
@@ -411,6 +486,7 @@ kv::Args kv_args(const KvAttention& a, int64_t parts) {
   g.keys_most = (int32_t)(a.table_width * a.cache.page_size);
   g.window = a.window > 0x7FFFFFFF ? 0 : (int32_t)a.window;
   g.parts = (int32_t)parts;
+  g.least = (int32_t)(LEAST_KEYS / 32);
   g.scale2 = a.scale * kLog2e;
   return g;
 }

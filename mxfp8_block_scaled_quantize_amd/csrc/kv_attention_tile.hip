@@ -137,7 +137,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
   seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
   const int begin = first_lo & ~(KEYS - 1), end = last_hi;
   const int steps = (end - begin + KEYS - 1) / KEYS;
-  const int each = (steps + a.parts - 1) / a.parts;
+  int each = (steps + a.parts - 1) / a.parts;
+  each = each < a.least / 2 ? a.least / 2 : each;
   const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
 
   // this lane's row, and the keys of the wave's rows
