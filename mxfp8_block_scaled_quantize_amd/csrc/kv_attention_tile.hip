@@ -25,18 +25,31 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 
-// The step's four runs of 16 keys: where their records are (null: no page, or no key).
-typedef uint64_t u64x4 __attribute__((ext_vector_type(4)));
+// The step's four runs of 16 keys: their page numbers, and which of them are pages.  No
+// branch here and in the loads (a number that is no page, a key behind the end are read
+// as ones that are there, and masked): the compiler can then wait for one step's loads
+// among the next one's.
 struct Runs {
-  u64x4 r;   // a vector, so that one chosen by a lane is selected in registers
-  __device__ __forceinline__ void find(const Args& a, const Tile& t, int head, int key, int end) {
+  int p[4];
+  uint32_t there;   // a bit for each
+  __device__ __forceinline__ void find(const Args& a, const Tile& t, int key, int end) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) r[i] = key + 16 * i < end ? reinterpret_cast<uint64_t>(record_of(a, t, head, key + 16 * i)) : 0;
+    for (int i = 0; i < 4; i++) {
+      const int at = key + 16 * i < end ? key + 16 * i : end - 1;
+      p[i] = a.table[t.sequence * a.ld_table + (at >> a.page_shift)];
+    }
   }
-  __device__ __forceinline__ bool all() const { return r[0] && r[1] && r[2] && r[3]; }
-  __device__ __forceinline__ const uint8_t* of(int run) const {
-    const uint64_t x = run == 0 ? r[0] : run == 1 ? r[1] : run == 2 ? r[2] : r[3];
-    return reinterpret_cast<const uint8_t*>(x);
+  __device__ __forceinline__ void check(const Args& a) {   // once the numbers are wanted
+    there = 0;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      const bool is = (unsigned)p[i] < (unsigned)a.pages;
+      there |= is ? 1u << i : 0u;
+      p[i] = is ? p[i] : 0;
+    }
+  }
+  __device__ __forceinline__ const uint8_t* record(const Args& a, int head, int i) const {
+    return a.cache + ((int64_t)p[i] * a.kv_heads + head) * a.record;
   }
 };
 
@@ -46,13 +59,13 @@ struct KeyPart {
   static constexpr int KS = D / 64;   // MFMA steps along a key
   u32x4 k[2][KS];
   uint32_t s[2][(KS + 1) / 2];
-  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int key) {
+  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key) {
     const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
     const int page_size = 1 << a.page_shift;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const uint8_t* r = c < 16 ? runs.of(2 * i) : runs.of(2 * i + 1);
-      if (!r) r = a.cache;   // any record: what comes is not used
+      const uint8_t *r0 = runs.record(a, head, 2 * i), *r1 = runs.record(a, head, 2 * i + 1);
+      const uint8_t* r = c < 16 ? r0 : r1;
       const int at = (key + 32 * i + c) & (page_size - 1);
 #pragma unroll
       for (int f = 0; f < KS; f++) k[i][f] = *reinterpret_cast<const u32x4*>(r + at * (D / 2) + 16 * (2 * f + h));
@@ -72,14 +85,14 @@ struct ValuePart {
   static constexpr int UNITS = D == 256 ? 2 : 1;
   u32x4 v[UNITS];
   uint32_t s[UNITS];
-  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int key) {
+  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key) {
     const int page_size = 1 << a.page_shift;
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
-      const int x = threadIdx.x + 256 * u, group = x / (D / 8), d = x % (D / 8), run = group >> 2;
-      if (D == 64 && x >= 128) break;   // whole waves
-      const uint8_t* r = runs.of(D == 64 ? run : __builtin_amdgcn_readfirstlane(run));
-      if (!r) r = a.cache;
+      const int x = (threadIdx.x + 256 * u) % (64 * (D / 8) / 4), group = x / (D / 8), d = x % (D / 8), run = group >> 2;
+      const uint8_t *r0 = runs.record(a, head, 0), *r1 = runs.record(a, head, 1), *r2 = runs.record(a, head, 2),
+                    *r3 = runs.record(a, head, 3);
+      const uint8_t *r01 = run & 1 ? r1 : r0, *r23 = run & 1 ? r3 : r2, *r = run & 2 ? r23 : r01;
       const int at = (key + 16 * run) & (page_size - 1);
       v[u] = *reinterpret_cast<const u32x4*>(r + page_size * (D / 2) + ((at >> 2) + (group & 3)) * (2 * D) + 16 * d);
       s[u] = *reinterpret_cast<const uint32_t*>(r + page_size * D + page_size * (D / 32) + (d >> 2) * page_size + at + 4 * (group & 3));
@@ -89,14 +102,13 @@ struct ValuePart {
   __device__ __forceinline__ void store(const Runs& runs, int key, int end, lds_u8* to) {
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
-      const int x = threadIdx.x + 256 * u, group = x / (D / 8), d = x % (D / 8);
-      if (D == 64 && x >= 128) break;
+      // with 64 values both halves of the workgroup have the same units
+      const int x = (threadIdx.x + 256 * u) % (64 * (D / 8) / 4), group = x / (D / 8), d = x % (D / 8);
       const int run = group >> 2, quad = group & 3;
-      if (key + KEYS > end || !runs.all()) {
-        const bool there = runs.of(run) != nullptr;
+      if (key + KEYS > end || runs.there != 0xF) {
 #pragma unroll
         for (int j = 0; j < 4; j++)
-          if (!there || key + 4 * group + j >= end) {
+          if (!(runs.there >> run & 1) || key + 4 * group + j >= end) {
             v[u][j] = 0;
             s[u] &= ~(0xFFu << (8 * j));
           }
@@ -197,26 +209,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
   KeyPart<D> keys;
   ValuePart<D> vals;
   if (s0 < s1) {
-    runs.find(a, t, head, begin + KEYS * s0, end);
-    keys.load(a, runs, begin + KEYS * s0);
-    vals.load(a, runs, begin + KEYS * s0);
-    ahead.find(a, t, head, begin + KEYS * (s0 + 1), end);
+    runs.find(a, t, begin + KEYS * s0, end);
+    ahead.find(a, t, begin + KEYS * (s0 + 1), end);
+    runs.check(a);
+    vals.load(a, runs, head, begin + KEYS * s0);
+    keys.load(a, runs, head, begin + KEYS * s0);
     vals.store(runs, begin + KEYS * s0, end, lds + (s0 & 1) * D * 128);
   }
   __syncthreads();
   for (int s = s0; s < s1; s++) {
     const int key = begin + KEYS * s;
-    const bool more = s + 1 < s1;
-    if (more) vals.load(a, ahead, key + KEYS);
+    Runs later;
+    ahead.check(a);
+    later.find(a, t, key + 2 * KEYS, end);
+    vals.load(a, ahead, head, key + KEYS);
     const bool work = key < wave_hi && key + KEYS > wave_lo;   // wave-uniform
-    auto stage = [&]() {
-      if (more) vals.store(ahead, key + KEYS, end, lds + ((s + 1) & 1) * D * 128);
-    };
-    if (!work) {
-      if (more) keys.load(a, ahead, key + KEYS);
-      stage();
-    } else {
-      v16f y[2];
+    v16f y[2];
+    u32x4 p[4];   // weights of 16 keys each
+    if (work) {
 #pragma unroll
       for (int i = 0; i < 2; i++) {
 #pragma unroll
@@ -235,9 +245,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
           }
         }
       }
-      if (more) keys.load(a, ahead, key + KEYS);   // in the registers that the products are done with
+    }
+    keys.load(a, ahead, head, key + KEYS);   // in the registers that the products are done with
+    if (work) {
       float mx = -INFINITY;
-      if (key >= all_lo && key + KEYS <= all_hi && runs.all()) {
+      if (key >= all_lo && key + KEYS <= all_hi && runs.there == 0xF) {
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -248,7 +260,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
 #pragma unroll
           for (int j = 0; j < 16; j++) {
             const int at = key + 32 * i + 8 * (j >> 2) + 4 * h + (j & 3);
-            if (!(at >= lo && at < hi && runs.of(2 * i + (j >> 3)))) y[i][j] = -INFINITY;
+            if (!(at >= lo && at < hi && (runs.there >> (2 * i + (j >> 3)) & 1))) y[i][j] = -INFINITY;
             mx = fmaxf(mx, y[i][j]);
           }
       }
@@ -263,7 +275,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
         for (int d = 0; d < D / 32; d++) o[d] *= shrink;
       }
       const float base = top > -INFINITY ? top : 0.0f;
-      u32x4 p[4];   // of 16 keys each
 #pragma unroll
       for (int i = 0; i < 2; i++)
 #pragma unroll
@@ -273,7 +284,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
           sum += e0 + e1;
           p[2 * i + (j >> 2)][j & 3] = bf16_pair(e0, e1);
         }
-      stage();
+    }
+    vals.store(ahead, key + KEYS, end, lds + ((s + 1) & 1) * D * 128);
+    if (work) {
       const lds_u8* v = lds + (s & 1) * D * 128 + c * 128;
 #pragma unroll
       for (int f = 0; f < 4; f++) {
@@ -285,7 +298,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       }
     }
     runs = ahead;
-    if (more) ahead.find(a, t, head, key + 2 * KEYS, end);
+    ahead = later;
     __syncthreads();
   }
 
