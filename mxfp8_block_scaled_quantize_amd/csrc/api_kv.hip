@@ -49,7 +49,8 @@ mxfp8_status check_cache(const void* cache, int64_t pages, int32_t page_size, in
   const mxfp8_status st = check_pages(pages, page_size);
   if (st != MXFP8_OK) return st;
   if (kv_heads < 1 || (head_dim != 64 && head_dim != 128 && head_dim != 256)) return MXFP8_ERR_SHAPE;
-  if (!product_ok(pages * kv_heads, (int64_t)page_size * (head_dim + head_dim / 16))) return MXFP8_ERR_LIMIT;
+  const int64_t record = (int64_t)page_size * (head_dim + head_dim / 16);
+  if (kv_heads > kMaxIndex / record || !product_ok(pages, kv_heads * record)) return MXFP8_ERR_LIMIT;
   if (!cache) return MXFP8_ERR_NULL;
   return aligned(cache, 16) ? MXFP8_OK : MXFP8_ERR_MISALIGNED;
 }

@@ -43,6 +43,7 @@ struct Args {
   int64_t q_token, q_head;
   const uint8_t* __restrict__ cache;
   int64_t record;
+  uint32_t page_stride;        // bytes of a page's records, below 2^31
   const int32_t* __restrict__ table;
   int64_t ld_table;
   const int32_t* __restrict__ lengths;
@@ -115,10 +116,9 @@ __device__ __forceinline__ void seen(const Args& a, const Tile& t, int x, int* l
   *lo = a.window > 0 && *hi > a.window ? *hi - a.window : 0;
 }
 
-// A page's record of a head, or null for a number that is no page.
-__device__ __forceinline__ const uint8_t* record_of(const Args& a, const Tile& t, int head, int key) {
-  const int page = a.table[t.sequence * a.ld_table + (key >> a.page_shift)];
-  return (unsigned)page < (unsigned)a.pages ? a.cache + ((int64_t)page * a.kv_heads + head) * a.record : nullptr;
+// A page's record of a head.
+__device__ __forceinline__ const uint8_t* record_of(const Args& a, int head, int page) {
+  return a.cache + head * a.record + (uint64_t)(uint32_t)page * a.page_stride;
 }
 
 // Eight BF16 query values as E4M3 parts (two words each) on the scale 2^(e - 127).

@@ -70,7 +70,7 @@ struct Keys {
       there[i] = (unsigned)pages.p[i] < (unsigned)a.pages;
       const int page = there[i] ? pages.p[i] : 0;
       const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<uint8_t*>(a.cache) + ((int64_t)page * a.kv_heads + head) * a.record, 0, there[i] && wanted ? (int)a.record : 0,
+          const_cast<uint8_t*>(record_of(a, head, page)), 0, there[i] && wanted ? (int)a.record : 0,
           0x00020000);
       const int o = (key + 16 * i) & (int)(page_size - 1);
       const int k0 = o * (D / 2), v0 = page_size * (D / 2) + (o >> 2) * (2 * D);
@@ -469,6 +469,7 @@ kv::Args kv_args(const KvAttention& a, int64_t parts) {
   g.q_head = a.q_head;
   g.cache = a.cache.data;
   g.record = a.cache.record();
+  g.page_stride = (uint32_t)(a.cache.record() * a.cache.heads);
   g.table = a.table;
   g.ld_table = a.ld_table;
   g.lengths = a.lengths;

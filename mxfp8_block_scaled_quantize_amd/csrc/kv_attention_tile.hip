@@ -21,6 +21,7 @@ using namespace kv;
 namespace {
 
 constexpr int KEYS = 64;
+constexpr int ROW = 2 * KEYS + 16;   // bytes of a value's LDS row: 16 spare ones set neighbouring rows apart
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
@@ -48,9 +49,6 @@ struct Runs {
       p[i] = is ? p[i] : 0;
     }
   }
-  __device__ __forceinline__ const uint8_t* record(const Args& a, int head, int i) const {
-    return a.cache + ((int64_t)p[i] * a.kv_heads + head) * a.record;
-  }
 };
 
 // What a lane loads of a step's keys: 32 codes (16 bytes) and a scale for every MFMA.
@@ -60,69 +58,80 @@ struct KeyPart {
   u32x4 k[2][KS];
   uint32_t s[2][(KS + 1) / 2];
   __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key) {
-    const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
     const int page_size = 1 << a.page_shift;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      const uint8_t *r0 = runs.record(a, head, 2 * i), *r1 = runs.record(a, head, 2 * i + 1);
-      const uint8_t* r = c < 16 ? r0 : r1;
-      const int at = (key + 32 * i + c) & (page_size - 1);
+      // the runs' first keys; a lane's own is at the same place behind either
+      const uint8_t* r[2];
 #pragma unroll
-      for (int f = 0; f < KS; f++) k[i][f] = *reinterpret_cast<const u32x4*>(r + at * (D / 2) + 16 * (2 * f + h));
-      const uint8_t* b = r + page_size * D + at * (D / 32);
-      if (D == 64) s[i][0] = *reinterpret_cast<const uint16_t*>(b);
+      for (int j = 0; j < 2; j++) r[j] = record_of(a, head, runs.p[2 * i + j]) + ((key + 32 * i + 16 * j) & (page_size - 1)) * (D / 2);
+      const uint8_t* k0 = (c & 16 ? r[1] : r[0]) + ((c & 15) * (D / 2) + 16 * h);
+#pragma unroll
+      for (int j = 0; j < 2; j++) {
+        const int at = (key + 32 * i + 16 * j) & (page_size - 1);
+        r[j] += page_size * D + at * (D / 32) - at * (D / 2);
+      }
+      const uint8_t* s0 = (c & 16 ? r[1] : r[0]) + (c & 15) * (D / 32);
+#pragma unroll
+      for (int f = 0; f < KS; f++) k[i][f] = *reinterpret_cast<const u32x4*>(k0 + 32 * f);
+      if (D == 64) s[i][0] = *reinterpret_cast<const uint16_t*>(s0);
       else {
 #pragma unroll
-        for (int f = 0; f < KS / 2; f++) s[i][f] = reinterpret_cast<const uint32_t*>(b)[f];
+        for (int f = 0; f < KS / 2; f++) s[i][f] = reinterpret_cast<const uint32_t*>(s0)[f];
       }
     }
   }
 };
 
-// What a lane loads of a step's values: units of 4 keys x 8 values.
+// What a lane loads of a step's values: units of 4 keys x 8 values of the wave's run of 16
+// keys (with 64 values both halves of the wave the same ones).
 template <int D>
 struct ValuePart {
   static constexpr int UNITS = D == 256 ? 2 : 1;
   u32x4 v[UNITS];
   uint32_t s[UNITS];
-  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key) {
-    const int page_size = 1 << a.page_shift;
+  static __device__ __forceinline__ uint32_t quad(int u) { return ((threadIdx.x & (D == 64 ? 31 : 63)) + 64 * u) / (D / 8); }
+  static __device__ __forceinline__ uint32_t eight(int u) { return ((threadIdx.x & 63) + 64 * u) % (D / 8); }
+  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key, int w) {
+    const uint32_t page_size = 1u << a.page_shift;
+    const int page = w == 0 ? runs.p[0] : w == 1 ? runs.p[1] : w == 2 ? runs.p[2] : runs.p[3];
+    const uint32_t at = (uint32_t)(key + 16 * w) & (page_size - 1);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(record_of(a, head, page)), 0, (int)a.record, 0x00020000);
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
-      const int x = (threadIdx.x + 256 * u) % (64 * (D / 8) / 4), group = x / (D / 8), d = x % (D / 8), run = group >> 2;
-      const uint8_t *r0 = runs.record(a, head, 0), *r1 = runs.record(a, head, 1), *r2 = runs.record(a, head, 2),
-                    *r3 = runs.record(a, head, 3);
-      const uint8_t *r01 = run & 1 ? r1 : r0, *r23 = run & 1 ? r3 : r2, *r = run & 2 ? r23 : r01;
-      const int at = (key + 16 * run) & (page_size - 1);
-      v[u] = *reinterpret_cast<const u32x4*>(r + page_size * (D / 2) + ((at >> 2) + (group & 3)) * (2 * D) + 16 * d);
-      s[u] = *reinterpret_cast<const uint32_t*>(r + page_size * D + page_size * (D / 32) + (d >> 2) * page_size + at + 4 * (group & 3));
+      v[u] = __builtin_amdgcn_raw_buffer_load_b128(r, quad(u) * (2 * D) + 16 * eight(u), page_size * (D / 2) + (at >> 2) * (2 * D), 0);
+      s[u] = __builtin_amdgcn_raw_buffer_load_b32(r, (eight(u) >> 2) * page_size + 4 * quad(u), page_size * (D + D / 32) + at, 0);
     }
   }
-  // As BF16 to the LDS rows.  Of places that no query sees, zeros.
-  __device__ __forceinline__ void store(const Runs& runs, int key, int end, lds_u8* to) {
+  // Of places that no query sees, zeros.
+  __device__ __forceinline__ void mask(const Runs& runs, int key, int end, int w) {
+    if (key + KEYS <= end && runs.there == 0xF) return;
+#pragma unroll
+    for (int u = 0; u < UNITS; u++)
+#pragma unroll
+      for (int j = 0; j < 4; j++)
+        if (!(runs.there >> w & 1) || key + 16 * w + 4 * (int)quad(u) + j >= end) {
+          v[u][j] = 0;
+          s[u] &= ~(0xFFu << (8 * j));
+        }
+  }
+  // As BF16 to the LDS rows.
+  __device__ __forceinline__ void store(lds_u8* to, int w) const {
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
-      // with 64 values both halves of the workgroup have the same units
-      const int x = (threadIdx.x + 256 * u) % (64 * (D / 8) / 4), group = x / (D / 8), d = x % (D / 8);
-      const int run = group >> 2, quad = group & 3;
-      if (key + KEYS > end || runs.there != 0xF) {
+      uint32_t x[4][4];
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-          if (!(runs.there >> run & 1) || key + 4 * group + j >= end) {
-            v[u][j] = 0;
-            s[u] &= ~(0xFFu << (8 * j));
-          }
-      }
-      uint32_t w[4][4];
-#pragma unroll
-      for (int j = 0; j < 4; j++) bf16_of(v[u][j], scale_of(s[u], j), w[j]);
-      const int chunk = 2 * run + (quad & 1);
+      for (int j = 0; j < 4; j++) bf16_of(v[u][j], scale_of(s[u], j), x[j]);
+      const uint32_t chunk = 2 * w + (quad(u) & 1), d = eight(u);
+      lds_u8* const row = to + 8 * d * ROW + ((chunk ^ d) & 7) * 16 + (quad(u) >> 1) * 8;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         u32x2 word;
-        word.x = (i & 1) ? highs(w[0][i >> 1], w[1][i >> 1]) : lows(w[0][i >> 1], w[1][i >> 1]);
-        word.y = (i & 1) ? highs(w[2][i >> 1], w[3][i >> 1]) : lows(w[2][i >> 1], w[3][i >> 1]);
-        *reinterpret_cast<lds_u32x2*>(to + (8 * d + i) * 128 + ((chunk ^ i ^ d) & 7) * 16 + (quad >> 1) * 8) = word;
+        word.x = (i & 1) ? highs(x[0][i >> 1], x[1][i >> 1]) : lows(x[0][i >> 1], x[1][i >> 1]);
+        word.y = (i & 1) ? highs(x[2][i >> 1], x[3][i >> 1]) : lows(x[2][i >> 1], x[3][i >> 1]);
+        *reinterpret_cast<lds_u32x2*>(row + i * ROW) = word;
       }
     }
   }
@@ -131,7 +140,7 @@ struct ValuePart {
 template <int D>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
   constexpr int KS = KeyPart<D>::KS;
-  __shared__ __attribute__((aligned(16))) uint8_t values[2][D * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t values[2][D * ROW];
   lds_u8* const lds = (lds_u8*)&values[0][0];
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -212,9 +221,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
     runs.find(a, t, begin + KEYS * s0, end);
     ahead.find(a, t, begin + KEYS * (s0 + 1), end);
     runs.check(a);
-    vals.load(a, runs, head, begin + KEYS * s0);
+    vals.load(a, runs, head, begin + KEYS * s0, w);
     keys.load(a, runs, head, begin + KEYS * s0);
-    vals.store(runs, begin + KEYS * s0, end, lds + (s0 & 1) * D * 128);
+    vals.mask(runs, begin + KEYS * s0, end, w);
+    vals.store(lds + (s0 & 1) * D * ROW, w);
   }
   __syncthreads();
   for (int s = s0; s < s1; s++) {
@@ -222,10 +232,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
     Runs later;
     ahead.check(a);
     later.find(a, t, key + 2 * KEYS, end);
-    vals.load(a, ahead, head, key + KEYS);
+    vals.load(a, ahead, head, key + KEYS, w);
     const bool work = key < wave_hi && key + KEYS > wave_lo;   // wave-uniform
     v16f y[2];
-    u32x4 p[4];   // weights of 16 keys each
     if (work) {
 #pragma unroll
       for (int i = 0; i < 2; i++) {
@@ -264,8 +273,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
             mx = fmaxf(mx, y[i][j]);
           }
       }
-      mx *= a.scale2;
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+      mx = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale2;
       if (__any(mx > top + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
         const float higher = fmaxf(mx, top);
         const float shrink = higher > -INFINITY ? __builtin_amdgcn_exp2f(top - higher) : 1.0f;
@@ -274,9 +283,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
 #pragma unroll
         for (int d = 0; d < D / 32; d++) o[d] *= shrink;
       }
+    }
+    vals.mask(ahead, key + KEYS, end, w);
+    lds_u8* const to = lds + ((s + 1) & 1) * D * ROW;
+    if (!work) {
+      vals.store(to, w);
+    } else {
       const float base = top > -INFINITY ? top : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 2; i++)
+      const lds_u8* v = lds + (s & 1) * D * ROW + c * ROW;
+      u32x4 p[4];   // weights of 16 keys each
+      auto weights = [&](int i) {
 #pragma unroll
         for (int j = 0; j < 8; j++) {
           const float e0 = __builtin_amdgcn_exp2f(fmaf(y[i][2 * j], a.scale2, -base));
@@ -284,18 +300,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
           sum += e0 + e1;
           p[2 * i + (j >> 2)][j & 3] = bf16_pair(e0, e1);
         }
-    }
-    vals.store(ahead, key + KEYS, end, lds + ((s + 1) & 1) * D * 128);
-    if (work) {
-      const lds_u8* v = lds + (s & 1) * D * 128 + c * 128;
-#pragma unroll
-      for (int f = 0; f < 4; f++) {
+      };
+      auto product = [&](int f) {
 #pragma unroll
         for (int d = 0; d < D / 32; d++) {
-          const u32x4 vw = *reinterpret_cast<const lds_u32x4*>(v + d * 4096 + (((2 * f + h) ^ c ^ (4 * d + (c >> 3))) & 7) * 16);
+          const u32x4 vw = *reinterpret_cast<const lds_u32x4*>(v + d * (32 * ROW) + (((2 * f + h) ^ (4 * d) ^ (c >> 3)) & 7) * 16);
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vw), __builtin_bit_cast(bf16x8, p[f]), o[d], 0, 0, 0);
         }
-      }
+      };
+      weights(0);
+      product(0);
+      product(1);
+      weights(1);
+      vals.store(to, w);
+      product(2);
+      product(3);
+
     }
     runs = ahead;
     ahead = later;
