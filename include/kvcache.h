@@ -43,7 +43,8 @@ extern "C" {
  * A request whose pages are more than table_width, whose rows end behind
  * `tokens`, or whose pages the stack does not cover any more (with those of the
  * requests before it, also the ones that got nothing for that reason) gets
- * nothing: lengths_out[b] = lengths[b], and its rows have slot -1.  A page
+ * nothing: lengths_out[b] = lengths[b], and its rows have slot -1 (and positions
+ * that end at 2^31 - 1).  A page
  * number outside [0, pages) gives slot -1.
  *
  * table [requests][ld_table] int32, ld_table >= table_width >= 0; lengths,

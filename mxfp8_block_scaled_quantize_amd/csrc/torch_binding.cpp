@@ -14,6 +14,7 @@
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/hip/HIPGraphsC10Utils.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
@@ -566,17 +567,19 @@ CacheShape cache_shape(const Tensor& c, int64_t head_dim) {
   if (c.size(1) > INT32_MAX) refuse("too many heads");
   return {c.size(0), c.size(1), (int32_t)page, (int32_t)head_dim};
 }
+// Whether the values of a head follow each other (of one value, or none, the stride says nothing).
+bool unit_heads(const Tensor& t) { return t.size(2) <= 1 || t.numel() == 0 || t.stride(2) == 1; }
 // A BF16 [tokens, heads, head_dim] tensor with unit stride along the head.
 const Tensor& rows3(PyObject* o, const char* name) {
   const std::string text = std::string(name) + " must be a BF16 [tokens, heads, head_dim] tensor with unit stride along the head";
   if (!THPVariable_Check(o)) refuse(text, PyExc_TypeError);
   const Tensor& t = THPVariable_Unpack(o);
-  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || (t.size(2) > 1 && t.stride(2) != 1)) refuse(text);
+  if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || !unit_heads(t)) refuse(text);
   on_gpu(t, name);
   return t;
 }
 // Strides of a dimension of size 1 say nothing.
-int64_t stride_of(const Tensor& t, int d) { return t.size(d) > 1 ? t.stride(d) : 0; }
+int64_t stride_of(const Tensor& t, int d) { return t.size(d) > 1 && t.numel() ? t.stride(d) : 0; }
 void no_gradient(const Tensor& t, const char* name) {
   if (t.requires_grad() && at::GradMode::is_enabled())
     refuse(std::string(name) + " requires a gradient, which this operator does not have: call it with gradients disabled");
@@ -587,7 +590,7 @@ const Tensor& block_table(PyObject* o, int64_t rows, c10::Device dev) {
   const Tensor& t = tensor(o, "table");
   if (t.dim() != 2) refuse("table must be an int32 [requests, pages] tensor");
   on_gpu(t, "table");
-  if (t.scalar_type() != at::kInt || !unit_columns(t)) refuse("table must be int32 with unit stride along a request's pages");
+  if (t.scalar_type() != at::kInt || !(t.numel() == 0 || unit_columns(t))) refuse("table must be int32 with unit stride along a request's pages");
   if (t.size(0) != rows) refuse("table has " + std::to_string(t.size(0)) + " requests, lengths " + std::to_string(rows));
   if (t.device() != dev) refuse("table is on " + t.device().str() + ", expected " + dev.str());
   return t;
@@ -806,12 +809,30 @@ std::pair<Tensor, Tensor> rotate_both(const Tensor& q, const Tensor& k, const Tu
   return {qo, ko};
 }
 
+// A leaf's accumulator keeps the stream on which it was made for as long as some graph
+// holds it.  If that is not the stream of a backward pass that is being captured, the
+// engine makes the two wait for each other once the pass is through, which a capture
+// does not allow: the process ends.  So the pass is refused before.
+int64_t leaf_stream(const Variable& v) {
+  const auto node = torch::autograd::impl::try_get_grad_accumulator(v);
+  const auto stream = node ? node->stream() : std::nullopt;
+  return stream ? (int64_t)stream->id() : -1;
+}
+void refuse_capture(int64_t leaf, c10::Device dev) {
+  if (leaf < 0 || c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+  if (leaf != (int64_t)c10::hip::getCurrentHIPStream(dev.index()).unwrap().id())
+    throw std::runtime_error("rotate: its gradient cannot be captured while a graph of q or k lives that was made on another "
+                             "stream: let go of that graph, or capture on its stream");
+}
+
 struct Rotate : torch::autograd::Function<Rotate> {
   static variable_list forward(AutogradContext* ctx, const Variable& q, const std::optional<Tensor>& k, const Tensor& positions,
                                const Tensor& turns, double magnitude, int64_t flags) {
     ctx->save_for_backward({positions, turns});
     ctx->saved_data["magnitude"] = magnitude;
     ctx->saved_data["flags"] = flags;
+    ctx->saved_data["q_stream"] = q.requires_grad() ? leaf_stream(q) : -1;
+    ctx->saved_data["k_stream"] = k && k->requires_grad() ? leaf_stream(*k) : -1;
     ctx->set_materialize_grads(false);
     auto [qo, ko] = rotate_both(q, k ? *k : Tensor(), {positions, turns, magnitude, (uint32_t)flags});
     if (!k) return {qo};
@@ -820,10 +841,11 @@ struct Rotate : torch::autograd::Function<Rotate> {
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const auto saved = ctx->get_saved_variables();
     variable_list out(6);
+    for (const char* name : {"q_stream", "k_stream"}) refuse_capture(ctx->saved_data[name].toInt(), saved[0].device());
     auto usable = [&](size_t i) {
       if (i >= grads.size() || !grads[i].defined() || !ctx->needs_input_grad(i)) return Tensor();
       at::AutoDispatchBelowADInplaceOrView below;
-      return grads[i].size(2) > 1 && grads[i].stride(2) != 1 ? grads[i].contiguous() : grads[i].detach();
+      return unit_heads(grads[i]) ? grads[i].detach() : grads[i].contiguous();
     };
     const Tensor dq = usable(0), dk = usable(1);
     if (dq.defined() || dk.defined()) {
@@ -844,12 +866,12 @@ PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!THPVariable_Check(a[0])) refuse(text, PyExc_TypeError);
     const Tensor& q = THPVariable_Unpack(a[0]);
     const Tensor* k = tensor_or_none(a[1], "k");
-    if (rotary_dtype(q) < 0 || q.dim() != 3 || (q.size(2) > 1 && q.stride(2) != 1)) refuse(text);
+    if (rotary_dtype(q) < 0 || q.dim() != 3 || !unit_heads(q)) refuse(text);
     on_gpu(q, "q");
     const c10::Device dev = q.device();
     if (k) {
       if (k->scalar_type() != q.scalar_type() || k->dim() != 3 || k->size(0) != q.size(0) || k->size(2) != q.size(2) ||
-          (k->size(2) > 1 && k->stride(2) != 1))
+          !unit_heads(*k))
         refuse("k must be [tokens, heads, head_dim] with q's type, tokens and head_dim and unit stride along the head");
       if (k->device() != dev) refuse("k is on " + k->device().str() + ", expected " + dev.str());
     }
