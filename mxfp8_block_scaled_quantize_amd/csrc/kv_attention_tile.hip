@@ -264,12 +264,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
 #pragma unroll
           for (int j = 0; j < 16; j++) mx = fmaxf(mx, y[i][j]);
       } else {
+        if (runs.there != 0xF) {
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int j = 0; j < 16; j++)
+              if (!(runs.there >> (2 * i + (j >> 3)) & 1)) y[i][j] = -INFINITY;
+        }
+        const uint32_t from = (uint32_t)(key + 4 * h - lo), span = (uint32_t)(hi - lo);
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
           for (int j = 0; j < 16; j++) {
-            const int at = key + 32 * i + 8 * (j >> 2) + 4 * h + (j & 3);
-            if (!(at >= lo && at < hi && (runs.there >> (2 * i + (j >> 3)) & 1))) y[i][j] = -INFINITY;
+            if (from + (32 * i + 8 * (j >> 2) + (j & 3)) >= span) y[i][j] = -INFINITY;
             mx = fmaxf(mx, y[i][j]);
           }
       }
