@@ -110,7 +110,8 @@ mxfp8_status kv_read(const uint8_t *cache, int64_t pages, int32_t page_size, int
  * max_queries  the longest run of queries as far as the caller knows it, >= 1:
  *          it decides which kernel runs, not what comes out.
  * scale    > 0, finite.   window >= 0 (0: none).
- * out      BF16 [tokens][heads][head_dim] dense, 16-byte aligned.
+ * out      BF16 [tokens][heads][head_dim] dense, 16-byte aligned; no output
+ *          overlaps an input.
  * lse      fp32 [tokens][heads] or NULL: log sum_j exp(scale <q, k_j>), -inf for
  *          a query that sees no key.
  * workspace  kv_attention_workspace_bytes(...) of the same sizes, 16-byte

@@ -71,5 +71,5 @@ class MXFP4Attention(torch.nn.Module):
         kvcache.append(cache, k, v, plan.slots)
         y = kvcache.attention(q, cache, table, plan.lengths, plan.offsets, scale=self.scale, window=self.window,
                               max_queries=max_queries)
-        a = mxfp4.quantize(y.view(x.shape[0], -1), packed=True)
+        a = mxfp4.quantize(y.view(x.shape[0], h * self.head_dim), packed=True)
         return mxfp4.gemm(a["q_row"], a["p_row"], self.out, self.out_scales)

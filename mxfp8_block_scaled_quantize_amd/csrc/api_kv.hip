@@ -70,7 +70,7 @@ mx::KvAttention attention_of(int64_t tokens, int32_t heads, int32_t kv_heads, in
   a.offsets = offsets;
   a.sequences = sequences;
   a.max_queries = !offsets ? 1 : max_queries < tokens ? max_queries : tokens > 1 ? tokens : 1;
-  a.window = window;
+  a.window = window > kMaxIndex ? 0 : window;   // no sequence is longer
   return a;
 }
 

@@ -18,7 +18,7 @@ using namespace kv;
 
 namespace {
 
-constexpr int WAVES = 4;
+constexpr int WAVES = 4, DEPTH = 2;   // DEPTH: steps on their way
 // Codes are read once: non-temporal loads (64 sequences of up to 8192 tokens: 70 us, 77 without).
 constexpr int NT = 2;
 
@@ -88,7 +88,7 @@ struct Keys {
   }
 };
 
-template <int D, int NB, int DEPTH>
+template <int D, int NB>
 __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 64 ? 3 : 2) void kv_attention_rows_kernel(Args a) {
   constexpr int TM = 16 * NB;
   constexpr int KB = Keys<D>::KB;
@@ -367,7 +367,14 @@ __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int64_t row = blockIdx.x, all_rows = (int64_t)a.tokens * a.heads;
   const int token = (int)(row / a.heads);
-  if (a.offsets && (token < a.offsets[0] || token >= a.offsets[a.sequences])) return;
+  if (a.offsets) {   // rows of no sequence; the offsets' running maximum is what counts
+    if (token < a.offsets[0]) return;
+    int end = a.offsets[a.sequences];
+    if (token >= end) {
+      for (int i = lane; i < a.sequences; i += 64) end = max(end, a.offsets[i]);
+      if (!__any(token < end)) return;   // the same for all waves
+    }
+  }
   const float* ml = a.sums + a.parts * all_rows * D + row * 2;
   float all = -INFINITY;
   for (int p = lane; p < a.parts; p += 64) all = fmaxf(all, ml[p * all_rows * 2]);
@@ -448,9 +455,8 @@ hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
   if (tm == 128) {
     e = launch_kv_attention_tile(a, parts, stream);
   } else {
-    constexpr int DEPTH = 2;
-    if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1, DEPTH>), grid, dim3(64 * WAVES), 0, stream, g);
-    else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2, 2>), grid, dim3(64 * WAVES), 0, stream, g);
+    if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
+    else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
   }
   if (e == hipSuccess && parts > 1) {
@@ -485,7 +491,7 @@ kv::Args kv_args(const KvAttention& a, int64_t parts) {
   g.pages = (int32_t)a.cache.pages;
   g.page_shift = a.cache.page_shift;
   g.keys_most = (int32_t)(a.table_width * a.cache.page_size);
-  g.window = a.window > 0x7FFFFFFF ? 0 : (int32_t)a.window;
+  g.window = (int32_t)a.window;
   g.parts = (int32_t)parts;
   g.least = (int32_t)(LEAST_KEYS / 32);
   g.scale2 = a.scale * kLog2e;
@@ -498,7 +504,9 @@ size_t kv_attention_workspace(const KvAttention& a) {
 }
 
 bool kv_attention_grid_fits(const KvAttention& a) {
-  return grid_fits(kv_tiles(a, rows_of(a)) * parts_of(a), a.cache.heads, 64 * WAVES) && grid_fits(a.tokens, a.heads, 64 * WAVES);
+  const int64_t parts = parts_of(a);
+  return grid_fits(kv_tiles(a, rows_of(a)) * parts, a.cache.heads, 64 * WAVES) &&
+         (parts == 1 || grid_fits(a.tokens, a.heads, 64 * WAVES));
 }
 
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream) {

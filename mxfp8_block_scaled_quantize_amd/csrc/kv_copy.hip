@@ -119,7 +119,7 @@ unsigned blocks_of(int64_t tokens, int32_t heads, int32_t head_dim) {
 }  // namespace
 
 bool kv_copy_grid_fits(int64_t tokens, int32_t heads, int32_t head_dim) {
-  return grid_fits((tokens + 3) / 4 * 4, (int64_t)heads * (head_dim / 8), 1) &&
+  return tokens <= kMaxWorkItems && grid_fits((tokens + 3) / 4 * 4, (int64_t)heads * (head_dim / 8), 1) &&
          (tokens + 3) / 4 * 4 * heads * (head_dim / 8) <= kMaxWorkItems - 255;
 }
 

@@ -183,7 +183,8 @@ def attention(q, cache, table, lengths, offsets=None, scale=None, window=0, max_
     knows it (a decoding step of several sequences is then not taken for a prompt); it
     decides how the work is cut, not what comes out.  lse=True: (out, log of the
     softmax's sum fp32 [T, heads]), to join parts.  Queries without a key get zeros (and
-    -inf); rows of no sequence are not written."""
+    -inf); rows of no sequence are not written.  out: dense, apart from q and the
+    cache."""
     if stream is not None:
         return on_stream(stream, (q, cache, table, lengths, offsets, out),
                          lambda: attention(q, cache, table, lengths, offsets, scale, window, max_queries, lse, out))

@@ -321,3 +321,21 @@ def test_c_mirror(side):
         assert torch.equal(a, b)
     with pytest.raises(mx.MXFP8Error, match="kv_attention"):
         kvcache.kv_attention(gq, HEADS * D, D, n, HEADS, twin, pages, PAGE, KV, D, table, width, width, out_lengths, None, n, 1, 0.0, 0, out)
+
+
+def test_no_rows_and_no_free_pages():
+    """A step without rows, and one whose requests get no page: lengths and cache stay as they were."""
+    torch = need_gpu()
+    from mxfp8_block_scaled_quantize_amd import kvcache
+    layer, normal = _layer(torch, 3, 0)
+    cache = kvcache.new(4, PAGE, KV, D, device="cuda")
+    free, _ = kvcache.pool(4, device="cuda")
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.full((2, 4), -1, dtype=torch.int32, device="cuda")
+    lengths = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for rows, counts in ((0, [0, 0]), (9, [3, 5])):
+        log("%d rows" % rows)
+        plan = kvcache.extend(table, lengths, torch.tensor(counts, dtype=torch.int32, device="cuda"), free, none, rows, PAGE)
+        assert plan.lengths.tolist() == [0, 0] and bool((plan.slots == -1).all()) and plan.free_count.tolist() == [0]
+        assert layer(normal(rows, HIDDEN).bfloat16(), cache, table, plan).shape == (rows, HIDDEN)
+        assert not bool(cache.any()) and bool((table == -1).all())

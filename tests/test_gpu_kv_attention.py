@@ -332,3 +332,44 @@ def test_drawn_sizes():
             continue
         c = Case(lengths, queries, kv_heads * group, kv_heads, d, page, seed=i)
         c.check(c.run(window=window, max_queries=max(max(queries), 1)), window=window, label="drawn %d" % i)
+
+
+@pytest.mark.parametrize("offsets", [[0, 5, 3, 9], [0, 9, 2, 4], [2, 7, 7, 1], [-4, 2, 100, 9]])
+@pytest.mark.parametrize("most", [3, 60])
+def test_odd_offsets_in_parts(offsets, most):
+    """The same where the keys are cut into parts: the joining launch holds the same rows for a sequence's."""
+    torch, kvcache = _kv()
+    log("offsets %s max_queries %d" % (offsets, most))
+    c = Case([5000, 60, 4000], [3, 3, 3], 2, 1, 64, 16, seed=10)
+    assert kvcache.kv_attention_workspace_bytes(9, 2, 1, 64, 3, c.table.shape[1], 16, 1, most, 0) > 0
+    out = torch.full((9, 2, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    kvcache.attention(c.q, c.cache, c.table, c.i32(c.lengths), c.i32(offsets), max_queries=most, out=out)
+    clamped, top = [], 0
+    for x in offsets:
+        top = max(top, min(max(x, 0), 9))
+        clamped.append(top)
+    want, _, bound, _ = ref.attention(c.q, c.k, c.v, 16, c.table, c.lengths, clamped, 64 ** -0.5, 0)
+    rows = ~want.isnan().all(2).all(1)
+    assert bool(((out.double() - want).abs() <= bound)[rows].all()) and bool((out[~rows] == 7).all())
+
+
+def test_as_many_sequences_and_heads_as_fit():
+    """2^24 rows of single queries: every sequence has the same page and query, and gets the same answer."""
+    torch, kvcache = _kv()
+    c = Case([13], [1], 128, 8, 64, 16, seed=11)
+    n = 1 << 17
+    log("%d sequences of %d heads" % (n, 128))
+    o, l = kvcache.attention(c.q.expand(n, 128, 64), c.cache, c.table.expand(n, -1).contiguous(), c.i32([13]).expand(n).contiguous(),
+                             lse=True)
+    want, lse = c.run(offsets=None)
+    assert bool((o == want).all()) and bool((l == lse).all())
+
+
+def test_windows_past_every_length():
+    """Windows that no sequence is as long as, up to the largest number: none."""
+    torch, kvcache = _kv()
+    c = Case([20011, 70], [2, 1], 4, 2, 128, 64, seed=12)
+    want = c.run(max_queries=2)
+    for window in (1 << 20, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1):
+        for x, y in zip(c.run(max_queries=2, window=window), want):
+            assert torch.equal(x, y)

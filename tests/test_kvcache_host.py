@@ -97,6 +97,7 @@ def test_append_and_read_refusals(mods):
         assert call(page=8) == SHAPE and call(pages=0) == SHAPE and call(heads=0) == SHAPE and call(d=96) == SHAPE
         assert call(d=32) == SHAPE and call(tokens=-1) == SHAPE
         assert call(pages=1 << 28) == LIMIT and call(heads=1 << 30) == LIMIT and call(tokens=1 << 33) == LIMIT
+        assert call(tokens=(1 << 63) - 1) == LIMIT
         assert call(cache=None) == NULL and call(k=None) == NULL and call(v=None) == NULL and call(slots=None) == NULL
         assert call(cache=P + 8) == MISALIGNED and call(k=P + 8) == MISALIGNED and call(v=P + 2) == MISALIGNED
         assert call(slots=P + 2) == MISALIGNED and call(tokens=0, k=None, v=None, slots=None) == OK
