@@ -26,30 +26,30 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 
-// The step's four runs of 16 keys: their page numbers, and which of them are pages.  No
-// branch here and in the loads (a number that is no page, a key behind the end are read
-// as ones that are there, and masked): the compiler can then wait for one step's loads
-// among the next one's.
+// WHOLE: 32 keys lie in one page (pages of 32 tokens or more), so that a step's keys have
+// scalar bases and their loads no address arithmetic (500 queries over 49152 keys, pages of
+// 64: 400 us, with an address for every lane 430).  Else pages are 16 tokens, a run each.
+//
+// The page numbers of a step's four runs of 16 keys, and of the wave's one.  No branch
+// here and in the loads (a number that is no page, a key behind the end are read as ones
+// that are there, and masked): the compiler can then wait for one step's loads among the
+// next one's.
+template <bool WHOLE>
 struct Runs {
-  int p[4];
-  uint32_t there;   // a bit for each
-  __device__ __forceinline__ void find(const Args& a, const Tile& t, int key, int end) {
+  uint32_t p[4], own;
+  __device__ __forceinline__ void find(const Args& a, const Tile& t, int key, int end, int w) {
+    const int32_t* row = a.table + t.sequence * a.ld_table;
+    const int shift = WHOLE ? a.page_shift : 4;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const int at = key + 16 * i < end ? key + 16 * i : end - 1;
-      p[i] = a.table[t.sequence * a.ld_table + (at >> a.page_shift)];
-    }
+    for (int i = 0; i < 4; i++) p[i] = WHOLE && (i & 1) ? p[i - 1] : (uint32_t)row[min(key + 16 * i, end - 1) >> shift];
+    own = (uint32_t)row[min(key + 16 * w, end - 1) >> shift];
   }
-  __device__ __forceinline__ void check(const Args& a) {   // once the numbers are wanted
-    there = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      const bool is = (unsigned)p[i] < (unsigned)a.pages;
-      there |= is ? 1u << i : 0u;
-      p[i] = is ? p[i] : 0;
-    }
-  }
+  __device__ __forceinline__ bool there(const Args& a, int i) const { return p[i] < (uint32_t)a.pages; }
+  __device__ __forceinline__ bool all(const Args& a) const { return max(max(p[0], p[1]), max(p[2], p[3])) < (uint32_t)a.pages; }
 };
+__device__ __forceinline__ const uint8_t* safe_record(const Args& a, int head, uint32_t page) {
+  return record_of(a, head, (int)min(page, (uint32_t)a.pages - 1));
+}
 
 // What a lane loads of a step's keys: 32 codes (16 bytes) and a scale for every MFMA.
 template <int D>
@@ -57,22 +57,29 @@ struct KeyPart {
   static constexpr int KS = D / 64;   // MFMA steps along a key
   u32x4 k[2][KS];
   uint32_t s[2][(KS + 1) / 2];
-  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key) {
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE>& runs, int head, int key) {
     const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
-    const int page_size = 1 << a.page_shift;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-      // the runs' first keys; a lane's own is at the same place behind either
-      const uint8_t* r[2];
+      if (WHOLE) {
+        const int page_size = 1 << a.page_shift;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(safe_record(a, head, runs.p[2 * i])), 0, (int)a.record, 0x00020000);
+        const int at = (key + 32 * i) & (page_size - 1);
 #pragma unroll
-      for (int j = 0; j < 2; j++) r[j] = record_of(a, head, runs.p[2 * i + j]) + ((key + 32 * i + 16 * j) & (page_size - 1)) * (D / 2);
-      const uint8_t* k0 = (c & 16 ? r[1] : r[0]) + ((c & 15) * (D / 2) + 16 * h);
+        for (int f = 0; f < KS; f++) k[i][f] = __builtin_amdgcn_raw_buffer_load_b128(r, c * (D / 2) + 16 * h + 32 * f, at * (D / 2), 0);
+        if (D == 64) s[i][0] = __builtin_amdgcn_raw_buffer_load_b16(r, c * (D / 32), page_size * D + at * (D / 32), 0);
+        else {
 #pragma unroll
-      for (int j = 0; j < 2; j++) {
-        const int at = (key + 32 * i + 16 * j) & (page_size - 1);
-        r[j] += page_size * D + at * (D / 32) - at * (D / 2);
+          for (int f = 0; f < KS / 2; f++) s[i][f] = __builtin_amdgcn_raw_buffer_load_b32(r, c * (D / 32) + 4 * f, page_size * D + at * (D / 32), 0);
+        }
+        continue;
       }
-      const uint8_t* s0 = (c & 16 ? r[1] : r[0]) + (c & 15) * (D / 32);
+      // a page for every 16 lanes
+      const uint8_t *r0 = safe_record(a, head, runs.p[2 * i]), *r1 = safe_record(a, head, runs.p[2 * i + 1]);
+      const uint8_t* const r = c & 16 ? r1 : r0;
+      const uint8_t *k0 = r + ((c & 15) * (D / 2) + 16 * h), *s0 = r + (16 * D + (c & 15) * (D / 32));
 #pragma unroll
       for (int f = 0; f < KS; f++) k[i][f] = *reinterpret_cast<const u32x4*>(k0 + 32 * f);
       if (D == 64) s[i][0] = *reinterpret_cast<const uint16_t*>(s0);
@@ -93,12 +100,12 @@ struct ValuePart {
   uint32_t s[UNITS];
   static __device__ __forceinline__ uint32_t quad(int u) { return ((threadIdx.x & (D == 64 ? 31 : 63)) + 64 * u) / (D / 8); }
   static __device__ __forceinline__ uint32_t eight(int u) { return ((threadIdx.x & 63) + 64 * u) % (D / 8); }
-  __device__ __forceinline__ void load(const Args& a, const Runs& runs, int head, int key, int w) {
-    const uint32_t page_size = 1u << a.page_shift;
-    const int page = w == 0 ? runs.p[0] : w == 1 ? runs.p[1] : w == 2 ? runs.p[2] : runs.p[3];
-    const uint32_t at = (uint32_t)(key + 16 * w) & (page_size - 1);
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE>& runs, int head, int key, int w) {
+    const uint32_t page_size = WHOLE ? 1u << a.page_shift : 16;
+    const uint32_t at = WHOLE ? (uint32_t)(key + 16 * w) & (page_size - 1) : 0;
     const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(record_of(a, head, page)), 0, (int)a.record, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(safe_record(a, head, runs.own)), 0, (int)a.record, 0x00020000);
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
       v[u] = __builtin_amdgcn_raw_buffer_load_b128(r, quad(u) * (2 * D) + 16 * eight(u), page_size * (D / 2) + (at >> 2) * (2 * D), 0);
@@ -106,13 +113,15 @@ struct ValuePart {
     }
   }
   // Of places that no query sees, zeros.
-  __device__ __forceinline__ void mask(const Runs& runs, int key, int end, int w) {
-    if (key + KEYS <= end && runs.there == 0xF) return;
+  template <bool WHOLE>
+  __device__ __forceinline__ void mask(const Args& a, const Runs<WHOLE>& runs, int key, int end, int w) {
+    const bool there = runs.own < (uint32_t)a.pages;
+    if (key + 16 * w + 16 <= end && there) return;
 #pragma unroll
     for (int u = 0; u < UNITS; u++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        if (!(runs.there >> w & 1) || key + 16 * w + 4 * (int)quad(u) + j >= end) {
+        if (!there || key + 16 * w + 4 * (int)quad(u) + j >= end) {
           v[u][j] = 0;
           s[u] &= ~(0xFFu << (8 * j));
         }
@@ -137,7 +146,7 @@ struct ValuePart {
   }
 };
 
-template <int D>
+template <int D, bool WHOLE>
 __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
   constexpr int KS = KeyPart<D>::KS;
   __shared__ __attribute__((aligned(16))) uint8_t values[2][D * ROW];
@@ -214,25 +223,24 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
     for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
   float top = -INFINITY, sum = 0.0f;
 
-  Runs runs, ahead;   // of this step and the next
+  Runs<WHOLE> runs, ahead;   // of this step and the next
   KeyPart<D> keys;
   ValuePart<D> vals;
   if (s0 < s1) {
-    runs.find(a, t, begin + KEYS * s0, end);
-    ahead.find(a, t, begin + KEYS * (s0 + 1), end);
-    runs.check(a);
+    runs.find(a, t, begin + KEYS * s0, end, w);
+    ahead.find(a, t, begin + KEYS * (s0 + 1), end, w);
     vals.load(a, runs, head, begin + KEYS * s0, w);
     keys.load(a, runs, head, begin + KEYS * s0);
-    vals.mask(runs, begin + KEYS * s0, end, w);
+    vals.mask(a, runs, begin + KEYS * s0, end, w);
     vals.store(lds + (s0 & 1) * D * ROW, w);
   }
   __syncthreads();
   for (int s = s0; s < s1; s++) {
     const int key = begin + KEYS * s;
-    Runs later;
-    ahead.check(a);
-    later.find(a, t, key + 2 * KEYS, end);
+    Runs<WHOLE> later;
+    later.find(a, t, key + 2 * KEYS, end, w);
     vals.load(a, ahead, head, key + KEYS, w);
+    lds_u8* const to = lds + ((s + 1) & 1) * D * ROW;
     const bool work = key < wave_hi && key + KEYS > wave_lo;   // wave-uniform
     v16f y[2];
     if (work) {
@@ -256,30 +264,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       }
     }
     keys.load(a, ahead, head, key + KEYS);   // in the registers that the products are done with
-    if (work) {
-      float mx = -INFINITY;
-      if (key >= all_lo && key + KEYS <= all_hi && runs.there == 0xF) {
-#pragma unroll
-        for (int i = 0; i < 2; i++)
-#pragma unroll
-          for (int j = 0; j < 16; j++) mx = fmaxf(mx, y[i][j]);
-      } else {
-        if (runs.there != 0xF) {
+    vals.mask(a, ahead, key + KEYS, end, w);
+    if (!work) {
+      vals.store(to, w);
+    } else {
+      const bool all = runs.all(a);
+      if (!(key >= all_lo && key + KEYS <= all_hi && all)) {
+        if (!all) {
 #pragma unroll
           for (int i = 0; i < 2; i++)
 #pragma unroll
             for (int j = 0; j < 16; j++)
-              if (!(runs.there >> (2 * i + (j >> 3)) & 1)) y[i][j] = -INFINITY;
+              if (!runs.there(a, 2 * i + (j >> 3))) y[i][j] = -INFINITY;
         }
         const uint32_t from = (uint32_t)(key + 4 * h - lo), span = (uint32_t)(hi - lo);
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll
-          for (int j = 0; j < 16; j++) {
+          for (int j = 0; j < 16; j++)
             if (from + (32 * i + 8 * (j >> 2) + (j & 3)) >= span) y[i][j] = -INFINITY;
-            mx = fmaxf(mx, y[i][j]);
-          }
       }
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int j = 0; j < 16; j++) mx = fmaxf(mx, y[i][j]);
       const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
       mx = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale2;
       if (__any(mx > top + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
@@ -290,12 +299,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
 #pragma unroll
         for (int d = 0; d < D / 32; d++) o[d] *= shrink;
       }
-    }
-    vals.mask(ahead, key + KEYS, end, w);
-    lds_u8* const to = lds + ((s + 1) & 1) * D * ROW;
-    if (!work) {
-      vals.store(to, w);
-    } else {
       const float base = top > -INFINITY ? top : 0.0f;
       const lds_u8* v = lds + (s & 1) * D * ROW + c * ROW;
       u32x4 p[4];   // weights of 16 keys each
@@ -322,7 +325,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       vals.store(to, w);
       product(2);
       product(3);
-
     }
     runs = ahead;
     ahead = later;
@@ -359,15 +361,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
   }
 }
 
+template <int D>
+void launch(const KvAttention& a, const Args& g, int64_t parts, hipStream_t stream) {
+  const int64_t tiles = kv_tiles(a, 128);
+  const dim3 grid((unsigned)(tiles * parts * a.cache.heads));
+  if (a.cache.page_size >= 32) hipLaunchKernelGGL((kv_attention_tile_kernel<D, true>), grid, dim3(256), 0, stream, g, (int)tiles);
+  else hipLaunchKernelGGL((kv_attention_tile_kernel<D, false>), grid, dim3(256), 0, stream, g, (int)tiles);
+}
+
 }  // namespace
 
 hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t parts, hipStream_t stream) {
   const kv::Args g = kv_args(a, parts);
-  const int64_t tiles = kv_tiles(a, 128);
-  const dim3 grid((unsigned)(tiles * parts * a.cache.heads));
-  if (a.cache.head_dim == 64) hipLaunchKernelGGL(kv_attention_tile_kernel<64>, grid, dim3(256), 0, stream, g, (int)tiles);
-  else if (a.cache.head_dim == 128) hipLaunchKernelGGL(kv_attention_tile_kernel<128>, grid, dim3(256), 0, stream, g, (int)tiles);
-  else hipLaunchKernelGGL(kv_attention_tile_kernel<256>, grid, dim3(256), 0, stream, g, (int)tiles);
+  if (a.cache.head_dim == 64) launch<64>(a, g, parts, stream);
+  else if (a.cache.head_dim == 128) launch<128>(a, g, parts, stream);
+  else launch<256>(a, g, parts, stream);
   return hipGetLastError();
 }
 
