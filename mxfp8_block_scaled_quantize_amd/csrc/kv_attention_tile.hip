@@ -9,9 +9,23 @@
 // product's operand as they are, with that product's keys in the order (4 h + 0..3, 8 +
 // 4 h + 0..3) for lane half h.  The values are turned to BF16 once for the workgroup,
 // a step ahead: a lane takes 4 keys x 8 values, swaps them pairwise and writes, for each
-// value, the 4 keys to an LDS row of 64 keys in that order (two buffers, 16-byte chunks
-// XOR-swizzled by the row so that neither writes nor reads collide).  O^T = V^T P^T by
-// 32x32x16 MFMAs.  One barrier a step.
+// value, the 4 keys to an LDS row of 64 keys in that order (two buffers).  O^T = V^T P^T
+// by 32x32x16 MFMAs.  One barrier a step.
+//
+// LDS: a row is 8 chunks of 8 keys (16 bytes), chunk k of value 8 e + i in place k ^ (i /
+// 2) ^ (e with its bits 1 and 2 swapped).  Reads take 16 bytes of 32 neighbouring rows,
+// which the hardware serves 16 lanes at a time (lanes 0-3, 12-15, 20-23, 24-27, then the
+// others): these meet all 16 chunks of 64 banks.  Writes of 8 bytes go 16 neighbouring
+// lanes at a time to 32 banks: 8 neighbouring e times the two halves of a chunk, which is
+// why lane bit 3 is the half.  No conflicts are counted (with the chunks placed by k ^ e
+// in padded rows 161 cycles a wave and step, and 3 % of the time).
+//
+// What bounds it: of a step's 2100 cycles a wave (500 queries over 49152 keys, 32 heads, 2
+// waves a SIMD at 2.0 GHz) the matrix cores work 960 and the vector unit 1000, of which
+// the exponentials are a quarter, and the two overlap little.  Tried and slower: 3 waves a
+// SIMD with 32 keys a softmax (470 us against 432), 8 waves that share the values (511),
+// 64 rows a wave (600), wave priorities (442), fragments read a product ahead (400
+// against 395).
 #include "kv_attention.h"
 
 namespace mx {
@@ -21,10 +35,15 @@ using namespace kv;
 namespace {
 
 constexpr int KEYS = 64;
-constexpr int ROW = 2 * KEYS + 16;   // bytes of a value's LDS row: 16 spare ones set neighbouring rows apart
+constexpr int ROW = 2 * KEYS;   // bytes of a value's LDS row: 8 chunks of 8 keys
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
+
+// Place of chunk k (bytes from its row's start) in the row of value 8 e + i: see the head.
+__device__ __forceinline__ uint32_t place_of(uint32_t k, uint32_t e, uint32_t i) {
+  return ((k ^ (i >> 1) ^ ((e & 1) | (e & 2) << 1 | (e & 4) >> 1)) & 7) * 16;
+}
 
 // WHOLE: 32 keys lie in one page (pages of 32 tokens or more), so that a step's keys have
 // scalar bases and their loads no address arithmetic (500 queries over 49152 keys, pages of
@@ -98,8 +117,11 @@ struct ValuePart {
   static constexpr int UNITS = D == 256 ? 2 : 1;
   u32x4 v[UNITS];
   uint32_t s[UNITS];
-  static __device__ __forceinline__ uint32_t quad(int u) { return ((threadIdx.x & (D == 64 ? 31 : 63)) + 64 * u) / (D / 8); }
-  static __device__ __forceinline__ uint32_t eight(int u) { return ((threadIdx.x & 63) + 64 * u) % (D / 8); }
+  // quad 2 * half + odd of the run's four
+  static __device__ __forceinline__ uint32_t half() { return (threadIdx.x >> 3) & 1; }
+  static __device__ __forceinline__ uint32_t odd(int u) { return D == 256 ? u : (threadIdx.x >> (D == 64 ? 4 : 5)) & 1; }
+  static __device__ __forceinline__ uint32_t quad(int u) { return 2 * half() + odd(u); }
+  static __device__ __forceinline__ uint32_t eight() { return ((threadIdx.x & 7) | ((threadIdx.x & 63) >> 4) << 3) & (D / 8 - 1); }
   template <bool WHOLE>
   __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE>& runs, int head, int key, int w) {
     const uint32_t page_size = WHOLE ? 1u << a.page_shift : 16;
@@ -108,8 +130,8 @@ struct ValuePart {
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(safe_record(a, head, runs.own)), 0, (int)a.record, 0x00020000);
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
-      v[u] = __builtin_amdgcn_raw_buffer_load_b128(r, quad(u) * (2 * D) + 16 * eight(u), page_size * (D / 2) + (at >> 2) * (2 * D), 0);
-      s[u] = __builtin_amdgcn_raw_buffer_load_b32(r, (eight(u) >> 2) * page_size + 4 * quad(u), page_size * (D + D / 32) + at, 0);
+      v[u] = __builtin_amdgcn_raw_buffer_load_b128(r, quad(u) * (2 * D) + 16 * eight(), page_size * (D / 2) + (at >> 2) * (2 * D), 0);
+      s[u] = __builtin_amdgcn_raw_buffer_load_b32(r, (eight() >> 2) * page_size + 4 * quad(u), page_size * (D + D / 32) + at, 0);
     }
   }
   // Of places that no query sees, zeros.
@@ -133,14 +155,14 @@ struct ValuePart {
       uint32_t x[4][4];
 #pragma unroll
       for (int j = 0; j < 4; j++) bf16_of(v[u][j], scale_of(s[u], j), x[j]);
-      const uint32_t chunk = 2 * w + (quad(u) & 1), d = eight(u);
-      lds_u8* const row = to + 8 * d * ROW + ((chunk ^ d) & 7) * 16 + (quad(u) >> 1) * 8;
+      lds_u8* const row = to + eight() * (8 * ROW) + 8 * half();
+      const uint32_t first = place_of(2 * w + odd(u), eight(), 0);
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         u32x2 word;
         word.x = (i & 1) ? highs(x[0][i >> 1], x[1][i >> 1]) : lows(x[0][i >> 1], x[1][i >> 1]);
         word.y = (i & 1) ? highs(x[2][i >> 1], x[3][i >> 1]) : lows(x[2][i >> 1], x[3][i >> 1]);
-        *reinterpret_cast<lds_u32x2*>(row + i * ROW) = word;
+        *reinterpret_cast<lds_u32x2*>(row + (first ^ (16 * (i >> 1))) + i * ROW) = word;
       }
     }
   }
@@ -301,6 +323,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       }
       const float base = top > -INFINITY ? top : 0.0f;
       const lds_u8* v = lds + (s & 1) * D * ROW + c * ROW;
+      const uint32_t first = place_of(h, c >> 3, c & 7);
       u32x4 p[4];   // weights of 16 keys each
       auto weights = [&](int i) {
 #pragma unroll
@@ -314,7 +337,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       auto product = [&](int f) {
 #pragma unroll
         for (int d = 0; d < D / 32; d++) {
-          const u32x4 vw = *reinterpret_cast<const lds_u32x4*>(v + d * (32 * ROW) + (((2 * f + h) ^ (4 * d) ^ (c >> 3)) & 7) * 16);
+          const u32x4 vw = *reinterpret_cast<const lds_u32x4*>(v + (first ^ (32 * (f ^ (d & 1)))) + d * (32 * ROW));
           o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vw), __builtin_bit_cast(bf16x8, p[f]), o[d], 0, 0, 0);
         }
       };
