@@ -360,57 +360,79 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   }
 }
 
-// ---- joining the parts of a row: a wave for each part in turn, a workgroup a row.
-template <int D>
+// ---- joining the parts of a row: bound by the stream of the parts' sums for many rows, by
+// two loads' latency for few.  G waves have a row (4 / G rows a workgroup), lane p part p's
+// maximum and sum (64 parts at most), every lane 2 (of 256: 4) of the outputs.  Their loads do
+// not wait for the statistics: what an empty part's place holds is loaded and not taken.
+// 16000 rows of 4 parts: 22 us with a workgroup a row and loads behind the statistics.
+template <int D, int G>
 __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
-  __shared__ float meet[WAVES][D];
+  constexpr int V = D == 256 ? 4 : 2, PER = 64 * V / D, AHEAD = 4;   // outputs of a lane; parts that a wave's lanes take at a time
+  typedef float vec __attribute__((ext_vector_type(V)));
+  __shared__ __attribute__((aligned(16))) float meet[G == 1 ? 1 : WAVES][D];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x, all_rows = (int64_t)a.tokens * a.heads;
+  const int64_t row = G == 1 ? (int64_t)blockIdx.x * WAVES + w : blockIdx.x, all_rows = (int64_t)a.tokens * a.heads;
+  if (row >= all_rows) return;
   const int token = (int)(row / a.heads);
   if (a.offsets) {   // rows of no sequence; the offsets' running maximum is what counts
     if (token < a.offsets[0]) return;
     int end = a.offsets[a.sequences];
     if (token >= end) {
       for (int i = lane; i < a.sequences; i += 64) end = max(end, a.offsets[i]);
-      if (!__any(token < end)) return;   // the same for all waves
+      if (!__any(token < end)) return;   // the same for all waves of the row
     }
   }
-  const float* ml = a.sums + a.parts * all_rows * D + row * 2;
-  float all = -INFINITY;
-  for (int p = lane; p < a.parts; p += 64) all = fmaxf(all, ml[p * all_rows * 2]);
+  const int at = (lane & (D / V - 1)) * V, mine = lane / (D / V), step = G * PER;
+  const float* const o = a.sums + row * D + at;
+  auto load = [&](vec* x, int p0) {
 #pragma unroll
-  for (int x = 32; x; x >>= 1) all = fmaxf(all, __shfl_xor(all, x, 64));
+    for (int u = 0; u < AHEAD; u++) x[u] = *reinterpret_cast<const vec*>(o + min(p0 + u * step + mine, a.parts - 1) * all_rows * D);
+  };
+  vec x[AHEAD], r;
+  const int first = (G == 1 ? 0 : w) * PER;
+  load(x, first);
+  const f32x2* const ml = reinterpret_cast<const f32x2*>(a.sums + a.parts * all_rows * D) + row;
+  f32x2 stat = {-INFINITY, 0.0f};
+  if (lane < a.parts) stat = ml[lane * all_rows];
+  float all = stat.x;
+#pragma unroll
+  for (int i = 32; i; i >>= 1) all = fmaxf(all, __shfl_xor(all, i, 64));
   const float base = all > -INFINITY ? all : 0.0f;
-  float total = 0.0f;
-  for (int p = lane; p < a.parts; p += 64) total += ml[p * all_rows * 2 + 1] * __builtin_amdgcn_exp2f(ml[p * all_rows * 2] - base);
+  // a part without a key has no outputs, not even zeros: -1
+  const float f = stat.y == 0.0f ? -1.0f : __builtin_amdgcn_exp2f(stat.x - base);
+  float total = stat.y == 0.0f ? 0.0f : stat.y * f;
 #pragma unroll
-  for (int x = 32; x; x >>= 1) total += __shfl_xor(total, x, 64);
-  float r[D / 64];
+  for (int i = 32; i; i >>= 1) total += __shfl_xor(total, i, 64);
 #pragma unroll
-  for (int i = 0; i < D / 64; i++) r[i] = 0.0f;
-  for (int p = w; p < a.parts; p += WAVES) {
-    const float m = ml[p * all_rows * 2], l = ml[p * all_rows * 2 + 1];
-    if (l == 0.0f) continue;   // nothing there, not even zeros
-    const float f = __builtin_amdgcn_exp2f(m - base);
-    const float* o = a.sums + (p * all_rows + row) * D;
+  for (int i = 0; i < V; i++) r[i] = 0.0f;
+  for (int p0 = first; p0 < a.parts; p0 += AHEAD * step) {
+    if (p0 > first) load(x, p0);
 #pragma unroll
-    for (int i = 0; i < D / 64; i++) r[i] += f * o[64 * i + lane];
-  }
+    for (int u = 0; u < AHEAD; u++) {
+      const int p = p0 + u * step + mine;
+      const float fp = __shfl(f, p < a.parts ? p : 0, 64);
+      const bool take = p < a.parts && !(fp < 0.0f);   // NaN too
 #pragma unroll
-  for (int i = 0; i < D / 64; i++) meet[w][64 * i + lane] = r[i];
-  __syncthreads();
-  const bool some = total > 0.0f || total != total;
-  if (threadIdx.x < D / 2) {
-    float x = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int u = 0; u < WAVES; u++) {
-      x += meet[u][2 * threadIdx.x];
-      y += meet[u][2 * threadIdx.x + 1];
+      for (int i = 0; i < V; i++) r[i] = take ? fmaf(fp, x[u][i], r[i]) : r[i];
     }
-    const float factor = some ? 1.0f / total : 0.0f;
-    reinterpret_cast<uint32_t*>(a.out + row * D)[threadIdx.x] = bf16_pair(x * factor, y * factor);
   }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = some ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
+  if (PER == 2)
+#pragma unroll
+    for (int i = 0; i < V; i++) r[i] += __shfl_xor(r[i], 32, 64);
+  if (G > 1) {
+    if (mine == 0) *reinterpret_cast<vec*>(&meet[w][at]) = r;
+    __syncthreads();
+    if (w > 0) return;
+    r = *reinterpret_cast<const vec*>(&meet[0][at]);
+#pragma unroll
+    for (int u = 1; u < WAVES; u++) r += *reinterpret_cast<const vec*>(&meet[u][at]);
+  }
+  const bool some = total > 0.0f || total != total;
+  const float factor = some ? 1.0f / total : 0.0f;
+  if (mine == 0)
+#pragma unroll
+    for (int i = 0; i < V; i += 2) reinterpret_cast<uint32_t*>(a.out + row * D + at)[i / 2] = bf16_pair(r[i] * factor, r[i + 1] * factor);
+  if (a.lse && lane == 0) a.lse[row] = some ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
 }
 
 int64_t group_of(const KvAttention& a) { return a.heads / a.cache.heads; }
@@ -424,11 +446,13 @@ int64_t rows_of(const KvAttention& a) {
 
 // Parts that the keys of a tile are cut into: as many as give every compute unit a
 // workgroup (two for the kernel for many queries), of at least 512 keys.  A second
-// launch joins them, 3 to 4 us, in which a workgroup goes through 1000 keys: one token of
-// a sequence of 131071 keys, 8 heads: 34.5 us with 32 parts, 38.9 with 64, 48 with 16; 64
-// sequences: 69 us with 1 part, 70 with 2, 72 with 4.  Where there are tiles enough, parts
-// bound what one very long sequence among them takes: 16384 keys are 70 us.
-constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;
+// launch joins them, about 3 us, in which a workgroup goes through 1000 keys: one token of
+// a sequence of 131071 keys, 8 heads: 29.6 us with 32 parts, 30.0 with 64, 44.5 with 16; of
+// 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of up to 8192: 68.0 us with 1 part, 68.5
+// with 2, 69.5 with 4; 500 queries over 49152 keys: 356 with 4, 434 with 3, 364 with 8.
+// Where there are tiles enough, parts bound what one very long sequence among them takes:
+// 16384 keys are 70 us.
+constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;   // a lane each in kv_join_kernel
 int64_t parts_of(const KvAttention& a) {
   const int64_t tm = rows_of(a);
   int64_t tiles = kv_tiles(a, tm);
@@ -460,7 +484,10 @@ hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
     e = hipGetLastError();
   }
   if (e == hipSuccess && parts > 1) {
-    hipLaunchKernelGGL(kv_join_kernel<D>, dim3((unsigned)(a.tokens * a.heads)), dim3(64 * WAVES), 0, stream, g);
+    // four waves a row where one would go through the parts in more than two rounds
+    const int64_t rows = a.tokens * a.heads;
+    if (parts <= 8) hipLaunchKernelGGL((kv_join_kernel<D, 1>), dim3((unsigned)((rows + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, g);
+    else hipLaunchKernelGGL((kv_join_kernel<D, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
   }
   return e;
