@@ -10,6 +10,12 @@
 // for lane group g, and the values' codes stand in groups of four keys for that.
 // The four waves of a workgroup take every fourth 32 keys; their maxima, sums and
 // outputs meet in LDS at the end.
+//
+// Measured (32 heads, 8 of keys, of 128): 64 sequences of up to 8192 tokens, 358 MB in 66 us,
+// 5.4 TB/s (a plain sum over as many bytes reaches 6.3; this kernel's loads alone take 64);
+// one of 131071, 143 MB in 26 us, and 4 for the join.  Two steps of a wave are on their
+// way, with 4 waves a SIMD: three steps, or fewer waves, were slower.  Of the chip's time the
+// matrix cores work 12 %, the vector unit 30.
 #include "kv_attention.h"
 
 namespace mx {
