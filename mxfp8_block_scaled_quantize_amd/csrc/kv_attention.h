@@ -185,6 +185,7 @@ inline int64_t kv_tiles(const KvAttention& a, int64_t tm) {
   return (a.tokens * group + with * (tm - 1)) / tm;
 }
 kv::Args kv_args(const KvAttention& a, int64_t parts);
-hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t parts, hipStream_t stream);
+// rows: 64 or 128 a workgroup.
+hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t rows, int64_t parts, hipStream_t stream);
 
 }  // namespace mx

@@ -443,33 +443,50 @@ __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
 
 int64_t group_of(const KvAttention& a) { return a.heads / a.cache.heads; }
 
-// Rows of a tile: 16 or 32 for a run of queries that fits, else 128 (the kernel for
-// many queries).
-int64_t rows_of(const KvAttention& a) {
-  const int64_t rows = a.max_queries < 65536 ? a.max_queries * group_of(a) : 65536;
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : 128;
-}
-
 // Parts that the keys of a tile are cut into: as many as give every compute unit a
-// workgroup (two for the kernel for many queries), of at least 512 keys.  A second
-// launch joins them, about 3 us, in which a workgroup goes through 1000 keys: one token of
-// a sequence of 131071 keys, 8 heads: 29.6 us with 32 parts, 30.0 with 64, 44.5 with 16; of
-// 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of up to 8192: 68.0 us with 1 part, 68.5
-// with 2, 69.5 with 4; 500 queries over 49152 keys: 356 with 4, 434 with 3, 364 with 8.
-// Where there are tiles enough, parts bound what one very long sequence among them takes:
-// 16384 keys are 70 us.
-constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;   // a lane each in kv_join_kernel
-int64_t parts_of(const KvAttention& a) {
-  const int64_t tm = rows_of(a);
+// workgroup (of the kernel for many queries as many as it holds), of at least 512 keys.  A
+// second launch joins them, about 3 us, in which a workgroup goes through 1000 keys: one
+// token of a sequence of 131071 keys, 8 heads: 29.6 us with 32 parts, 30.0 with 64, 44.5 with
+// 16; of 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of up to 8192: 68.0 us with 1
+// part, 68.5 with 2, 69.5 with 4; 500 queries over 49152 keys: 356 with 4, 434 with 3, 364
+// with 8.  Where there are tiles enough, parts bound what one very long sequence among them
+// takes: 16384 keys are 70 us.
+constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;   // parts: a lane each in kv_join_kernel
+
+// Keys that a tile can see.
+int64_t keys_of(const KvAttention& a) {
+  const int64_t keys = a.table_width * a.cache.page_size;
+  return a.window > 0 && a.window + a.max_queries < keys ? a.window + a.max_queries : keys;
+}
+// Tiles of tm rows times heads: as many as runs of max_queries have, if that is less than
+// what any offsets can give.
+int64_t blocks_of(const KvAttention& a, int64_t tm) {
   int64_t tiles = kv_tiles(a, tm);
-  if (a.offsets && a.max_queries < 65536) {   // as many as runs of max_queries have, if that is less
+  if (a.offsets && a.max_queries < 65536) {
     const int64_t likely = a.sequences * ((a.max_queries * group_of(a) + tm - 1) / tm);
     tiles = tiles < likely ? tiles : likely;
   }
-  const int64_t blocks = tiles * a.cache.heads;
-  int64_t keys = a.table_width * a.cache.page_size;
-  if (a.window > 0 && a.window + a.max_queries < keys) keys = a.window + a.max_queries;
-  const int64_t fill = (tm == 128 ? 512 : 256) / (blocks > 0 ? blocks : 1), bound = (keys + MOST_KEYS - 1) / MOST_KEYS;
+  return tiles * a.cache.heads;
+}
+// Rows of a tile: 16 or 32 for a run of queries that fits, else 128, or 64 (the kernel for
+// many queries).  64 rows leave no wave idle where a run has no more, but two waves then do
+// what four do for the values: of 256 values, where registers leave a SIMD one wave, it is
+// faster everywhere (36 rows of 16 sequences of 16384 keys: 191 us, 295 with 128 rows; 64 of
+// 2048: 101 and 166), else where the keys give four workgroups a compute unit (of 128 values:
+// 94 and 114 us, 61 and 60; one sequence of 65536 keys, 512 workgroups: 46 and 42).
+constexpr int64_t FILL_64 = 1024;
+int64_t rows_of(const KvAttention& a) {
+  const int64_t rows = a.max_queries < 65536 ? a.max_queries * group_of(a) : 65536;
+  if (rows <= 32) return rows <= 16 ? 16 : 32;
+  if (rows > 64) return 128;
+  const int64_t most = keys_of(a) / LEAST_KEYS;
+  return a.cache.head_dim == 256 || blocks_of(a, 64) * (most < MOST_PARTS ? most : MOST_PARTS) >= FILL_64 ? 64 : 128;
+}
+
+int64_t parts_of(const KvAttention& a) {
+  const int64_t tm = rows_of(a), blocks = blocks_of(a, tm), keys = keys_of(a);
+  const int64_t wanted = tm < 64 ? 256 : tm == 64 && a.cache.head_dim < 256 ? FILL_64 : 512;
+  const int64_t fill = wanted / (blocks > 0 ? blocks : 1), bound = (keys + MOST_KEYS - 1) / MOST_KEYS;
   int64_t parts = fill > bound ? fill : bound;
   const int64_t most = keys / LEAST_KEYS;
   parts = parts < most ? parts : most;
@@ -482,8 +499,8 @@ hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
   const int64_t tm = rows_of(a);
   const dim3 grid((unsigned)(kv_tiles(a, tm) * parts * a.cache.heads));
   hipError_t e = hipSuccess;
-  if (tm == 128) {
-    e = launch_kv_attention_tile(a, parts, stream);
+  if (tm >= 64) {
+    e = launch_kv_attention_tile(a, tm, parts, stream);
   } else {
     if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
     else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);

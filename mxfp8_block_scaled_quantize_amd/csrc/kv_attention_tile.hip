@@ -1,7 +1,7 @@
 // Attention of many queries (prompts, pieces of prompts) over the paged MXFP4 cache:
 // bound by the matrix cores and, beside them, by the softmax's exponentials.
 //
-// A workgroup of 4 waves has 128 rows of one sequence and key-value head, 32 a wave,
+// A workgroup of W = 4 (or 2) waves has 32 W rows of one sequence and key-value head,
 // and goes through its keys 64 at a time.  S^T = K Q^T by 32x32x64 scaled MFMAs whose
 // FP4 operand is 16 bytes of a key's codes a lane, loaded straight from the cache a
 // step ahead.  Lane (c, h) = (l % 32, l / 32) gets the scores of row c and keys 8 (i /
@@ -49,19 +49,20 @@ __device__ __forceinline__ uint32_t place_of(uint32_t k, uint32_t e, uint32_t i)
 // scalar bases and their loads no address arithmetic (500 queries over 49152 keys, pages of
 // 64: 400 us, with an address for every lane 430).  Else pages are 16 tokens, a run each.
 //
-// The page numbers of a step's four runs of 16 keys, and of the wave's one.  No branch
+// The page numbers of a step's four runs of 16 keys, and of the wave's R.  No branch
 // here and in the loads (a number that is no page, a key behind the end are read as ones
 // that are there, and masked): the compiler can then wait for one step's loads among the
 // next one's.
-template <bool WHOLE>
+template <bool WHOLE, int R>
 struct Runs {
-  uint32_t p[4], own;
+  uint32_t p[4], own[R];
   __device__ __forceinline__ void find(const Args& a, const Tile& t, int key, int end, int w) {
     const int32_t* row = a.table + t.sequence * a.ld_table;
     const int shift = WHOLE ? a.page_shift : 4;
 #pragma unroll
     for (int i = 0; i < 4; i++) p[i] = WHOLE && (i & 1) ? p[i - 1] : (uint32_t)row[min(key + 16 * i, end - 1) >> shift];
-    own = (uint32_t)row[min(key + 16 * w, end - 1) >> shift];
+#pragma unroll
+    for (int j = 0; j < R; j++) own[j] = (uint32_t)row[min(key + 16 * (R * w + j), end - 1) >> shift];
   }
   __device__ __forceinline__ bool there(const Args& a, int i) const { return p[i] < (uint32_t)a.pages; }
   __device__ __forceinline__ bool all(const Args& a) const { return max(max(p[0], p[1]), max(p[2], p[3])) < (uint32_t)a.pages; }
@@ -76,8 +77,8 @@ struct KeyPart {
   static constexpr int KS = D / 64;   // MFMA steps along a key
   u32x4 k[2][KS];
   uint32_t s[2][(KS + 1) / 2];
-  template <bool WHOLE>
-  __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE>& runs, int head, int key) {
+  template <bool WHOLE, int R>
+  __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE, R>& runs, int head, int key) {
     const uint32_t lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -110,8 +111,8 @@ struct KeyPart {
   }
 };
 
-// What a lane loads of a step's values: units of 4 keys x 8 values of the wave's run of 16
-// keys (with 64 values both halves of the wave the same ones).
+// What a lane loads of a run's values: units of 4 keys x 8 values of 16 keys, run w of the
+// step (with 64 values both halves of the wave the same ones).
 template <int D>
 struct ValuePart {
   static constexpr int UNITS = D == 256 ? 2 : 1;
@@ -123,11 +124,11 @@ struct ValuePart {
   static __device__ __forceinline__ uint32_t quad(int u) { return 2 * half() + odd(u); }
   static __device__ __forceinline__ uint32_t eight() { return ((threadIdx.x & 7) | ((threadIdx.x & 63) >> 4) << 3) & (D / 8 - 1); }
   template <bool WHOLE>
-  __device__ __forceinline__ void load(const Args& a, const Runs<WHOLE>& runs, int head, int key, int w) {
+  __device__ __forceinline__ void load(const Args& a, uint32_t page, int head, int key, int w) {
     const uint32_t page_size = WHOLE ? 1u << a.page_shift : 16;
     const uint32_t at = WHOLE ? (uint32_t)(key + 16 * w) & (page_size - 1) : 0;
     const __amdgpu_buffer_rsrc_t r =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(safe_record(a, head, runs.own)), 0, (int)a.record, 0x00020000);
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(safe_record(a, head, page)), 0, (int)a.record, 0x00020000);
 #pragma unroll
     for (int u = 0; u < UNITS; u++) {
       v[u] = __builtin_amdgcn_raw_buffer_load_b128(r, quad(u) * (2 * D) + 16 * eight(), page_size * (D / 2) + (at >> 2) * (2 * D), 0);
@@ -135,9 +136,8 @@ struct ValuePart {
     }
   }
   // Of places that no query sees, zeros.
-  template <bool WHOLE>
-  __device__ __forceinline__ void mask(const Args& a, const Runs<WHOLE>& runs, int key, int end, int w) {
-    const bool there = runs.own < (uint32_t)a.pages;
+  __device__ __forceinline__ void mask(const Args& a, uint32_t page, int key, int end, int w) {
+    const bool there = page < (uint32_t)a.pages;
     if (key + 16 * w + 16 <= end && there) return;
 #pragma unroll
     for (int u = 0; u < UNITS; u++)
@@ -168,8 +168,8 @@ struct ValuePart {
   }
 };
 
-template <int D, bool WHOLE>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
+template <int D, bool WHOLE, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
   constexpr int KS = KeyPart<D>::KS;
   __shared__ __attribute__((aligned(16))) uint8_t values[2][D * ROW];
   lds_u8* const lds = (lds_u8*)&values[0][0];
@@ -180,8 +180,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
   const int part = rest % a.parts;
   Tile t;
   // the last tiles of a sequence, which see the most keys, first
-  if (!find_tile<128>(a, tiles - 1 - rest / a.parts, &t)) return;   // the whole workgroup
-  const int rows = t.rows < 128 ? t.rows : 128;
+  if (!find_tile<32 * W>(a, tiles - 1 - rest / a.parts, &t)) return;   // the whole workgroup
+  const int rows = t.rows < 32 * W ? t.rows : 32 * W;
   const int64_t all_rows = (int64_t)a.tokens * a.heads;
 
   int first_lo, first_hi, last_lo, last_hi;
@@ -245,23 +245,36 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
     for (int i = 0; i < 16; i++) o[d][i] = 0.0f;
   float top = -INFINITY, sum = 0.0f;
 
-  Runs<WHOLE> runs, ahead;   // of this step and the next
+  constexpr int R = 4 / W;   // runs of 16 keys whose values a wave turns to BF16
+  Runs<WHOLE, R> runs, ahead;   // of this step and the next
   KeyPart<D> keys;
-  ValuePart<D> vals;
+  ValuePart<D> vals[R];
+  auto load_values = [&](const Runs<WHOLE, R>& of, int key) {
+#pragma unroll
+    for (int j = 0; j < R; j++) vals[j].template load<WHOLE>(a, of.own[j], head, key, R * w + j);
+  };
+  auto mask_values = [&](const Runs<WHOLE, R>& of, int key) {
+#pragma unroll
+    for (int j = 0; j < R; j++) vals[j].mask(a, of.own[j], key, end, R * w + j);
+  };
+  auto store_values = [&](lds_u8* to) {
+#pragma unroll
+    for (int j = 0; j < R; j++) vals[j].store(to, R * w + j);
+  };
   if (s0 < s1) {
     runs.find(a, t, begin + KEYS * s0, end, w);
     ahead.find(a, t, begin + KEYS * (s0 + 1), end, w);
-    vals.load(a, runs, head, begin + KEYS * s0, w);
+    load_values(runs, begin + KEYS * s0);
     keys.load(a, runs, head, begin + KEYS * s0);
-    vals.mask(a, runs, begin + KEYS * s0, end, w);
-    vals.store(lds + (s0 & 1) * D * ROW, w);
+    mask_values(runs, begin + KEYS * s0);
+    store_values(lds + (s0 & 1) * D * ROW);
   }
   __syncthreads();
   for (int s = s0; s < s1; s++) {
     const int key = begin + KEYS * s;
-    Runs<WHOLE> later;
+    Runs<WHOLE, R> later;
     later.find(a, t, key + 2 * KEYS, end, w);
-    vals.load(a, ahead, head, key + KEYS, w);
+    load_values(ahead, key + KEYS);
     lds_u8* const to = lds + ((s + 1) & 1) * D * ROW;
     const bool work = key < wave_hi && key + KEYS > wave_lo;   // wave-uniform
     v16f y[2];
@@ -286,9 +299,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       }
     }
     keys.load(a, ahead, head, key + KEYS);   // in the registers that the products are done with
-    vals.mask(a, ahead, key + KEYS, end, w);
+    mask_values(ahead, key + KEYS);
     if (!work) {
-      vals.store(to, w);
+      store_values(to);
     } else {
       const bool all = runs.all(a);
       if (!(key >= all_lo && key + KEYS <= all_hi && all)) {
@@ -345,7 +358,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
       product(0);
       product(1);
       weights(1);
-      vals.store(to, w);
+      store_values(to);
       product(2);
       product(3);
     }
@@ -384,21 +397,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void kv_attention_tile_kerne
   }
 }
 
-template <int D>
+template <int D, int W>
 void launch(const KvAttention& a, const Args& g, int64_t parts, hipStream_t stream) {
-  const int64_t tiles = kv_tiles(a, 128);
+  const int64_t tiles = kv_tiles(a, 32 * W);
   const dim3 grid((unsigned)(tiles * parts * a.cache.heads));
-  if (a.cache.page_size >= 32) hipLaunchKernelGGL((kv_attention_tile_kernel<D, true>), grid, dim3(256), 0, stream, g, (int)tiles);
-  else hipLaunchKernelGGL((kv_attention_tile_kernel<D, false>), grid, dim3(256), 0, stream, g, (int)tiles);
+  if (a.cache.page_size >= 32) hipLaunchKernelGGL((kv_attention_tile_kernel<D, true, W>), grid, dim3(64 * W), 0, stream, g, (int)tiles);
+  else hipLaunchKernelGGL((kv_attention_tile_kernel<D, false, W>), grid, dim3(64 * W), 0, stream, g, (int)tiles);
+}
+template <int D>
+void launch(const KvAttention& a, const Args& g, int64_t rows, int64_t parts, hipStream_t stream) {
+  if (rows == 64) launch<D, 2>(a, g, parts, stream);
+  else launch<D, 4>(a, g, parts, stream);
 }
 
 }  // namespace
 
-hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t parts, hipStream_t stream) {
+hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t rows, int64_t parts, hipStream_t stream) {
   const kv::Args g = kv_args(a, parts);
-  if (a.cache.head_dim == 64) launch<64>(a, g, parts, stream);
-  else if (a.cache.head_dim == 128) launch<128>(a, g, parts, stream);
-  else launch<256>(a, g, parts, stream);
+  if (a.cache.head_dim == 64) launch<64>(a, g, rows, parts, stream);
+  else if (a.cache.head_dim == 128) launch<128>(a, g, rows, parts, stream);
+  else launch<256>(a, g, rows, parts, stream);
   return hipGetLastError();
 }
 

@@ -373,3 +373,16 @@ def test_windows_past_every_length():
     for window in (1 << 20, 2 ** 31 - 1, 2 ** 31, 2 ** 63 - 1):
         for x, y in zip(c.run(max_queries=2, window=window), want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("heads,kv_heads,most", [(8, 2, 9), (8, 2, 16), (3, 3, 33), (3, 3, 64), (7, 1, 9), (60, 1, 1)])
+def test_between_few_and_many_rows(d, page, heads, kv_heads, most):
+    """33 to 64 rows of a sequence and head; runs longer than announced; windows; a long context in parts."""
+    queries = [most, 1, max(most - 3, 1), 2 * most + 1, most]
+    lengths = [700, 130, 40, 333, 5000]
+    log("D=%d page=%d heads %d/%d queries %s" % (d, page, heads, kv_heads, queries))
+    c = Case(lengths, queries, heads, kv_heads, d, page, seed=most + d)
+    c.check(c.run(max_queries=most))
+    c.check(c.run(max_queries=most, window=77), window=77)
