@@ -370,7 +370,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
 // two loads' latency for few.  G waves have a row (4 / G rows a workgroup), lane p part p's
 // maximum and sum (64 parts at most), every lane 2 (of 256: 4) of the outputs.  Their loads do
 // not wait for the statistics: what an empty part's place holds is loaded and not taken.
-// 16000 rows of 4 parts: 22 us with a workgroup a row and loads behind the statistics.
+// 16000 rows of 4 parts of 128: 10 us, 37 MB (22 with a workgroup a row and loads behind the
+// statistics); 32 rows of 32 parts: 4.5 (7.6).
 template <int D, int G>
 __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
   constexpr int V = D == 256 ? 4 : 2, PER = 64 * V / D, AHEAD = 4;   // outputs of a lane; parts that a wave's lanes take at a time
