@@ -386,3 +386,24 @@ def test_between_few_and_many_rows(d, page, heads, kv_heads, most):
     c = Case(lengths, queries, heads, kv_heads, d, page, seed=most + d)
     c.check(c.run(max_queries=most))
     c.check(c.run(max_queries=most, window=77), window=77)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("queries", [1, 5, 40])
+@pytest.mark.parametrize("longest", [1100, 2000, 4000])
+def test_few_parts(d, queries, longest):
+    """Two to eight parts, which one wave of a row joins; rows in front of the sequences and behind them stay."""
+    torch, kvcache = _kv()
+    runs = [queries, 1, queries, 2, 1]
+    log("D=%d queries=%d longest=%d" % (d, queries, longest))
+    c = Case([longest, 7, longest - 600, 0, 530], runs, 6, 2, d, 16, seed=longest + queries)
+    t, width = sum(runs), c.table.shape[1]
+    size = kvcache.kv_attention_workspace_bytes(t + 8, 6, 2, d, 5, width, 16, 1, queries, 0)
+    assert 2 <= size // ((t + 8) * 6 * (d + 2) * 4) <= 8
+    first = c.run(max_queries=queries)
+    c.check(first)
+    c.check(c.run(max_queries=queries, window=900), window=900)
+    q = torch.cat((c.q[:3], c.q, c.q[:1].expand(5, -1, -1)))
+    out = torch.full((t + 8, 6, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    kvcache.attention(q, c.cache, c.table, c.i32(c.lengths), c.i32([3 + x for x in c.offsets]), max_queries=queries, out=out)
+    assert torch.equal(out[3:3 + t], first[0]) and bool((out[:3] == 7).all()) and bool((out[3 + t:] == 7).all())
