@@ -96,8 +96,9 @@ mxfp8_status kv_read(const uint8_t *cache, int64_t pages, int32_t page_size, int
  * lengths[b] keys: query x (0 .. n - 1) is at position lengths[b] - n + x and sees
  * the keys j at and before it, with window > 0 only the last `window` of them.
  * Key j of b is token j % page_size of page table[b][j / page_size]; keys of a
- * page number outside [0, pages) and beyond table_width pages are not there.  A
- * query that sees no key gets zeros.
+ * page number outside [0, pages) and beyond table_width pages are not there: a
+ * length past the table moves no query, and a query whose keys all lie behind the
+ * table sees none.  A query that sees no key gets zeros.
  * Head h of q uses head h / (heads / kv_heads) of the cache.
  *
  * q        BF16 [tokens][heads][head_dim] with strides q_token, q_head in

@@ -103,17 +103,18 @@ __device__ __forceinline__ bool find_tile(const Args& a, int t, Tile* tile) {
     }
   }
   tile->rows = tile->queries * a.group - tile->row0;
-  int length = __builtin_amdgcn_readfirstlane(a.lengths[tile->sequence]);
-  length = length < 0 ? 0 : length > a.keys_most ? a.keys_most : length;
-  tile->length = length;
+  const int length = __builtin_amdgcn_readfirstlane(a.lengths[tile->sequence]);
+  tile->length = length < 0 ? 0 : length;
   return true;
 }
 
-// Keys [lo, hi) that query x of a tile's sequence sees (lo < hi, or both 0).
+// Keys [lo, hi) that query x of a tile's sequence sees, none where lo >= hi: those up to its
+// place, which the sequence's length alone gives, as far as the table has them.  Both rise
+// with x (hi may be negative, lo is not).
 __device__ __forceinline__ void seen(const Args& a, const Tile& t, int x, int* lo, int* hi) {
-  const int at = t.length - t.queries + x;
-  *hi = at < 0 ? 0 : at + 1;
-  *lo = a.window > 0 && *hi > a.window ? *hi - a.window : 0;
+  const int behind = t.length - t.queries + x + 1;
+  *hi = behind < a.keys_most ? behind : a.keys_most;
+  *lo = a.window > 0 && behind > a.window ? behind - a.window : 0;
 }
 
 // A page's record of a head.

@@ -117,8 +117,8 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   int first_lo, first_hi, last_lo, last_hi;
   seen(a, t, t.row0 / a.group, &first_lo, &first_hi);
   seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
-  const int begin = first_lo & ~31, end = last_hi;
-  const int steps = (end - begin + 31) / 32;
+  const int end = last_hi, begin = first_lo < end ? first_lo & ~31 : 0;   // (behind the table first_lo may be near 2^31)
+  const int steps = first_lo < end ? (end - begin + 31) / 32 : 0;
   int each = (steps + a.parts - 1) / a.parts;
   each = each < a.least ? a.least : each;
   each = (each + WAVES - 1) / WAVES * WAVES;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   Keys<D> ring[DEPTH];
   Pages pages;
   const int stride = 32 * WAVES, first = begin + 32 * (s0 + w), last = s0 < s1 ? begin + 32 * s1 : 0;
-  if (end > 0) {
+  if (steps > 0) {
     pages.find(a, t, first, end);
 #pragma unroll
     for (int u = 0; u < DEPTH; u++) {
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
     for (int d = 0; d < DT; d++) o[n][d] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  // what every query of the tile sees
+  // what every query of the tile sees: nothing where one sees none, whose lo is no less than its hi
   const int full_lo = last_lo, full_hi = first_hi;
   auto step = [&](Keys<D>& now, const int key) {
     // values of places that no query sees are taken as zeros, whatever they hold

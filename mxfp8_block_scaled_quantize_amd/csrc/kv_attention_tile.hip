@@ -187,8 +187,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
   int first_lo, first_hi, last_lo, last_hi;
   seen(a, t, t.row0 / a.group, &first_lo, &first_hi);
   seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
-  const int begin = first_lo & ~(KEYS - 1), end = last_hi;
-  const int steps = (end - begin + KEYS - 1) / KEYS;
+  const int end = last_hi, begin = first_lo < end ? first_lo & ~(KEYS - 1) : 0;
+  const int steps = first_lo < end ? (end - begin + KEYS - 1) / KEYS : 0;
   int each = (steps + a.parts - 1) / a.parts;
   each = each < a.least / 2 ? a.least / 2 : each;
   const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
@@ -312,7 +312,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
             for (int j = 0; j < 16; j++)
               if (!runs.there(a, 2 * i + (j >> 3))) y[i][j] = -INFINITY;
         }
-        const uint32_t from = (uint32_t)(key + 4 * h - lo), span = (uint32_t)(hi - lo);
+        const uint32_t from = (uint32_t)(key + 4 * h - lo), span = (uint32_t)max(hi - lo, 0);
 #pragma unroll
         for (int i = 0; i < 2; i++)
 #pragma unroll

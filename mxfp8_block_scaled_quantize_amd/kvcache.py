@@ -176,8 +176,9 @@ def attention(q, cache, table, lengths, offsets=None, scale=None, window=0, max_
     """softmax(scale q k^T) v in BF16 [T, heads, head_dim] for q (BF16, unit stride
     along the head) over the keys that table (int32 [B, W]) and lengths (int32 [B])
     give each sequence.  The queries of sequence b, rows offsets[b] .. offsets[b + 1] -
-    1 (int32 [B + 1]; None: one each), stand at the end of its keys: each sees the keys
-    up to its own, with window > 0 the last ``window`` of them.  heads is a multiple of
+    1 (int32 [B + 1]; None: one each), stand at the end of its lengths[b] keys: each sees
+    the keys up to its own, with window > 0 the last ``window`` of them; keys that the
+    table does not hold are not there, also behind its last page.  heads is a multiple of
     the cache's, whose head h serves heads h * group .. + group - 1.  scale: head_dim **
     -0.5 unless given.  max_queries: the longest run of queries, where the program
     knows it (a decoding step of several sequences is then not taken for a prompt); it
