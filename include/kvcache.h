@@ -115,8 +115,8 @@ mxfp8_status kv_read(const uint8_t *cache, int64_t pages, int32_t page_size, int
  *          overlaps an input.
  * lse      fp32 [tokens][heads] or NULL: log sum_j exp(scale <q, k_j>), -inf for
  *          a query that sees no key.
- * workspace  kv_attention_workspace_bytes(...) of the same sizes, 16-byte
- *          aligned (NULL where that is 0); not kept.
+ * workspace  kv_attention_workspace_bytes(...) of the same sizes, at most 80 MiB,
+ *          16-byte aligned (NULL where that is 0); not kept.
  *
  * Keys meet the queries in 32 bits: a query is taken apart into two E4M3 parts
  * that hold all of its bits down to 2^-21 of its largest value.  The softmax's

@@ -2,9 +2,11 @@
 //
 // Rows.  The queries of a sequence and the heads that share a key-value head are
 // rows of one product: row = query * group + head of the group.  A tile is some
-// rows of one sequence and key-value head; its keys are cut into parts, each for a
+// rows of one sequence and key-value head; its keys may be cut into parts, each for a
 // workgroup, whose sums meet in the workspace (`sums`) and are joined by
-// kv_join_kernel.
+// kv_join_kernel.  A launch has as many places for parts as the table's width may
+// want; how many a tile really has is settled on the device, by its keys: a tile of one
+// writes its outputs at once, and a workgroup without a part does nothing.
 //
 // Scores.  S^T = K Q^T on the scaled matrix instructions: the keys' codes go from
 // the cache into the FP4 operand as they are, 32 codes and a scale byte a lane.  The
@@ -51,9 +53,43 @@ struct Args {
   uint16_t* __restrict__ out;
   float* __restrict__ lse;
   float* __restrict__ sums;   // O [parts][rows][D], then (m, l) [parts][rows][2]; null: one part
-  int32_t tokens, heads, kv_heads, group, sequences, pages, page_shift, keys_most, window, parts;
-  int32_t least;              // steps of 32 keys of a part, at least
+  int32_t* __restrict__ used; // [rows], behind them: the parts that a row has (one: its outputs are written)
+  int32_t tokens, heads, kv_heads, group, sequences, pages, page_shift, keys_most, window;
+  int32_t tiles, likely;      // of the launch: as any offsets may need, as runs of max_queries have
+  int32_t parts, fill;        // places for parts; parts that give the chip enough workgroups
   float scale2;               // scale * log2(e)
+};
+
+// Keys of a part: at least (a second launch joins the parts, about 3 us, in which a
+// workgroup goes through 1000 keys), and at most where there are tiles enough (parts then
+// bound what one very long sequence among them takes: 16384 keys are 70 us).
+constexpr int LEAST_KEYS = 512, MOST_KEYS = 16384;
+
+// Steps (of STEP keys) of a part of a tile that has `steps` > 0: as many as make `fill`
+// parts, between the two bounds, or as `parts` places need.
+template <int STEP>
+__device__ __forceinline__ int part_steps(const Args& a, int steps) {
+  if (!a.sums) return steps;
+  const int even = (steps + a.fill - 1) / a.fill, room = (steps + a.parts - 1) / a.parts;
+  return max(min(max(even, LEAST_KEYS / STEP), MOST_KEYS / STEP), room);
+}
+
+// The workgroup's head, tile and part.  The hardware deals workgroups out in turn, those that
+// have nothing to do like the others, so that they must not stand between those with work: parts
+// are the slowest (the places behind a tile's last part come at the end), and tiles past the
+// likely number come behind all parts of the likely ones.
+struct Place {
+  int head, tile, part;
+  __device__ __forceinline__ explicit Place(const Args& a) {
+    unsigned rest = blockIdx.x / (unsigned)a.kv_heads;
+    head = (int)(blockIdx.x % (unsigned)a.kv_heads);
+    const unsigned inside = (unsigned)a.likely * (unsigned)a.parts;
+    const bool first = rest < inside;
+    rest = first ? rest : rest - inside;
+    const unsigned run = first ? (unsigned)a.likely : (unsigned)(a.tiles - a.likely);   // not 0: the grid has it
+    part = (int)(rest / run);
+    tile = (int)(rest % run) + (first ? 0 : a.likely);
+  }
 };
 
 struct Tile {
@@ -185,8 +221,7 @@ inline int64_t kv_tiles(const KvAttention& a, int64_t tm) {
   const int64_t with = a.sequences < a.tokens ? a.sequences : a.tokens;
   return (a.tokens * group + with * (tm - 1)) / tm;
 }
-kv::Args kv_args(const KvAttention& a, int64_t parts);
 // rows: 64 or 128 a workgroup.
-hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t rows, int64_t parts, hipStream_t stream);
+hipError_t launch_kv_attention_tile(const KvCache& c, const kv::Args& g, int64_t rows, dim3 grid, hipStream_t stream);
 
 }  // namespace mx

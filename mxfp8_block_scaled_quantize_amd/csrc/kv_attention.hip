@@ -105,11 +105,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   __shared__ float stats[WAVES][16][2];
   const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int head = (int)(blockIdx.x % (unsigned)a.kv_heads);
-  const int rest = (int)(blockIdx.x / (unsigned)a.kv_heads);
-  const int part = rest % a.parts;
+  const Place place(a);
+  const int head = place.head, part = place.part;
   Tile t;
-  if (!find_tile<TM>(a, rest / a.parts, &t)) return;   // the whole workgroup
+  if (!find_tile<TM>(a, place.tile, &t)) return;   // the whole workgroup
   const int rows = t.rows < TM ? t.rows : TM;
   const int64_t all_rows = (int64_t)a.tokens * a.heads;
 
@@ -119,9 +118,10 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
   const int end = last_hi, begin = first_lo < end ? first_lo & ~31 : 0;   // (behind the table first_lo may be near 2^31)
   const int steps = first_lo < end ? (end - begin + 31) / 32 : 0;
-  int each = (steps + a.parts - 1) / a.parts;
-  each = each < a.least ? a.least : each;
-  each = (each + WAVES - 1) / WAVES * WAVES;
+  const int each = steps ? (part_steps<32>(a, steps) + WAVES - 1) / WAVES * WAVES : 1;
+  const int used = (steps + each - 1) / each;
+  if (part > 0 && part >= used) return;
+  const bool whole = used <= 1;   // the outputs are written here
   const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
 
   // the lane's rows: column c of each block
@@ -334,18 +334,19 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
           total += stats[u][c][1] * part_of[u];
         }
         const bool some = total > 0.0f || total != total;
-        if (!a.sums) factor = some ? 1.0f / total : 0.0f;
+        if (whole) factor = some ? 1.0f / total : 0.0f;
         if (valid && w == 0 && g == 0) {
-          if (a.sums) {
+          if (!whole) {
             float* ml = a.sums + a.parts * all_rows * D + (part * all_rows + row) * 2;
             ml[0] = all;
             ml[1] = total;
           } else if (a.lse) {
             a.lse[row] = some ? (all + __builtin_amdgcn_logf(total)) * kLn2 : -INFINITY;
           }
+          if (a.sums && part == 0) a.used[row] = used;
         }
       }
-      if (valid && !(a.sums && s0 >= s1)) {   // an empty part has nothing but its statistics
+      if (valid) {
 #pragma unroll
         for (int q = 0; q < CH / 4; q++) {
           float r[4];
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
           }
           const int m = 4 * g + w;   // row of the blocks: (eight values, or half of them)
           const int to = D == 64 ? 8 * (m & 7) + 4 * (m >> 3) : 16 * d0 + 8 * m + 4 * q;
-          if (a.sums) *reinterpret_cast<v4f*>(a.sums + (part * all_rows + row) * D + to) = v4f{r[0], r[1], r[2], r[3]};
+          if (!whole) *reinterpret_cast<v4f*>(a.sums + (part * all_rows + row) * D + to) = v4f{r[0], r[1], r[2], r[3]};
           else *reinterpret_cast<u32x2*>(a.out + row * D + to) = u32x2{bf16_pair(r[0], r[1]), bf16_pair(r[2], r[3])};
         }
       }
@@ -367,11 +368,9 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
 }
 
 // ---- joining the parts of a row: bound by the stream of the parts' sums for many rows, by
-// two loads' latency for few.  G waves have a row (4 / G rows a workgroup), lane p part p's
-// maximum and sum (64 parts at most), every lane 2 (of 256: 4) of the outputs.  Their loads do
-// not wait for the statistics: what an empty part's place holds is loaded and not taken.
-// 16000 rows of 4 parts of 128: 10 us, 37 MB (22 with a workgroup a row and loads behind the
-// statistics); 32 rows of 32 parts: 4.5 (7.6).
+// three loads' latency for few.  G waves have a row (4 / G rows a workgroup), lane p part p's
+// maximum and sum (64 parts at most), every lane 2 (of 256: 4) of the outputs.  What the
+// places behind a row's parts hold is not loaded, but for the statistics, which are not taken.
 template <int D, int G>
 __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
   constexpr int V = D == 256 ? 4 : 2, PER = 64 * V / D, AHEAD = 4;   // outputs of a lane; parts that a wave's lanes take at a time
@@ -389,36 +388,39 @@ __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
       if (!__any(token < end)) return;   // the same for all waves of the row
     }
   }
+  const f32x2* const ml = reinterpret_cast<const f32x2*>(a.sums + a.parts * all_rows * D) + row;
+  f32x2 stat = {-INFINITY, 0.0f};
+  if (lane < a.parts) stat = ml[lane * all_rows];
+  const int used = __builtin_amdgcn_readfirstlane(a.used[row]);   // the row's, in all lanes
+  if (used <= 1) return;
   const int at = (lane & (D / V - 1)) * V, mine = lane / (D / V), step = G * PER;
   const float* const o = a.sums + row * D + at;
   auto load = [&](vec* x, int p0) {
 #pragma unroll
-    for (int u = 0; u < AHEAD; u++) x[u] = *reinterpret_cast<const vec*>(o + min(p0 + u * step + mine, a.parts - 1) * all_rows * D);
+    for (int u = 0; u < AHEAD; u++) x[u] = *reinterpret_cast<const vec*>(o + min(p0 + u * step + mine, used - 1) * all_rows * D);
   };
   vec x[AHEAD], r;
   const int first = (G == 1 ? 0 : w) * PER;
   load(x, first);
-  const f32x2* const ml = reinterpret_cast<const f32x2*>(a.sums + a.parts * all_rows * D) + row;
-  f32x2 stat = {-INFINITY, 0.0f};
-  if (lane < a.parts) stat = ml[lane * all_rows];
+  if (lane >= used) stat = f32x2{-INFINITY, 0.0f};
   float all = stat.x;
 #pragma unroll
   for (int i = 32; i; i >>= 1) all = fmaxf(all, __shfl_xor(all, i, 64));
   const float base = all > -INFINITY ? all : 0.0f;
-  // a part without a key has no outputs, not even zeros: -1
+  // a part that the row sees nothing of is not taken: -1
   const float f = stat.y == 0.0f ? -1.0f : __builtin_amdgcn_exp2f(stat.x - base);
   float total = stat.y == 0.0f ? 0.0f : stat.y * f;
 #pragma unroll
   for (int i = 32; i; i >>= 1) total += __shfl_xor(total, i, 64);
 #pragma unroll
   for (int i = 0; i < V; i++) r[i] = 0.0f;
-  for (int p0 = first; p0 < a.parts; p0 += AHEAD * step) {
+  for (int p0 = first; p0 < used; p0 += AHEAD * step) {
     if (p0 > first) load(x, p0);
 #pragma unroll
     for (int u = 0; u < AHEAD; u++) {
       const int p = p0 + u * step + mine;
-      const float fp = __shfl(f, p < a.parts ? p : 0, 64);
-      const bool take = p < a.parts && !(fp < 0.0f);   // NaN too
+      const float fp = __shfl(f, p < used ? p : 0, 64);
+      const bool take = p < used && !(fp < 0.0f);   // NaN too
 #pragma unroll
       for (int i = 0; i < V; i++) r[i] = take ? fmaf(fp, x[u][i], r[i]) : r[i];
     }
@@ -444,31 +446,26 @@ __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
 
 int64_t group_of(const KvAttention& a) { return a.heads / a.cache.heads; }
 
-// Parts that the keys of a tile are cut into: as many as give every compute unit a
-// workgroup (of the kernel for many queries as many as it holds), of at least 512 keys.  A
-// second launch joins them, about 3 us, in which a workgroup goes through 1000 keys: one
-// token of a sequence of 131071 keys, 8 heads: 29.6 us with 32 parts, 30.0 with 64, 44.5 with
-// 16; of 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of up to 8192: 68.0 us with 1
-// part, 68.5 with 2, 69.5 with 4; 500 queries over 49152 keys: 356 with 4, 434 with 3, 364
-// with 8.  Where there are tiles enough, parts bound what one very long sequence among them
-// takes: 16384 keys are 70 us.
-constexpr int64_t LEAST_KEYS = 512, MOST_KEYS = 16384, MOST_PARTS = 64;   // parts: a lane each in kv_join_kernel
+// Places for parts, a lane each in kv_join_kernel, and bytes of their sums: 512 tiles of 128
+// rows of 256 values, which fill the chip, take 68 MB.  Workgroups for places that nothing but
+// the table's width asks for: 64 sequences of up to 8192 tokens in a table of 2^20 take 66 us
+// with one place, 68 with 8, 84 with 64.
+constexpr int64_t MOST_PARTS = 64, MOST_BYTES = 80ll << 20, MOST_BLOCKS = 8192;
 
 // Keys that a tile can see.
 int64_t keys_of(const KvAttention& a) {
   const int64_t keys = a.table_width * a.cache.page_size;
   return a.window > 0 && a.window + a.max_queries < keys ? a.window + a.max_queries : keys;
 }
-// Tiles of tm rows times heads: as many as runs of max_queries have, if that is less than
-// what any offsets can give.
-int64_t blocks_of(const KvAttention& a, int64_t tm) {
-  int64_t tiles = kv_tiles(a, tm);
-  if (a.offsets && a.max_queries < 65536) {
-    const int64_t likely = a.sequences * ((a.max_queries * group_of(a) + tm - 1) / tm);
-    tiles = tiles < likely ? tiles : likely;
-  }
-  return tiles * a.cache.heads;
+// Tiles of tm rows: as many as runs of max_queries have, if that is less than what any offsets
+// can give; and those times heads.
+int64_t likely_tiles(const KvAttention& a, int64_t tm) {
+  const int64_t tiles = kv_tiles(a, tm);
+  if (!a.offsets || a.max_queries >= 65536) return tiles;
+  const int64_t likely = a.sequences * ((a.max_queries * group_of(a) + tm - 1) / tm);
+  return tiles < likely ? tiles : likely;
 }
+int64_t blocks_of(const KvAttention& a, int64_t tm) { return likely_tiles(a, tm) * a.cache.heads; }
 // Rows of a tile: 16 or 32 for a run of queries that fits, else 128, or 64 (the kernel for
 // many queries).  64 rows leave no wave idle where a run has no more, but two waves then do
 // what four do for the values: of 256 values, where registers leave a SIMD one wave, it is
@@ -484,42 +481,56 @@ int64_t rows_of(const KvAttention& a) {
   return a.cache.head_dim == 256 || blocks_of(a, 64) * (most < MOST_PARTS ? most : MOST_PARTS) >= FILL_64 ? 64 : 128;
 }
 
-int64_t parts_of(const KvAttention& a) {
-  const int64_t tm = rows_of(a), blocks = blocks_of(a, tm), keys = keys_of(a);
+// Of a tile's keys: the parts that give every compute unit a workgroup (of the kernel for
+// many queries as many as it holds), and the places that the table's width may want for them,
+// as far as their sums and the grid have room.  How many a tile really has is settled on the
+// device (part_steps).  One token of a sequence of 131071 keys, 8 heads: 29.6 us with 32
+// parts, 30.0 with 64, 44.5 with 16; of 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of
+// up to 8192: 68.0 us with 1 part, 68.5 with 2, 69.5 with 4; 500 queries over 49152 keys: 356
+// with 4, 434 with 3, 364 with 8.
+struct Parts {
+  int64_t fill, places;
+};
+Parts parts_of(const KvAttention& a) {
+  const int64_t tm = rows_of(a), blocks = blocks_of(a, tm), keys = keys_of(a), rows = a.tokens * a.heads;
   const int64_t wanted = tm < 64 ? 256 : tm == 64 && a.cache.head_dim < 256 ? FILL_64 : 512;
-  const int64_t fill = wanted / (blocks > 0 ? blocks : 1), bound = (keys + MOST_KEYS - 1) / MOST_KEYS;
-  int64_t parts = fill > bound ? fill : bound;
-  const int64_t most = keys / LEAST_KEYS;
-  parts = parts < most ? parts : most;
-  return parts < 1 ? 1 : parts > MOST_PARTS ? MOST_PARTS : parts;
+  const auto least = [](int64_t x, int64_t y) { return x < y ? x : y; };
+  const int64_t most = least(keys / LEAST_KEYS, MOST_PARTS);
+  Parts p{least(wanted / (blocks > 0 ? blocks : 1), most), least((keys + MOST_KEYS - 1) / MOST_KEYS, most)};
+  p.fill = p.fill < 1 ? 1 : p.fill;
+  if (blocks > 0) p.places = least(p.places, MOST_BLOCKS / blocks);
+  p.places = p.fill > p.places ? p.fill : p.places;
+  if (rows > 0) p.places = least(p.places, (MOST_BYTES / rows / 4 - 1) / (a.cache.head_dim + 2));
+  const int64_t tiles = kv_tiles(a, tm) * a.cache.heads;
+  if (tiles > 0) p.places = least(p.places, kMaxWorkItems / (64 * WAVES) / tiles);
+  p.places = p.places < 1 ? 1 : p.places;
+  return p;
 }
 
 template <int D>
-hipError_t launch_all(const KvAttention& a, int64_t parts, hipStream_t stream) {
-  const Args g = kv_args(a, parts);
+hipError_t launch_all(const KvAttention& a, const Args& g, hipStream_t stream) {
   const int64_t tm = rows_of(a);
-  const dim3 grid((unsigned)(kv_tiles(a, tm) * parts * a.cache.heads));
+  const dim3 grid((unsigned)g.tiles * (unsigned)g.parts * (unsigned)a.cache.heads);
   hipError_t e = hipSuccess;
   if (tm >= 64) {
-    e = launch_kv_attention_tile(a, tm, parts, stream);
+    e = launch_kv_attention_tile(a.cache, g, tm, grid, stream);
   } else {
     if (tm == 16) hipLaunchKernelGGL((kv_attention_rows_kernel<D, 1>), grid, dim3(64 * WAVES), 0, stream, g);
     else hipLaunchKernelGGL((kv_attention_rows_kernel<D, 2>), grid, dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
   }
-  if (e == hipSuccess && parts > 1) {
-    // four waves a row where one would go through the parts in more than two rounds
+  if (e == hipSuccess && g.parts > 1) {
+    // four waves a row where one would go through the parts in more than two rounds; the rows
+    // that MOST_BYTES has room for fit a grid in either form
     const int64_t rows = a.tokens * a.heads;
-    if (parts <= 8) hipLaunchKernelGGL((kv_join_kernel<D, 1>), dim3((unsigned)((rows + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, g);
+    if (g.parts <= 8) hipLaunchKernelGGL((kv_join_kernel<D, 1>), dim3((unsigned)((rows + WAVES - 1) / WAVES)), dim3(64 * WAVES), 0, stream, g);
     else hipLaunchKernelGGL((kv_join_kernel<D, WAVES>), dim3((unsigned)rows), dim3(64 * WAVES), 0, stream, g);
     e = hipGetLastError();
   }
   return e;
 }
 
-}  // namespace
-
-kv::Args kv_args(const KvAttention& a, int64_t parts) {
+kv::Args kv_args(const KvAttention& a, Parts parts) {
   kv::Args g{};
   g.q = a.q;
   g.q_token = a.q_token;
@@ -533,7 +544,10 @@ kv::Args kv_args(const KvAttention& a, int64_t parts) {
   g.offsets = a.offsets;
   g.out = a.out;
   g.lse = a.lse;
-  g.sums = parts > 1 ? a.workspace : nullptr;
+  if (parts.places > 1) {
+    g.sums = a.workspace;
+    g.used = reinterpret_cast<int32_t*>(a.workspace + parts.places * a.tokens * a.heads * (a.cache.head_dim + 2));
+  }
   g.tokens = (int32_t)a.tokens;
   g.heads = a.heads;
   g.kv_heads = a.cache.heads;
@@ -543,28 +557,30 @@ kv::Args kv_args(const KvAttention& a, int64_t parts) {
   g.page_shift = a.cache.page_shift;
   g.keys_most = (int32_t)(a.table_width * a.cache.page_size);
   g.window = (int32_t)a.window;
-  g.parts = (int32_t)parts;
-  g.least = (int32_t)(LEAST_KEYS / 32);
+  g.tiles = (int32_t)kv_tiles(a, rows_of(a));
+  g.likely = (int32_t)likely_tiles(a, rows_of(a));
+  g.parts = (int32_t)parts.places;
+  g.fill = (int32_t)parts.fill;
   g.scale2 = a.scale * kLog2e;
   return g;
 }
 
+}  // namespace
+
 size_t kv_attention_workspace(const KvAttention& a) {
-  const int64_t parts = parts_of(a);
-  return parts > 1 ? (size_t)parts * (size_t)a.tokens * (size_t)a.heads * (size_t)(a.cache.head_dim + 2) * 4 : 0;
+  const size_t parts = (size_t)parts_of(a).places, rows = (size_t)a.tokens * (size_t)a.heads;
+  return parts > 1 ? rows * (parts * (size_t)(a.cache.head_dim + 2) + 1) * 4 : 0;
 }
 
 bool kv_attention_grid_fits(const KvAttention& a) {
-  const int64_t parts = parts_of(a);
-  return grid_fits(kv_tiles(a, rows_of(a)) * parts, a.cache.heads, 64 * WAVES) &&
-         (parts == 1 || grid_fits(a.tokens, a.heads, 64 * WAVES));
+  return grid_fits(kv_tiles(a, rows_of(a)), a.cache.heads, 64 * WAVES);
 }
 
 hipError_t launch_kv_attention(const KvAttention& a, hipStream_t stream) {
-  const int64_t parts = parts_of(a);
-  if (a.cache.head_dim == 64) return launch_all<64>(a, parts, stream);
-  if (a.cache.head_dim == 128) return launch_all<128>(a, parts, stream);
-  return launch_all<256>(a, parts, stream);
+  const Args g = kv_args(a, parts_of(a));
+  if (a.cache.head_dim == 64) return launch_all<64>(a, g, stream);
+  if (a.cache.head_dim == 128) return launch_all<128>(a, g, stream);
+  return launch_all<256>(a, g, stream);
 }
 
 }  // namespace mx

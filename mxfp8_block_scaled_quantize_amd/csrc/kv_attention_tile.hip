@@ -169,18 +169,17 @@ struct ValuePart {
 };
 
 template <int D, bool WHOLE, int W>
-__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a, int tiles) {
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_kernel(Args a) {
   constexpr int KS = KeyPart<D>::KS;
   __shared__ __attribute__((aligned(16))) uint8_t values[2][D * ROW];
   lds_u8* const lds = (lds_u8*)&values[0][0];
   const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const int head = (int)(blockIdx.x % (unsigned)a.kv_heads);
-  const int rest = (int)(blockIdx.x / (unsigned)a.kv_heads);
-  const int part = rest % a.parts;
+  const Place place(a);
+  const int head = place.head, part = place.part;
   Tile t;
   // the last tiles of a sequence, which see the most keys, first
-  if (!find_tile<32 * W>(a, tiles - 1 - rest / a.parts, &t)) return;   // the whole workgroup
+  if (!find_tile<32 * W>(a, place.tile < a.likely ? a.likely - 1 - place.tile : place.tile, &t)) return;   // the whole workgroup
   const int rows = t.rows < 32 * W ? t.rows : 32 * W;
   const int64_t all_rows = (int64_t)a.tokens * a.heads;
 
@@ -189,13 +188,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
   seen(a, t, (t.row0 + rows - 1) / a.group, &last_lo, &last_hi);
   const int end = last_hi, begin = first_lo < end ? first_lo & ~(KEYS - 1) : 0;
   const int steps = first_lo < end ? (end - begin + KEYS - 1) / KEYS : 0;
-  int each = (steps + a.parts - 1) / a.parts;
-  each = each < a.least / 2 ? a.least / 2 : each;
+  const int each = steps ? __builtin_amdgcn_readfirstlane(part_steps<KEYS>(a, steps)) : 1;
+  const int used = __builtin_amdgcn_readfirstlane((steps + each - 1) / each);
+  const bool whole = used <= 1;   // the outputs are written here
   const int s0 = part * each, s1 = s0 + each < steps ? s0 + each : steps;
 
   // this lane's row, and the keys of the wave's rows
+  // (a workgroup without a part has none: a return here would cost the kernel 7 to 14 registers)
   const int row = 32 * w + c;
-  const bool valid = row < rows;
+  const bool valid = row < rows && (part == 0 || part < used);
   const int x = (t.row0 + (valid ? row : 0)) / a.group;
   const int64_t token = t.first_token + x;
   const int q_head = head * a.group + (t.row0 + (valid ? row : 0)) - x * a.group;
@@ -371,13 +372,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
   if (!valid) return;
   const int64_t at = token * a.heads + q_head;
   const bool some = sum > 0.0f || sum != sum;
-  if (a.sums) {
+  if (a.sums && part == 0 && h == 0) a.used[at] = used;
+  if (!whole) {
     if (h == 0) {
       float* ml = a.sums + a.parts * all_rows * D + (part * all_rows + at) * 2;
       ml[0] = top;
       ml[1] = sum;
     }
-    if (s0 >= s1) return;
     float* to = a.sums + (part * all_rows + at) * D;
 #pragma unroll
     for (int d = 0; d < D / 32; d++)
@@ -398,25 +399,22 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
 }
 
 template <int D, int W>
-void launch(const KvAttention& a, const Args& g, int64_t parts, hipStream_t stream) {
-  const int64_t tiles = kv_tiles(a, 32 * W);
-  const dim3 grid((unsigned)(tiles * parts * a.cache.heads));
-  if (a.cache.page_size >= 32) hipLaunchKernelGGL((kv_attention_tile_kernel<D, true, W>), grid, dim3(64 * W), 0, stream, g, (int)tiles);
-  else hipLaunchKernelGGL((kv_attention_tile_kernel<D, false, W>), grid, dim3(64 * W), 0, stream, g, (int)tiles);
+void launch(const KvCache& c, const Args& g, dim3 grid, hipStream_t stream) {
+  if (c.page_size >= 32) hipLaunchKernelGGL((kv_attention_tile_kernel<D, true, W>), grid, dim3(64 * W), 0, stream, g);
+  else hipLaunchKernelGGL((kv_attention_tile_kernel<D, false, W>), grid, dim3(64 * W), 0, stream, g);
 }
 template <int D>
-void launch(const KvAttention& a, const Args& g, int64_t rows, int64_t parts, hipStream_t stream) {
-  if (rows == 64) launch<D, 2>(a, g, parts, stream);
-  else launch<D, 4>(a, g, parts, stream);
+void launch(const KvCache& c, const Args& g, int64_t rows, dim3 grid, hipStream_t stream) {
+  if (rows == 64) launch<D, 2>(c, g, grid, stream);
+  else launch<D, 4>(c, g, grid, stream);
 }
 
 }  // namespace
 
-hipError_t launch_kv_attention_tile(const KvAttention& a, int64_t rows, int64_t parts, hipStream_t stream) {
-  const kv::Args g = kv_args(a, parts);
-  if (a.cache.head_dim == 64) launch<64>(a, g, rows, parts, stream);
-  else if (a.cache.head_dim == 128) launch<128>(a, g, rows, parts, stream);
-  else launch<256>(a, g, rows, parts, stream);
+hipError_t launch_kv_attention_tile(const KvCache& c, const kv::Args& g, int64_t rows, dim3 grid, hipStream_t stream) {
+  if (c.head_dim == 64) launch<64>(c, g, rows, grid, stream);
+  else if (c.head_dim == 128) launch<128>(c, g, rows, grid, stream);
+  else launch<256>(c, g, rows, grid, stream);
   return hipGetLastError();
 }
 
