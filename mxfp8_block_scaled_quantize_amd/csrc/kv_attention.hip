@@ -207,15 +207,16 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
   // what every query of the tile sees: nothing where one sees none, whose lo is no less than its hi
   const int full_lo = last_lo, full_hi = first_hi;
   auto step = [&](Keys<D>& now, const int key) {
-    // values of places that no query sees are taken as zeros, whatever they hold
-    if (key + 32 > end) {
+    // values of places that no query of the tile sees, in front of its first one's window or
+    // behind its last one, are taken as zeros, whatever they hold
+    if (key < first_lo || key + 32 > end) {
 #pragma unroll
       for (int i = 0; i < 2; i++)
 #pragma unroll
         for (int b = 0; b < KB; b++)
 #pragma unroll
           for (int j = 0; j < 4; j++)
-            if (key + 16 * i + 4 * g + j >= end) {
+            if (key + 16 * i + 4 * g + j < first_lo || key + 16 * i + 4 * g + j >= end) {
               now.v[i][b][j] = 0;
               now.vs[i][b] &= ~(0xFFu << (8 * j));
             }

@@ -135,15 +135,16 @@ struct ValuePart {
       s[u] = __builtin_amdgcn_raw_buffer_load_b32(r, (eight() >> 2) * page_size + 4 * quad(u), page_size * (D + D / 32) + at, 0);
     }
   }
-  // Of places that no query sees, zeros.
-  __device__ __forceinline__ void mask(const Args& a, uint32_t page, int key, int end, int w) {
+  // Of places that no query of the tile sees, zeros: [lo, end) are the keys of some.
+  __device__ __forceinline__ void mask(const Args& a, uint32_t page, int key, int lo, int end, int w) {
     const bool there = page < (uint32_t)a.pages;
-    if (key + 16 * w + 16 <= end && there) return;
+    const int at = key + 16 * w;
+    if (at >= lo && at + 16 <= end && there) return;
 #pragma unroll
     for (int u = 0; u < UNITS; u++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        if (!there || key + 16 * w + 4 * (int)quad(u) + j >= end) {
+        if (!there || at + 4 * (int)quad(u) + j < lo || at + 4 * (int)quad(u) + j >= end) {
           v[u][j] = 0;
           s[u] &= ~(0xFFu << (8 * j));
         }
@@ -256,7 +257,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
   };
   auto mask_values = [&](const Runs<WHOLE, R>& of, int key) {
 #pragma unroll
-    for (int j = 0; j < R; j++) vals[j].mask(a, of.own[j], key, end, R * w + j);
+    for (int j = 0; j < R; j++) vals[j].mask(a, of.own[j], key, first_lo, end, R * w + j);
   };
   auto store_values = [&](lds_u8* to) {
 #pragma unroll
