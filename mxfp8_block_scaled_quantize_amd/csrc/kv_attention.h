@@ -182,10 +182,11 @@ __device__ __forceinline__ uint32_t amax8(uint4 v) {
   const uint32_t m = pk_max_u16(pk_max_u16(abs_bits2(v.x), abs_bits2(v.y)), pk_max_u16(abs_bits2(v.z), abs_bits2(v.w)));
   return max(m & 0xFFFFu, m >> 16);
 }
-// Scale byte of `hi` (that of `lo` is 4 less) for a row's amax pattern.
+// Scale byte of `hi` (that of `lo` is 4 less, and not below 0) for a row's amax pattern.  On the
+// least, 2^-123, half of lo's smallest step is 2^-137, and BF16's smallest number 2^-133.
 __device__ __forceinline__ int query_scale(uint32_t amax_bits) {
   const int e = (int)(amax_bits >> 7);
-  return (e < 20 ? 20 : e > 254 ? 254 : e) - 7;
+  return (e < 11 ? 11 : e > 254 ? 254 : e) - 7;
 }
 
 // Codes 2 x and 2 x + 1 of a word as a BF16 pair.
