@@ -167,7 +167,7 @@ __global__ __launch_bounds__(THREADS) void kv_release_kernel(int32_t* __restrict
                                                              int32_t* __restrict__ free_count_out) {
   // One workgroup: how many of a request's entries are page numbers decides where
   // the next ones go, so the entries are looked at in order.
-  __shared__ int befores[CHUNK], helds[CHUNK];
+  __shared__ int befores[CHUNK];
   __shared__ int waves[4];
   const int tid = threadIdx.x;
   int count = free_count[0];
@@ -190,7 +190,6 @@ __global__ __launch_bounds__(THREADS) void kv_release_kernel(int32_t* __restrict
 #pragma unroll
     for (int i = 0; i < EACH; i++) {
       befores[tid * EACH + i] = before;
-      helds[tid * EACH + i] = held[i];
       before = sat_add(before, held[i]);
     }
     __syncthreads();
