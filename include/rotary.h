@@ -36,6 +36,9 @@ extern "C" {
  * q_out, k_out  dense [tokens][heads][head_dim]; may not overlap the inputs.
  * positions int32 [tokens]; turns fp64 [pairs], 8-byte aligned.
  * head_dim >= 1, 0 <= 2 * pairs <= head_dim, head_dim <= 65536.
+ * tokens * (q_heads + k_heads) * head_dim < 2^40, and at most 2^32 - 256 threads,
+ * each of which takes two runs of 16 bytes (two elements where pairs, head_dim, the
+ * strides or the addresses are no multiples of 16 bytes) of up to eight heads.
  * Errors: NULL, SHAPE, MISALIGNED, FLAGS (dtype or flags unknown), LIMIT, HIP.
  */
 mxfp8_status rotary_rotate(const void *q, int64_t q_token, int64_t q_head, int64_t q_heads, const void *k,

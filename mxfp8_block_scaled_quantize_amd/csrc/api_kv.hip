@@ -217,8 +217,11 @@ mxfp8_status rotary_rotate(const void* q, int64_t q_token, int64_t q_head, int64
     return MXFP8_ERR_SHAPE;
   if (head_dim > 65536 || q_heads > (1 << 20) || k_heads > (1 << 20) || !product_ok(tokens, q_token) ||
       !product_ok(tokens, k_token) || !product_ok(q_heads, q_head) || !product_ok(k_heads, k_head) ||
-      !mx::rotary_grid_fits(tokens, q_heads + k_heads, head_dim))
+      !product_ok(tokens, (q_heads + k_heads) * head_dim))
     return MXFP8_ERR_LIMIT;
+  const mx::RotaryCall call{{q, q_out, q_token, q_head, q_heads}, {k, k_out, k_token, k_head, k_heads}, dtype, tokens, head_dim, pairs,
+                            positions, turns, magnitude, (flags & ROTARY_INTERLEAVED) != 0, (flags & ROTARY_INVERSE) != 0};
+  if (tokens > 0 && q_heads + k_heads > 0 && !mx::rotary_grid_fits(call)) return MXFP8_ERR_LIMIT;
   if (tokens == 0 || q_heads + k_heads == 0) return MXFP8_OK;
   if ((q_heads > 0 && (!q || !q_out)) || (k_heads > 0 && (!k || !k_out)) || (pairs > 0 && (!positions || !turns)))
     return MXFP8_ERR_NULL;
@@ -226,9 +229,7 @@ mxfp8_status rotary_rotate(const void* q, int64_t q_token, int64_t q_head, int64
   if (!aligned(q, size) || !aligned(k, size) || !aligned(q_out, size) || !aligned(k_out, size) || !aligned(positions, 4) ||
       !aligned(turns, 8))
     return MXFP8_ERR_MISALIGNED;
-  return hip_status(mx::launch_rotary({q, q_out, q_token, q_head, q_heads}, {k, k_out, k_token, k_head, k_heads}, dtype, tokens,
-                                      head_dim, pairs, positions, turns, magnitude, flags & ROTARY_INTERLEAVED,
-                                      flags & ROTARY_INVERSE, static_cast<hipStream_t>(stream)));
+  return hip_status(mx::launch_rotary(call, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -59,9 +59,16 @@ struct RotaryRows {   // strides in elements
   void* out;
   int64_t token, head, heads;
 };
-bool rotary_grid_fits(int64_t tokens, int64_t heads, int64_t head_dim);
-hipError_t launch_rotary(RotaryRows q, RotaryRows k, int dtype, int64_t tokens, int64_t head_dim, int64_t pairs,
-                         const int32_t* positions, const double* turns, float magnitude, bool interleaved, bool inverse,
-                         hipStream_t stream);
+struct RotaryCall {
+  RotaryRows q, k;
+  int dtype;
+  int64_t tokens, head_dim, pairs;
+  const int32_t* positions;
+  const double* turns;
+  float magnitude;
+  bool interleaved, inverse;
+};
+bool rotary_grid_fits(const RotaryCall& c);
+hipError_t launch_rotary(const RotaryCall& c, hipStream_t stream);
 
 }  // namespace mx

@@ -39,6 +39,7 @@ struct Rotary {
   RotaryRows q, k;
   int64_t tokens;
   int32_t head_dim, pairs, heads, heads_each, parts, turning;   // parts of a token: `turning` of them turn
+  int32_t width;   // elements of a run: 16 bytes, or one
   const int32_t* positions;
   const double* turns;
   float magnitude;
@@ -110,23 +111,32 @@ __global__ __launch_bounds__(256) void rotary_kernel(Rotary r) {
   }
 }
 
-// Runs of V elements start on multiples of V everywhere: 16-byte accesses.
-bool wide(const RotaryRows& x, int64_t v, int64_t size) {
-  return x.heads == 0 || ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) % 16 == 0 &&
-                          x.token % v == 0 && x.head % v == 0 && v * size == 16);
+// Runs of v elements start on multiples of v everywhere: 16-byte accesses.
+bool wide(const RotaryRows& x, int64_t v) {
+  return x.heads == 0 || ((reinterpret_cast<uintptr_t>(x.in) | reinterpret_cast<uintptr_t>(x.out)) % 16 == 0 && x.token % v == 0 &&
+                          x.head % v == 0);
+}
+
+int64_t groups_of(const Rotary& r) { return (r.heads + r.heads_each - 1) / r.heads_each; }
+
+// How a call is cut into threads.
+Rotary plan_of(const RotaryCall& c) {
+  Rotary r{c.q, c.k, c.tokens, (int32_t)c.head_dim, (int32_t)c.pairs, (int32_t)(c.q.heads + c.k.heads), 8, 0, 0, 1, c.positions, c.turns, c.magnitude};
+  const int32_t v = c.dtype == 0 ? 4 : 8;
+  if (c.pairs % v == 0 && c.head_dim % v == 0 && wide(c.q, v) && wide(c.k, v)) r.width = v;
+  r.turning = r.pairs / r.width;
+  const int64_t rest = r.head_dim - 2 * (int64_t)r.pairs;
+  r.parts = (int)(r.turning + (rest + 2 * r.width - 1) / (2 * r.width));
+  // heads of a thread: up to 8, fewer where that would leave less than 8 waves a compute unit
+  // (2^17 tokens and more never do)
+  const int64_t tokens = r.tokens < (1 << 17) ? r.tokens : 1 << 17;
+  while (r.heads_each > 1 && tokens * r.parts * groups_of(r) < 256 * 8 * 64) r.heads_each >>= 1;
+  return r;
 }
 
 template <typename T, int V>
-hipError_t launch(Rotary r, bool interleaved, bool inverse, hipStream_t stream) {
-  r.turning = r.pairs / V;
-  const int64_t rest = r.head_dim - 2 * (int64_t)r.pairs;
-  r.parts = (int)(r.turning + (rest + 2 * V - 1) / (2 * V));
-  // heads of a thread: up to 8, fewer where that would leave less than 8 waves a
-  // compute unit
-  r.heads_each = 8;
-  while (r.heads_each > 1 && r.tokens * r.parts * ((r.heads + r.heads_each - 1) / r.heads_each) < 256 * 8 * 64) r.heads_each >>= 1;
-  const int64_t groups = (r.heads + r.heads_each - 1) / r.heads_each;
-  const dim3 grid((unsigned)((r.tokens * r.parts * groups + 255) / 256));
+hipError_t launch(const Rotary& r, bool interleaved, bool inverse, hipStream_t stream) {
+  const dim3 grid((unsigned)((r.tokens * r.parts * groups_of(r) + 255) / 256));
 #define MX_ROT(IL, INV) hipLaunchKernelGGL((rotary_kernel<T, V, IL, INV>), grid, dim3(256), 0, stream, r)
   if (interleaved) { if (inverse) MX_ROT(true, true); else MX_ROT(true, false); }
   else { if (inverse) MX_ROT(false, true); else MX_ROT(false, false); }
@@ -136,25 +146,21 @@ hipError_t launch(Rotary r, bool interleaved, bool inverse, hipStream_t stream) 
 
 template <typename T>
 hipError_t launch_type(const Rotary& r, bool interleaved, bool inverse, hipStream_t stream) {
-  constexpr int V = 16 / sizeof(T);
-  const bool w = r.pairs % V == 0 && r.head_dim % V == 0 && wide(r.q, V, sizeof(T)) && wide(r.k, V, sizeof(T));
-  return w ? launch<T, V>(r, interleaved, inverse, stream) : launch<T, 1>(r, interleaved, inverse, stream);
+  return r.width > 1 ? launch<T, 16 / sizeof(T)>(r, interleaved, inverse, stream) : launch<T, 1>(r, interleaved, inverse, stream);
 }
 
 }  // namespace
 
-bool rotary_grid_fits(int64_t tokens, int64_t heads, int64_t head_dim) {
-  return heads <= kMaxWorkItems && head_dim <= kMaxWorkItems && grid_fits(tokens, heads * head_dim, 1) &&
-         tokens * heads * head_dim <= kMaxWorkItems - 255;
+bool rotary_grid_fits(const RotaryCall& c) {
+  const Rotary r = plan_of(c);
+  return grid_fits(c.tokens, (int64_t)r.parts * groups_of(r), 1) && c.tokens * r.parts * groups_of(r) <= kMaxWorkItems - 255;
 }
 
-hipError_t launch_rotary(RotaryRows q, RotaryRows k, int dtype, int64_t tokens, int64_t head_dim, int64_t pairs,
-                         const int32_t* positions, const double* turns, float magnitude, bool interleaved, bool inverse,
-                         hipStream_t stream) {
-  const Rotary r{q, k, tokens, (int32_t)head_dim, (int32_t)pairs, (int32_t)(q.heads + k.heads), 1, 0, 0, positions, turns, magnitude};
-  if (dtype == 0) return launch_type<float>(r, interleaved, inverse, stream);
-  if (dtype == 1) return launch_type<__bf16>(r, interleaved, inverse, stream);
-  return launch_type<_Float16>(r, interleaved, inverse, stream);
+hipError_t launch_rotary(const RotaryCall& c, hipStream_t stream) {
+  const Rotary r = plan_of(c);
+  if (c.dtype == 0) return launch_type<float>(r, c.interleaved, c.inverse, stream);
+  if (c.dtype == 1) return launch_type<__bf16>(r, c.interleaved, c.inverse, stream);
+  return launch_type<_Float16>(r, c.interleaved, c.inverse, stream);
 }
 
 }  // namespace mx
