@@ -20,8 +20,8 @@ class MXFP4Attention(torch.nn.Module):
     """heads queries and kv_heads keys and values of head_dim, projected from and to
     ``hidden`` features with weights in MXFP4 (``load``).  hidden and heads * head_dim
     are multiples of 128.  turns and magnitude: the frequencies of ``rotary.turns`` (None:
-    no rotary positions); interleaved, window and scale as for ``rotary.rotate`` and
-    ``kvcache.attention``."""
+    no rotary positions; 64 bits, also after a cast of the module); interleaved, window and
+    scale as for ``rotary.rotate`` and ``kvcache.attention``."""
 
     def __init__(self, hidden, heads, kv_heads, head_dim, turns=None, magnitude=1.0, interleaved=False, window=0, scale=None,
                  device=None):
@@ -41,6 +41,14 @@ class MXFP4Attention(torch.nn.Module):
         self.register_buffer("qkv_scales", torch.zeros((hidden // 128, rows), dtype=i32, device=device))
         self.register_buffer("out", torch.zeros((hidden, width // 2), dtype=u8, device=device))
         self.register_buffer("out_scales", torch.zeros((width // 128, hidden), dtype=i32, device=device))
+
+    def _apply(self, fn, recurse=True):
+        # a cast of the module (``.to(torch.bfloat16)``, ``.half()``) moves the frequencies and leaves their 64 bits
+        turns = self.turns
+        super()._apply(fn, recurse)
+        if turns is not None and self.turns.dtype != turns.dtype:
+            self.turns = turns.to(self.turns.device)
+        return self
 
     @torch.no_grad()
     def load(self, qkv, out):

@@ -1,0 +1,30 @@
+"""The attention layer's frequencies stay in 64 bits."""
+
+import pytest
+import torch
+
+from mxfp8_block_scaled_quantize_amd import rotary
+from mxfp8_block_scaled_quantize_amd.attention_layer import MXFP4Attention
+
+
+@pytest.mark.parametrize("cast", [lambda m: m.to(torch.bfloat16), lambda m: m.half(), lambda m: m.float(), lambda m: m.double(),
+                                  lambda m: torch.nn.Sequential(m).to(dtype=torch.float16)[0], lambda m: m.bfloat16().double(),
+                                  lambda m: m.to("cpu", torch.bfloat16)])
+def test_a_cast_leaves_the_frequencies(cast):
+    turns, magnitude = rotary.turns(64, scaling="yarn", factor=4.0, trained=512)
+    layer = cast(MXFP4Attention(128, 4, 2, 64, turns, magnitude))
+    assert layer.turns.dtype == torch.float64 and torch.equal(layer.turns, turns)
+    assert layer.qkv.dtype == torch.uint8 and layer.qkv_scales.dtype == torch.int32
+    assert cast(MXFP4Attention(128, 4, 2, 64)).turns is None
+
+
+def test_moves_and_copies():
+    turns = rotary.turns(64)[0]
+    layer = MXFP4Attention(128, 4, 2, 64, turns)
+    assert "turns" in layer.state_dict() and layer.state_dict()["turns"].dtype == torch.float64
+    assert layer.to("meta").turns.is_meta and layer.turns.dtype == torch.float64 and layer.qkv.is_meta
+    other = MXFP4Attention(128, 4, 2, 64, turns * 2).to(torch.bfloat16)
+    other.load_state_dict(MXFP4Attention(128, 4, 2, 64, turns).state_dict())
+    assert torch.equal(other.turns, turns)
+    shared = MXFP4Attention(128, 4, 2, 64, turns).to_empty(device="cpu")
+    assert shared.turns.shape == turns.shape and shared.turns.dtype == torch.float64
