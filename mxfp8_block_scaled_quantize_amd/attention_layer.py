@@ -60,16 +60,22 @@ class MXFP4Attention(torch.nn.Module):
             scales.copy_(q["p_row"])
         return self
 
-    @torch.no_grad()
     def forward(self, x, cache, table, plan, max_queries=None):
         """x BF16 [tokens, hidden], the rows that ``kvcache.extend`` planned (plan, with
         the cache's table) -> BF16 of the same shape; the rows' keys and values are
         written to the cache.  What a row that belongs to no request comes out as means
         nothing, nor do the rows of a request that got no slots.  max_queries as for
-        ``kvcache.attention``."""
+        ``kvcache.attention``.  There is no gradient: an x that requires one is refused
+        while gradients are enabled."""
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.hidden:
             raise ValueError("input must be a BF16 [tokens, %d] tensor" % self.hidden)
+        if x.requires_grad and torch.is_grad_enabled():
+            raise ValueError("input requires a gradient, which MXFP4Attention does not have: call it with gradients disabled")
         no_tangent("MXFP4Attention", x)
+        with torch.no_grad():
+            return self._step(x, cache, table, plan, max_queries)
+
+    def _step(self, x, cache, table, plan, max_queries):
         h, hkv = self.heads, self.kv_heads
         a = mxfp4.quantize(x.contiguous(), packed=True)
         q, k, v = mxfp4.gemm(a["q_row"], a["p_row"], self.qkv, self.qkv_scales).view(

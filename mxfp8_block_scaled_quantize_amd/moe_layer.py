@@ -62,7 +62,8 @@ class MXFP4MoE(torch.nn.Module):
 
     @torch.no_grad()
     def forward(self, x):
-        """x BF16 [.., hidden] -> BF16 of the same shape."""
+        """x BF16 [.., hidden] -> BF16 of the same shape, without a gradient (also where x
+        requires one)."""
         if x.dtype != torch.bfloat16 or x.shape[-1] != self.hidden:
             raise ValueError("input must be BF16 with %d features" % self.hidden)
         no_tangent("MXFP4MoE", x)

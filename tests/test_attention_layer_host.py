@@ -1,4 +1,4 @@
-"""The attention layer's frequencies stay in 64 bits."""
+"""The attention layer's frequencies stay in 64 bits, and a gradient that it does not have is refused."""
 
 import pytest
 import torch
@@ -28,3 +28,12 @@ def test_moves_and_copies():
     assert torch.equal(other.turns, turns)
     shared = MXFP4Attention(128, 4, 2, 64, turns).to_empty(device="cpu")
     assert shared.turns.shape == turns.shape and shared.turns.dtype == torch.float64
+
+
+def test_a_gradient_is_refused():
+    layer = MXFP4Attention(128, 4, 2, 64)
+    x = torch.zeros((3, 128), dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(ValueError, match="gradient"):
+        layer(x, None, None, None)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):     # as any input, which is on the wrong device here
+        layer(x, None, None, None)
