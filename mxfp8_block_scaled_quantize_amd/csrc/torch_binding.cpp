@@ -10,6 +10,8 @@
 #include <Python.h>
 
 #include <array>
+#include <unordered_set>
+#include <vector>
 
 #include <ATen/hip/EmptyTensor.h>
 #include <c10/core/AutogradState.h>
@@ -18,7 +20,9 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/functions/accumulate_grad.h>
 #include <torch/csrc/autograd/functions/basic_ops.h>
+#include <torch/csrc/autograd/graph_task.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "../../include/kvcache.h"
@@ -812,17 +816,35 @@ std::pair<Tensor, Tensor> rotate_both(const Tensor& q, const Tensor& k, const Tu
 // A leaf's accumulator keeps the stream on which it was made for as long as some graph
 // holds it.  If that is not the stream of a backward pass that is being captured, the
 // engine makes the two wait for each other once the pass is through, which a capture
-// does not allow: the process ends.  So the pass is refused before.
-int64_t leaf_stream(const Variable& v) {
-  const auto node = torch::autograd::impl::try_get_grad_accumulator(v);
-  const auto stream = node ? node->stream() : std::nullopt;
-  return stream ? (int64_t)stream->id() : -1;
-}
-void refuse_capture(int64_t leaf, c10::Device dev) {
-  if (leaf < 0 || c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
-  if (leaf != (int64_t)c10::hip::getCurrentHIPStream(dev.index()).unwrap().id())
-    throw std::runtime_error("rotate: its gradient cannot be captured while a graph of q or k lives that was made on another "
-                             "stream: let go of that graph, or capture on its stream");
+// does not allow: the process ends.  So a pass that leads from this operator to such a
+// leaf, directly or through other operators, is refused before.
+void refuse_capture(c10::Device dev) {
+  if (c10::hip::currentStreamCaptureStatusMayInitCtx() == c10::hip::CaptureStatus::None) return;
+  using torch::autograd::Node;
+  const auto here = torch::autograd::get_current_node();
+  if (!here) return;
+  const auto* const run = torch::autograd::get_current_graph_task_exec_info();   // empty: every node
+  const c10::StreamId now = c10::hip::getCurrentHIPStream(dev.index()).id();
+  std::unordered_set<const Node*> seen;
+  std::vector<Node*> open{here.get()};
+  while (!open.empty()) {
+    Node* const n = open.back();
+    open.pop_back();
+    for (const auto& e : n->next_edges()) {
+      Node* const next = e.function.get();
+      if (!next || !seen.insert(next).second) continue;
+      if (run && !run->empty()) {
+        const auto info = run->find(next);
+        if (info == run->end() || !info->second.should_execute()) continue;
+      }
+      open.push_back(next);
+      if (!dynamic_cast<torch::autograd::AccumulateGrad*>(next)) continue;
+      const auto stream = next->stream();
+      if (stream && stream->device_index() == dev.index() && stream->id() != now)   // (a HIP stream's device has another type)
+        throw std::runtime_error("rotate: its gradient cannot be captured while a graph of q or k, or of what they were made of, lives "
+                                 "that was made on another stream: let go of that graph, or capture on its stream");
+    }
+  }
 }
 
 struct Rotate : torch::autograd::Function<Rotate> {
@@ -831,8 +853,6 @@ struct Rotate : torch::autograd::Function<Rotate> {
     ctx->save_for_backward({positions, turns});
     ctx->saved_data["magnitude"] = magnitude;
     ctx->saved_data["flags"] = flags;
-    ctx->saved_data["q_stream"] = q.requires_grad() ? leaf_stream(q) : -1;
-    ctx->saved_data["k_stream"] = k && k->requires_grad() ? leaf_stream(*k) : -1;
     ctx->set_materialize_grads(false);
     auto [qo, ko] = rotate_both(q, k ? *k : Tensor(), {positions, turns, magnitude, (uint32_t)flags});
     if (!k) return {qo};
@@ -841,7 +861,7 @@ struct Rotate : torch::autograd::Function<Rotate> {
   static variable_list backward(AutogradContext* ctx, variable_list grads) {
     const auto saved = ctx->get_saved_variables();
     variable_list out(6);
-    for (const char* name : {"q_stream", "k_stream"}) refuse_capture(ctx->saved_data[name].toInt(), saved[0].device());
+    refuse_capture(saved[0].device());
     auto usable = [&](size_t i) {
       if (i >= grads.size() || !grads[i].defined() || !ctx->needs_input_grad(i)) return Tensor();
       at::AutoDispatchBelowADInplaceOrView below;
