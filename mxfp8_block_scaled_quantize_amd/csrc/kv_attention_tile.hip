@@ -139,12 +139,12 @@ struct ValuePart {
   __device__ __forceinline__ void mask(const Args& a, uint32_t page, int key, int lo, int end, int w) {
     const bool there = page < (uint32_t)a.pages;
     const int at = key + 16 * w;
-    if (at >= lo && at + 16 <= end && there) return;
+    if ((uint32_t)(at - lo) < (uint32_t)max(end - lo - 15, 0) && there) return;
 #pragma unroll
     for (int u = 0; u < UNITS; u++)
 #pragma unroll
       for (int j = 0; j < 4; j++)
-        if (!there || at + 4 * (int)quad(u) + j < lo || at + 4 * (int)quad(u) + j >= end) {
+        if (!there || (uint32_t)(at + 4 * (int)quad(u) + j - lo) >= (uint32_t)(end - lo)) {
           v[u][j] = 0;
           s[u] &= ~(0xFFu << (8 * j));
         }
