@@ -121,9 +121,10 @@ mxfp8_status kv_read(const uint8_t *cache, int64_t pages, int32_t page_size, int
  * Keys meet the queries in 32 bits: a query is taken apart into two E4M3 parts
  * that hold all of its bits down to 2^-21 of its largest value.  The softmax's
  * statistics and sums are fp32; a weight p_j is rounded to BF16 for the sum of the
- * values.  What a place holds that no query of a sequence sees does not matter.  A
- * value that is not finite, which kv_append does not write, at a place that some
- * queries see may reach others of the sequence, through 0 * inf.
+ * values, which holds values of up to 2^88.  What a place holds that no query of a
+ * sequence sees does not matter.  A value that is not finite, which kv_append does
+ * not write, at a place that some queries see may reach others of the sequence,
+ * through 0 * inf.
  * kv_heads >= 1, heads a multiple of it, heads / kv_heads <= 65536; tokens *
  * heads < 2^31.
  * Errors: NULL, SHAPE, MISALIGNED, WORKSPACE, LIMIT, HIP.

@@ -64,8 +64,9 @@ class MXFP4Attention(torch.nn.Module):
         """x BF16 [tokens, hidden], the rows that ``kvcache.extend`` planned (plan, with
         the cache's table) -> BF16 of the same shape; the rows' keys and values are
         written to the cache.  What a row that belongs to no request comes out as means
-        nothing, nor do the rows of a request that got no slots.  max_queries as for
-        ``kvcache.attention``.  There is no gradient: an x that requires one is refused
+        nothing, nor do the rows of a request that got no slots.  max_queries, the longest
+        run of new tokens of a request, as for ``kvcache.attention``: without it a step of
+        single tokens takes the kernel for prompts.  There is no gradient: an x that requires one is refused
         while gradients are enabled."""
         if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != self.hidden:
             raise ValueError("input must be a BF16 [tokens, %d] tensor" % self.hidden)

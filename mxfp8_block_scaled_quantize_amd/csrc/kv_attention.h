@@ -18,7 +18,18 @@
 // of half the cost of a BF16 one, and no conversion of the keys.
 //
 // Values.  O^T = V^T P^T on the BF16 matrix instructions, as a token's values have
-// scales of their own: codes and scale become BF16 (exactly).
+// scales of their own: codes and scale become BF16 (exactly).  The weights are rounded to
+// BF16 for it, by 2^-8 of themselves at most; their sums are not.  The outputs are then
+// 0.0023 of their norm off, of which their own rounding is 0.0017.  A second product, with
+// what the rounding left of the weights, would bring 0.0017 and cost 6 % of the time with few
+// rows (64 sequences of up to 8192 tokens: 71 us, not 66.5), 17 to 39 % with many (500
+// queries over 49152 keys: 524 us, not 380).
+//
+// Maximum.  The running maximum follows the scores only when one passes it by more than 8
+// (in log2), so that most steps rescale nothing.  Weights are then up to 2^8 and rounded in
+// the same relation, but the weight of a row's largest score need not be 1, which BF16 holds
+// exactly: an output that one key dominates carries that rounding too.  Sums overflow 2^8
+// earlier; those of 2^31 keys hold values up to 2^88.
 #pragma once
 
 #include "kv.h"

@@ -15,7 +15,8 @@
 // 5.4 TB/s (a plain sum over as many bytes reaches 6.3; this kernel's loads alone take 64);
 // one of 131071, 143 MB in 26 us, and 4 for the join.  Two steps of a wave are on their
 // way, with 4 waves a SIMD: three steps, or fewer waves, were slower.  Of the chip's time the
-// matrix cores work 12 %, the vector unit 30.
+// matrix cores work 12 %, the vector unit 30; with 64 values 7 and 29 (16 sequences of 16384
+// keys, 143 MB in 39 us: a workgroup a compute unit then has half the bytes on their way).
 #include "kv_attention.h"
 
 namespace mx {
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
 #pragma unroll
         for (int j = 0; j < 4; j++) mx = fmaxf(mx, x[i][j]);
       mx = group_max(mx * a.scale2);
-      if (__any(mx > top[n] + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
+      if (__any(mx > top[n] + 8.0f)) {   // the maximum may be 8 too low: see kv_attention.h
         const float higher = fmaxf(mx, top[n]);
         const float shrink = higher > -INFINITY ? __builtin_amdgcn_exp2f(top[n] - higher) : 1.0f;
         top[n] = higher;
@@ -372,6 +373,7 @@ __global__ __launch_bounds__(64 * WAVES, D == 256 ? 3 - NB : NB == 1 ? 4 : D == 
 // three loads' latency for few.  G waves have a row (4 / G rows a workgroup), lane p part p's
 // maximum and sum (64 parts at most), every lane 2 (of 256: 4) of the outputs.  What the
 // places behind a row's parts hold is not loaded, but for the statistics, which are not taken.
+// 16000 rows of 4 parts of 128: 10 us, 39 MB; 32 rows of 32 parts: 4.4.
 template <int D, int G>
 __global__ __launch_bounds__(64 * WAVES) void kv_join_kernel(Args a) {
   constexpr int V = D == 256 ? 4 : 2, PER = 64 * V / D, AHEAD = 4;   // outputs of a lane; parts that a wave's lanes take at a time
@@ -470,9 +472,10 @@ int64_t blocks_of(const KvAttention& a, int64_t tm) { return likely_tiles(a, tm)
 // Rows of a tile: 16 or 32 for a run of queries that fits, else 128, or 64 (the kernel for
 // many queries).  64 rows leave no wave idle where a run has no more, but two waves then do
 // what four do for the values: of 256 values, where registers leave a SIMD one wave, it is
-// faster everywhere (36 rows of 16 sequences of 16384 keys: 191 us, 295 with 128 rows; 64 of
-// 2048: 101 and 166), else where the keys give four workgroups a compute unit (of 128 values:
-// 94 and 114 us, 61 and 60; one sequence of 65536 keys, 512 workgroups: 46 and 42).
+// faster everywhere (36 rows of 16 sequences of 16384 keys: 201 us, 318 with 128 rows; 64 of
+// 2048: 104 and 166; one of 65536: 64 and 97), else where the keys give four workgroups a
+// compute unit (of 128 values: 96 and 118, 56 and 61; one sequence, 512 workgroups: 43 and 40;
+// of 64: 72 and 96, 52 and 50, 37 and 33).
 constexpr int64_t FILL_64 = 1024;
 int64_t rows_of(const KvAttention& a) {
   const int64_t rows = a.max_queries < 65536 ? a.max_queries * group_of(a) : 65536;
@@ -485,10 +488,10 @@ int64_t rows_of(const KvAttention& a) {
 // Of a tile's keys: the parts that give every compute unit a workgroup (of the kernel for
 // many queries as many as it holds), and the places that the table's width may want for them,
 // as far as their sums and the grid have room.  How many a tile really has is settled on the
-// device (part_steps).  One token of a sequence of 131071 keys, 8 heads: 29.6 us with 32
-// parts, 30.0 with 64, 44.5 with 16; of 2048 keys: 10.1 with 4, 13.4 with 1; 64 sequences of
-// up to 8192: 68.0 us with 1 part, 68.5 with 2, 69.5 with 4; 500 queries over 49152 keys: 356
-// with 4, 434 with 3, 364 with 8.
+// device (part_steps).  One token of a sequence of 131071 keys, 8 heads: 30 us with 32 parts,
+// 29 with 64, 46 with 16; of 2048 keys: 11.4 with 4, 14.0 with 1; 64 sequences of up to 8192:
+// 66 us with 1 part, 70 with 2 and with 4; 500 queries over 49152 keys: 379 with 4, 447 with 3,
+// 384 with 8.
 struct Parts {
   int64_t fill, places;
 };

@@ -20,12 +20,14 @@
 // why lane bit 3 is the half.  No conflicts are counted (with the chunks placed by k ^ e
 // in padded rows 161 cycles a wave and step, and 3 % of the time).
 //
-// What bounds it: of a step's 2100 cycles a wave (500 queries over 49152 keys, 32 heads, 2
-// waves a SIMD at 2.0 GHz) the matrix cores work 960 and the vector unit 1000, of which
-// the exponentials are a quarter, and the two overlap little.  Tried and slower: 3 waves a
-// SIMD with 32 keys a softmax (470 us against 432), 8 waves that share the values (511),
-// 64 rows a wave (600), wave priorities (442), fragments read a product ahead (400
-// against 395).
+// What bounds it: of the 2160 cycles that a SIMD takes for a wave's step (500 queries over
+// 49152 keys, 32 heads of 128, 2 waves a SIMD at 2.0 GHz) the matrix cores work 1025 and the
+// vector unit 1050, of which the exponentials are a quarter, and the two overlap little.  With
+// 64 values the vector unit works 70 % of the time and the matrix cores 31; with 256, one wave
+// a SIMD, 35 and 27, as nothing stands beside a wave's waiting (prompts of up to 4096
+// queries).  Tried and slower: 3 waves a SIMD with 32 keys a softmax (470 us against 432),
+// 8 waves that share the values (511), 64 rows a wave (600), wave priorities (442),
+// fragments read a product ahead (400 against 395).
 #include "kv_attention.h"
 
 namespace mx {
@@ -328,7 +330,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv_attention_tile_ke
         for (int j = 0; j < 16; j++) mx = fmaxf(mx, y[i][j]);
       const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
       mx = fmaxf(__uint_as_float(both[0]), __uint_as_float(both[1])) * a.scale2;
-      if (__any(mx > top + 8.0f)) {   // a maximum that is 8 too low costs no accuracy
+      if (__any(mx > top + 8.0f)) {   // the maximum may be 8 too low: see kv_attention.h
         const float higher = fmaxf(mx, top);
         const float shrink = higher > -INFINITY ? __builtin_amdgcn_exp2f(top - higher) : 1.0f;
         top = higher;

@@ -9,7 +9,9 @@
 //
 // Bound by latency: one decoding step of 64 requests takes 4.6 us (two sums of 1024 numbers
 // with their barriers, two binary searches, a store; an empty launch is 2), 509 requests with
-// 592000 new tokens 8.6, of which 4.7 MB of lists are 1.
+// 592000 new tokens 8.6, of which 4.7 MB of lists are 1.  Pages are given back by one
+// workgroup, 256 entries a round (a load, a search, a sum): 64 requests of 4 pages 3.0 us, of
+// 512 pages 117.
 #include "kv.h"
 #include "launch.h"
 #include "wave_scan.h"

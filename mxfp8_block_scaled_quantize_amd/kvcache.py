@@ -181,8 +181,9 @@ def attention(q, cache, table, lengths, offsets=None, scale=None, window=0, max_
     table does not hold are not there, also behind its last page.  heads is a multiple of
     the cache's, whose head h serves heads h * group .. + group - 1.  scale: head_dim **
     -0.5 unless given.  max_queries: the longest run of queries, where the program
-    knows it (a decoding step of several sequences is then not taken for a prompt); it
-    decides how the work is cut, not what comes out.  lse=True: (out, log of the
+    knows it (without it a decoding step of several sequences with offsets is taken for a
+    prompt, whose kernel answers single tokens more slowly); it decides how the work is
+    cut, not what comes out.  lse=True: (out, log of the
     softmax's sum fp32 [T, heads]), to join parts.  Queries without a key get zeros (and
     -inf); rows of no sequence are not written.  out: dense, apart from q and the
     cache."""
